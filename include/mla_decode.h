@@ -49,7 +49,7 @@
 extern "C" {
 #endif
 
-#define MLA_DECODE_ABI_VERSION 5
+#define MLA_DECODE_ABI_VERSION 6
 
 /* Status codes. */
 #define MLA_OK                 0
@@ -62,6 +62,9 @@ extern "C" {
 #define MLA_ERR_TIMEOUT       -7  /* device: a bounded wait inside a kernel expired */
 #define MLA_ERR_SCRATCH_LIMIT -8  /* mla_decode_noalloc: plan needs more than its fixed scratch */
 #define MLA_ERR_RANGE         -9  /* device: mla_decode_fp8 saw a q entry beyond +-65504 */
+#define MLA_ERR_NO_PAGES     -10  /* device: mla_cache_fork needs more free pages than there are */
+#define MLA_ERR_PAGE_STATE   -11  /* device: a page whose count does not allow the operation */
+#define MLA_ERR_BAD_ROW      -12  /* device: a row index outside the block table */
 
 /* Kernel variants the planner can choose (mla_decode_plan_t.kernel). */
 #define MLA_KERNEL_SIMT   1  /* CUDA-core split kernel, any 1 <= N <= 128 */
@@ -483,6 +486,161 @@ int mla_decode_v_up_proj(const mla_decode_plan_t* plan, const void* q, const voi
                          float softmax_scale, const void* w_uv, void* out, float* lse,
                          void* latent_out, void* workspace, size_t workspace_bytes,
                          void* stream);
+
+/*
+ * Expansion of cached latent rows into per-head keys and values, for the
+ * attention in its expanded form (vLLM mla_attention API docs,
+ * "Compute Friendly Approach (i.e. forward_mha)" and
+ * _compute_prefill_context: gather_cache, then the kv_b projection). Packed
+ * row t of request b, t in [cu_seqlens_k[b], cu_seqlens_k[b + 1]), is its
+ * cached token first_token[b] + t - cu_seqlens_k[b]; with the 576-wide entry
+ * e of that token, read through the block table,
+ *     kv[t, n, 0:128]   = sum_l e[l] * w_uk_t[n, 0:128, l]   (l < 512)
+ *     kv[t, n, 128:256] = sum_l e[l] * w_uv[n, l, 0:128]
+ *     k_pe[t, 0:64]     = e[512:576]
+ * Accumulation in fp32, one rounding to bf16 (nearest even). k_pe is one row
+ * for all heads; kv is the layout of a kv_b projection's output, so new
+ * tokens' keys and values may come from such a product too.
+ *
+ *   latent_cache   device, bf16 [num_blocks, 64, 576] (mla_expand_kv), or
+ *                  E4M3 codes with entry = k_scale * e4m3(code), k_scale
+ *                  finite and > 0 (mla_expand_kv_fp8: k_scale multiplies the
+ *                  fp32 sums). 16-byte aligned.
+ *   block_table    device, int32 [batch, max_blocks_per_seq].
+ *   first_token    device, int32 [batch], or NULL (all 0).
+ *   cu_seqlens_k   device, int32 [batch + 1], not decreasing, from 0 on; rows of
+ *                  kv and k_pe at cu_seqlens_k[batch] and after are left as
+ *                  they were.
+ *   total_k        rows of kv and k_pe; work is sized by it, so it should be
+ *                  cu_seqlens_k[batch] or little more.
+ *   w_uk_t, w_uv   device, bf16 [N, 128, 512] and [N, 512, 128], 16-byte
+ *                  aligned: the weights of mla_q_absorb_concat_cache and
+ *                  mla_v_up_proj.
+ *   kv             device, bf16 [total_k, N, 256], 32-byte aligned, written.
+ *   k_pe           device, bf16 [total_k, 64], 16-byte aligned, written.
+ *   workspace      a status header (>= 8192 bytes, 256-byte aligned).
+ * 1 <= num_heads <= 128. A token past the block table (MLA_ERR_BAD_SEQ_LEN)
+ * or on a page outside the cache (MLA_ERR_BAD_BLOCK_ID) is recorded and its
+ * rows are zeros. One launch on `stream`, no synchronisation.
+ */
+int mla_expand_kv(const void* latent_cache, int64_t num_blocks, const int32_t* block_table,
+                  int max_blocks_per_seq, const int32_t* first_token,
+                  const int32_t* cu_seqlens_k, int batch, int total_k, int num_heads,
+                  const void* w_uk_t, const void* w_uv, void* kv, void* k_pe, void* workspace,
+                  size_t workspace_bytes, void* stream);
+int mla_expand_kv_fp8(const void* latent_cache_fp8, float k_scale, int64_t num_blocks,
+                      const int32_t* block_table, int max_blocks_per_seq,
+                      const int32_t* first_token, const int32_t* cu_seqlens_k, int batch,
+                      int total_k, int num_heads, const void* w_uk_t, const void* w_uv, void* kv,
+                      void* k_pe, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Page bookkeeping of the latent cache: requests that share pages.
+ *
+ * State: `ref_counts` int32 [num_blocks], one count per page: how many
+ * block-table entries name it (0 = free, never negative), and the block
+ * tables. There is no free list: the free pages are those with count 0 and
+ * are always given out in ascending order, so the results follow from the
+ * arguments alone. A page table that several requests share is read by the
+ * decode as it is; only pages that one request alone holds may be written
+ * (mla_cache_fork gives each child a page of its own for the rows after the
+ * shared whole pages).
+ *
+ * Common arguments.
+ *   latent_cache        device, [num_layers, num_blocks, 64, 576] entries of
+ *                       entry_bytes bytes (2: bf16, 1: fp8), 16-byte aligned:
+ *                       the caches of all layers that one block table
+ *                       addresses, layer l at l * layer_stride_bytes (a
+ *                       multiple of 16, >= one layer's bytes; unused with one
+ *                       layer).
+ *   num_blocks          1 .. 8388606 (more: MLA_ERR_UNSUPPORTED).
+ *   ref_counts,         device, int32 [num_blocks]; the counts before and
+ *   ref_counts_out      after: the same array (in place) or disjoint ones.
+ *   block_table         device, int32 [rows, max_blocks_per_seq].
+ *   workspace           device, 256-byte aligned, initialised once with
+ *                       mla_workspace_init; >= mla_cache_workspace_bytes
+ *                       bytes (mla_cache_free: a status header of 8192 bytes
+ *                       is enough). Calls that share one must not overlap.
+ * Device-detected errors go to its status word (mla_read_error). Each call is
+ * two or three launches on `stream`, no synchronisation, and can be captured.
+ *
+ * mla_cache_workspace_bytes -- host only; 0 for arguments out of range.
+ */
+size_t mla_cache_workspace_bytes(int64_t num_blocks, int children);
+
+/*
+ * mla_cache_fork -- make `children` requests that start from cached ones.
+ * Child c takes over the first S = shared_lens[c] tokens of row parents[c]
+ * and gets pages for L = child_lens[c] >= S tokens:
+ *   - the S / 64 whole pages are shared (their counts + 1);
+ *   - the S % 64 tokens after them are copied, in every layer, into a page of
+ *     its own (its other rows are left as they were);
+ *   - pages up to ceil(L / 64) are fresh.
+ * Fresh pages (the copied-into ones too) are the lowest free ones in order of
+ * child, then position; their counts become 1. parents[c] < 0 with S = 0
+ * makes a request from nothing. A request grows when its length is a multiple
+ * of 64: fork it with S = its length and more room, then free its old row.
+ *
+ *   parents, shared_lens, child_lens   device, int32 [children];
+ *                  children <= 8192 (more: MLA_ERR_UNSUPPORTED).
+ *   child_table    device, int32 [children, max_blocks_per_seq]: entries
+ *                  0 .. ceil(L / 64) - 1 of row c are written, the others left
+ *                  as they were. Must not overlap block_table.
+ * All or nothing: with too few free pages (MLA_ERR_NO_PAGES, detail: how many
+ * are missing), a length outside 0 <= S <= L <= 64 * max_blocks_per_seq
+ * (MLA_ERR_BAD_SEQ_LEN), a parent row outside the table (MLA_ERR_BAD_ROW), a
+ * page id outside the cache (MLA_ERR_BAD_BLOCK_ID) or a shared page whose
+ * count is 0 (MLA_ERR_PAGE_STATE), the error is recorded, ref_counts_out gets
+ * ref_counts, and no child and no page is written.
+ */
+int mla_cache_fork(void* latent_cache, int num_layers, int64_t layer_stride_bytes,
+                   int64_t num_blocks, int entry_bytes, const int32_t* ref_counts,
+                   int32_t* ref_counts_out, const int32_t* block_table, int rows,
+                   int max_blocks_per_seq, const int32_t* parents, const int32_t* shared_lens,
+                   const int32_t* child_lens, int children, int32_t* child_table,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mla_cache_free -- the requests in rows free_rows[0..count) end: the count of
+ * every page in the first ceil(seq_lens[row] / 64) entries of each goes down
+ * by one. The tables and the pages are not written.
+ *
+ *   seq_lens    device, int32 [rows].
+ *   free_rows   device, int32 [count]; a row named twice is freed twice.
+ *   num_freed   device, int32 [1]: how many pages became free.
+ * A bad row, length or page id is recorded (MLA_ERR_BAD_ROW, _BAD_SEQ_LEN,
+ * _BAD_BLOCK_ID) and skipped; a page named more often than its count allows
+ * is recorded (MLA_ERR_PAGE_STATE) and its count ends at 0.
+ */
+int mla_cache_free(const int32_t* ref_counts, int32_t* ref_counts_out, int64_t num_blocks,
+                   const int32_t* block_table, int rows, int max_blocks_per_seq,
+                   const int32_t* seq_lens, const int32_t* free_rows, int count,
+                   int32_t* num_freed, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mla_cache_compact -- move the M live pages (count > 0) into ids 0..M-1 with
+ * the fewest copies: the k-th live page with id >= M goes to the k-th free id
+ * below M, in every layer; the other live pages stay. Counts, block table and
+ * page map follow.
+ *
+ *   block_table_out  device, int32 [rows, max_blocks_per_seq]: the first
+ *                    ceil(seq_lens[row] / 64) entries of each row are
+ *                    written, the others left as they were. block_table
+ *                    itself or disjoint from it.
+ *   page_map         device, int32 [num_blocks], or NULL: a live page's new
+ *                    id, -1 for a free page (for tables kept elsewhere).
+ *   num_live         device, int32 [1], or NULL: M.
+ * A bad length is recorded and its row left as it was; an entry that names
+ * no page of the cache (MLA_ERR_BAD_BLOCK_ID) or, as far as the call sees, a
+ * free one (MLA_ERR_PAGE_STATE) is recorded and passed on unchanged. The
+ * pages at M and above keep their old contents.
+ */
+int mla_cache_compact(void* latent_cache, int num_layers, int64_t layer_stride_bytes,
+                      int64_t num_blocks, int entry_bytes, const int32_t* ref_counts,
+                      int32_t* ref_counts_out, const int32_t* block_table,
+                      int32_t* block_table_out, int rows, int max_blocks_per_seq,
+                      const int32_t* seq_lens, int32_t* page_map, int32_t* num_live,
+                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * mla_read_error -- synchronise `stream`, then read and clear the device

@@ -23,6 +23,9 @@ MLA_ERR_BAD_SEQ_LEN = -6
 MLA_ERR_TIMEOUT = -7
 MLA_ERR_SCRATCH_LIMIT = -8
 MLA_ERR_RANGE = -9
+MLA_ERR_NO_PAGES = -10
+MLA_ERR_PAGE_STATE = -11
+MLA_ERR_BAD_ROW = -12
 
 MLA_KERNEL_SIMT = 1
 MLA_KERNEL_TC = 2
@@ -45,6 +48,8 @@ EXPORTED_SYMBOLS = (
     "mla_q_absorb_concat_cache", "mla_v_up_proj", "mla_multi_token_scratch_bytes",
     "mla_decode_multi_token", "mla_debug_loader_pages", "mla_multi_token_row_lens",
     "mla_decode_fp8", "mla_merge_splits_v_up_proj", "mla_decode_v_up_proj",
+    "mla_expand_kv", "mla_expand_kv_fp8", "mla_cache_workspace_bytes", "mla_cache_fork",
+    "mla_cache_free", "mla_cache_compact",
 )
 
 
@@ -123,10 +128,21 @@ def load_library(path=None):
     lib.mla_multi_token_row_lens.argtypes = [vp, i32, i32, i32, vp]
     lib.mla_decode_multi_token.argtypes = [ctypes.POINTER(MlaDecodePlan), i32, i32, i32, vp, vp,
                                            i64, vp, vp, f32, vp, vp, vp, sz, vp, sz, vp]
+    lib.mla_expand_kv.argtypes = [vp, i64, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, sz,
+                                  vp]
+    lib.mla_expand_kv_fp8.argtypes = [vp, f32, i64, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp,
+                                      vp, sz, vp]
+    lib.mla_cache_workspace_bytes.argtypes = [i64, i32]
+    lib.mla_cache_fork.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp, i32, i32, vp, vp, vp, i32,
+                                   vp, vp, sz, vp]
+    lib.mla_cache_free.argtypes = [vp, vp, i64, vp, i32, i32, vp, vp, i32, vp, vp, sz, vp]
+    lib.mla_cache_compact.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp, vp, i32, i32, vp, vp, vp,
+                                      vp, sz, vp]
     for name in EXPORTED_SYMBOLS:
-        if name not in ("mla_status_string", "mla_multi_token_scratch_bytes"):
+        if name != "mla_status_string":
             getattr(lib, name).restype = ctypes.c_int
     lib.mla_multi_token_scratch_bytes.restype = ctypes.c_size_t
+    lib.mla_cache_workspace_bytes.restype = ctypes.c_size_t
     if path == LIB_PATH:
         _LIB = lib
     return lib
@@ -499,6 +515,234 @@ def mla_v_up_proj(x, w_uv, *, workspace, out=None, stream=None):
                                       workspace.numel(), _stream_ptr(stream))
     _check(rc, "mla_v_up_proj")
     return out
+
+
+def _on(device, stream):
+    """The torch stream a call runs on: `stream`, else the device's current one."""
+    import torch
+    return stream if stream is not None else torch.cuda.current_stream(device)
+
+
+def _empty(shape, dtype, device, stream, fill=None):
+    """A new tensor that belongs to the stream the call runs on."""
+    import torch
+    make = torch.empty if fill is None else (lambda *a, **k: torch.full(*a, fill, **k))
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _check_tensors(device, *args):
+    """Each (name, tensor, dtype, shape or None) is a contiguous tensor of
+    that type and shape on `device`."""
+    for name, t, dtype, shape in args:
+        _check_tensor(t, name, dtype, shape)
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _call(device, stream, name, *args):
+    """Call a library function with `device` current; raises on a status."""
+    import torch
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, _on(device, stream).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _on(device, stream).cuda_stream)
+    _check(rc, name)
+
+
+def _expand_kv(name, cache_dtype, latent_cache, block_table, cu_seqlens_k, w_uk_t, w_uv, k_scale,
+               total_k, first_token, kv, k_pe, workspace, stream):
+    import torch
+    dev = latent_cache.device
+    _check_tensors(dev, ("latent_cache", latent_cache, cache_dtype, None),
+                   ("block_table", block_table, torch.int32, None),
+                   ("cu_seqlens_k", cu_seqlens_k, torch.int32, None),
+                   ("w_uk_t", w_uk_t, torch.bfloat16, None), ("w_uv", w_uv, torch.bfloat16, None),
+                   ("workspace", workspace, torch.uint8, None))
+    if latent_cache.dim() != 3 or latent_cache.shape[1:] != (PAGE_SIZE, HEAD_DIM):
+        raise ValueError("latent_cache must be [num_blocks, 64, 576]")
+    if cu_seqlens_k.dim() != 1 or cu_seqlens_k.shape[0] < 1:
+        raise ValueError("cu_seqlens_k must be [B + 1]")
+    B = cu_seqlens_k.shape[0] - 1
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks_per_seq]")
+    N = w_uk_t.shape[0]
+    if tuple(w_uk_t.shape) != (N, 128, 512) or tuple(w_uv.shape) != (N, 512, 128):
+        raise ValueError("w_uk_t must be [N, 128, 512] and w_uv [N, 512, 128]")
+    if first_token is not None:
+        _check_tensors(dev, ("first_token", first_token, torch.int32, (B,)))
+    T = int(total_k)
+    if T < 0:
+        raise ValueError("total_k must not be negative")
+    if kv is None:
+        kv = _empty((T, N, 256), torch.bfloat16, dev, stream)
+    if k_pe is None:
+        k_pe = _empty((T, ROPE_DIM), torch.bfloat16, dev, stream)
+    _check_tensors(dev, ("kv", kv, torch.bfloat16, (T, N, 256)),
+                   ("k_pe", k_pe, torch.bfloat16, (T, ROPE_DIM)))
+    scale = () if k_scale is None else (float(k_scale),)
+    _call(dev, stream, name, latent_cache.data_ptr(), *scale, latent_cache.shape[0],
+          block_table.data_ptr(), block_table.shape[1],
+          first_token.data_ptr() if first_token is not None else None, cu_seqlens_k.data_ptr(), B,
+          T, N, w_uk_t.data_ptr(), w_uv.data_ptr(), kv.data_ptr(), k_pe.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return kv, k_pe
+
+
+def mla_expand_kv(latent_cache, block_table, cu_seqlens_k, w_uk_t, w_uv, *, total_k, workspace,
+                  first_token=None, kv=None, k_pe=None, stream=None):
+    """Per-head keys and values of cached tokens: packed row t of request b is
+    its token ``first_token[b] + t - cu_seqlens_k[b]``. Returns ``(kv bf16
+    [total_k, N, 256] = [k_nope | v], k_pe bf16 [total_k, 64])``; rows from
+    ``cu_seqlens_k[B]`` on are not written."""
+    import torch
+    return _expand_kv("mla_expand_kv", torch.bfloat16, latent_cache, block_table, cu_seqlens_k,
+                      w_uk_t, w_uv, None, total_k, first_token, kv, k_pe, workspace, stream)
+
+
+def mla_expand_kv_fp8(latent_cache_fp8, block_table, cu_seqlens_k, w_uk_t, w_uv, k_scale, *,
+                      total_k, workspace, first_token=None, kv=None, k_pe=None, stream=None):
+    """``mla_expand_kv`` over an fp8 cache (uint8 E4M3 codes, per-tensor ``k_scale``)."""
+    import torch
+    return _expand_kv("mla_expand_kv_fp8", torch.uint8, latent_cache_fp8, block_table,
+                      cu_seqlens_k, w_uk_t, w_uv, k_scale, total_k, first_token, kv, k_pe,
+                      workspace, stream)
+
+
+def new_cache_workspace(num_blocks, children=0, device=None, stream=None):
+    """A workspace for mla_cache_fork (of up to `children`), _free and _compact."""
+    nbytes = int(load_library().mla_cache_workspace_bytes(int(num_blocks), int(children)))
+    if nbytes == 0:
+        raise MlaError(MLA_ERR_UNSUPPORTED, "mla_cache_workspace_bytes")
+    import torch
+    dev = torch.device(device or "cuda")
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    ws = _empty((nbytes,), torch.uint8, dev, stream)
+    _call(dev, stream, "mla_workspace_init", ws.data_ptr(), nbytes)
+    return ws
+
+
+def _cache_view(latent_cache):
+    """(pointer, layers, layer stride in bytes, blocks, bytes per entry) of a
+    cache [num_blocks, 64, 576] or [layers, num_blocks, 64, 576], bf16 or
+    uint8; each layer contiguous, the layers any distance apart."""
+    import torch
+    t = latent_cache
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("latent_cache must be a CUDA tensor")
+    if t.dtype not in (torch.bfloat16, torch.uint8):
+        raise TypeError(f"latent_cache must be bfloat16 or uint8, got {t.dtype}")
+    if t.dim() not in (3, 4) or t.shape[-2:] != (PAGE_SIZE, HEAD_DIM):
+        raise ValueError("latent_cache must be [num_blocks, 64, 576] or [layers, num_blocks, 64, 576]")
+    one = t if t.dim() == 3 else t[0]
+    if not one.is_contiguous():
+        raise ValueError("each layer of latent_cache must be contiguous")
+    size = t.element_size()
+    return (t.data_ptr(), 1 if t.dim() == 3 else t.shape[0],
+            0 if t.dim() == 3 else t.stride(0) * size, one.shape[0], size)
+
+
+def mla_cache_fork(latent_cache, ref_counts, block_table, parents, shared_lens, child_lens, *,
+                   workspace, child_table=None, ref_counts_out=None, stream=None):
+    """Requests that start from cached ones: child c shares the whole pages of
+    the first ``shared_lens[c]`` tokens of row ``parents[c]``, gets a copy of
+    the rest of them and fresh pages up to ``child_lens[c]`` tokens. Returns
+    ``(child_table int32 [C, max_blocks], counts)``; the counts are
+    ``ref_counts`` itself unless ``ref_counts_out`` is given, and a new child
+    table's unused entries are -1. All or nothing: see the header."""
+    import torch
+    dev = ref_counts.device
+    ptr, layers, stride, blocks, size = _cache_view(latent_cache)
+    _check_tensors(dev, ("ref_counts", ref_counts, torch.int32, (blocks,)),
+                   ("block_table", block_table, torch.int32, None),
+                   ("parents", parents, torch.int32, None),
+                   ("workspace", workspace, torch.uint8, None))
+    if latent_cache.device != dev:
+        raise ValueError(f"latent_cache must be on {dev}, got {latent_cache.device}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [rows, max_blocks_per_seq]")
+    C, (rows, mb) = parents.numel(), block_table.shape
+    if child_table is None:
+        child_table = _empty((C, mb), torch.int32, dev, stream, fill=-1)
+    out = ref_counts if ref_counts_out is None else ref_counts_out
+    _check_tensors(dev, ("parents", parents, torch.int32, (C,)),
+                   ("shared_lens", shared_lens, torch.int32, (C,)),
+                   ("child_lens", child_lens, torch.int32, (C,)),
+                   ("child_table", child_table, torch.int32, (C, mb)),
+                   ("ref_counts_out", out, torch.int32, (blocks,)))
+    _call(dev, stream, "mla_cache_fork", ptr, layers, stride, blocks, size, ref_counts.data_ptr(),
+          out.data_ptr(), block_table.data_ptr(), rows, mb, parents.data_ptr(),
+          shared_lens.data_ptr(), child_lens.data_ptr(), C, child_table.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return child_table, out
+
+
+def mla_cache_free(ref_counts, block_table, seq_lens, free_rows, *, workspace, ref_counts_out=None,
+                   num_freed=None, stream=None):
+    """Take the rows ``free_rows`` (int32 [count]) off their pages' counts.
+    Returns ``(counts, num_freed int32 [1])``; the counts are ``ref_counts``
+    itself unless ``ref_counts_out`` is given."""
+    import torch
+    dev = ref_counts.device
+    _check_tensors(dev, ("ref_counts", ref_counts, torch.int32, None),
+                   ("block_table", block_table, torch.int32, None),
+                   ("free_rows", free_rows, torch.int32, None),
+                   ("workspace", workspace, torch.uint8, None))
+    if block_table.dim() != 2 or ref_counts.dim() != 1 or free_rows.dim() != 1:
+        raise ValueError("block_table must be [rows, max_blocks_per_seq], ref_counts and "
+                         "free_rows one-dimensional")
+    rows, mb = block_table.shape
+    out = ref_counts if ref_counts_out is None else ref_counts_out
+    if num_freed is None:
+        num_freed = _empty((1,), torch.int32, dev, stream)
+    _check_tensors(dev, ("seq_lens", seq_lens, torch.int32, (rows,)),
+                   ("ref_counts_out", out, torch.int32, ref_counts.shape),
+                   ("num_freed", num_freed, torch.int32, (1,)))
+    _call(dev, stream, "mla_cache_free", ref_counts.data_ptr(), out.data_ptr(),
+          ref_counts.shape[0], block_table.data_ptr(), rows, mb, seq_lens.data_ptr(),
+          free_rows.data_ptr(), free_rows.shape[0], num_freed.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
+    return out, num_freed
+
+
+def mla_cache_compact(latent_cache, ref_counts, block_table, seq_lens, *, workspace,
+                      block_table_out=None, ref_counts_out=None, page_map=None, num_live=None,
+                      stream=None):
+    """Move the M live pages into ids 0..M-1 with the fewest copies. Returns
+    ``(block table, counts, page_map int32 [num_blocks], num_live int32 [1])``;
+    table and counts are changed in place unless ``*_out`` are given."""
+    import torch
+    dev = ref_counts.device
+    ptr, layers, stride, blocks, size = _cache_view(latent_cache)
+    if latent_cache.device != dev:
+        raise ValueError(f"latent_cache must be on {dev}, got {latent_cache.device}")
+    _check_tensors(dev, ("ref_counts", ref_counts, torch.int32, (blocks,)),
+                   ("block_table", block_table, torch.int32, None),
+                   ("workspace", workspace, torch.uint8, None))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [rows, max_blocks_per_seq]")
+    rows, mb = block_table.shape
+    out = ref_counts if ref_counts_out is None else ref_counts_out
+    table = block_table if block_table_out is None else block_table_out
+    if page_map is None:
+        page_map = _empty((blocks,), torch.int32, dev, stream)
+    if num_live is None:
+        num_live = _empty((1,), torch.int32, dev, stream)
+    _check_tensors(dev, ("seq_lens", seq_lens, torch.int32, (rows,)),
+                   ("ref_counts_out", out, torch.int32, (blocks,)),
+                   ("block_table_out", table, torch.int32, (rows, mb)),
+                   ("page_map", page_map, torch.int32, (blocks,)),
+                   ("num_live", num_live, torch.int32, (1,)))
+    _call(dev, stream, "mla_cache_compact", ptr, layers, stride, blocks, size,
+          ref_counts.data_ptr(), out.data_ptr(), block_table.data_ptr(), table.data_ptr(), rows,
+          mb, seq_lens.data_ptr(), page_map.data_ptr(), num_live.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
+    return table, out, page_map, num_live
 
 
 def read_error(workspace, stream=None):

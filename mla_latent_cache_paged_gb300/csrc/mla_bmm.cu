@@ -31,14 +31,11 @@
 // TMA store, and warps 2-3 insert the new tokens' latent rows (the CTAs of
 // a batch tile share them out by head) while the MMAs run. Every wait is bounded (MLA_ERR_TIMEOUT);
 // a slot outside the cache is recorded (MLA_ERR_BAD_BLOCK_ID), not written.
-#include <cuda.h>
-#include <cuda_runtime.h>
-#include <cudaTypedefs.h>
-
 #include <cstdint>
 
 #include "mla_device.cuh"
 #include "tc_ptx.cuh"
+#include "tensor_map.cuh"
 
 namespace mla {
 namespace {
@@ -500,33 +497,6 @@ mla_bmm_kernel(const BmmParams p, const __grid_constant__ CUtensorMap tmap_a,
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == 1) ptx::tmem_dealloc(tmem, Sh::kTmemCols);
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 bmm_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
-}
-
-// Row-major bf16 [rows, cols] view, boxes of box_rows x 64 columns, 128-byte swizzle.
-bool encode_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
-    PFN_cuTensorMapEncodeTiled_v12000 encode = bmm_encoder();
-    if (encode == nullptr) return false;
-    const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {cols * 2};
-    const cuuint32_t box[2] = {64, box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int J, int KD, int STAGES, int kMode>

@@ -297,6 +297,9 @@ extern "C" const char* mla_status_string(int status) {
         case MLA_ERR_SCRATCH_LIMIT:
             return "plan needs more scratch than the 32 MiB of mla_decode_noalloc";
         case MLA_ERR_RANGE: return "q entry beyond the f16 range of the fp8-cache decode";
+        case MLA_ERR_NO_PAGES: return "not enough free pages";
+        case MLA_ERR_PAGE_STATE: return "page count does not allow the operation";
+        case MLA_ERR_BAD_ROW: return "row index outside the block table";
         default: return "unknown status";
     }
 }

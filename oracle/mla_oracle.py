@@ -448,3 +448,87 @@ def mla_decode_reference_fp8(q, cache_bits, block_table, seq_lens, softmax_scale
     ``supports_quant_query_input``)."""
     return mla_decode_reference(q, dequantize_e4m3_cache(cache_bits, k_scale), block_table,
                                 seq_lens, softmax_scale, kv_lora_rank)
+
+
+# ------------------------------------------------------- the prefill side
+
+def expand_kv(cache, block_table, first_token, lens, w_uk_t, w_uv):
+    """Per-head keys and values of ``lens[b]`` cached tokens of each request
+    from ``first_token[b]`` on, packed: ``(kv [T, N, 256], k_pe [T, 64])``."""
+    page = cache.shape[1]
+    rows = [cache[block_table[b][t // page], t % page]
+            for b in range(len(lens)) for t in range(first_token[b], first_token[b] + lens[b])]
+    e = np.array(rows, dtype=np.float64).reshape(-1, cache.shape[2])
+    c = e[:, :512]
+    k = np.einsum("tl,npl->tnp", c, w_uk_t)
+    v = np.einsum("tl,nlv->tnv", c, w_uv)
+    return np.concatenate([k, v], axis=-1), e[:, 512:]
+
+
+def prefill_attention(q, kv, k_pe, q_lens, k_lens, softmax_scale, causal):
+    """Expanded-form attention of packed sequences: query i of a sequence of
+    ``Lq`` queries and ``Lk`` keys sits at position ``Lk - Lq + i`` and, with
+    ``causal``, sees the keys up to it. Only visible keys enter any sum.
+    Returns ``(out [Tq, N, 128], lse [Tq, N])``."""
+    n = q.shape[1]
+    out = np.zeros((q.shape[0], n, 128))
+    lse = np.full((q.shape[0], n), -np.inf)
+    a = c = 0
+    for lq, lk in zip(q_lens, k_lens):
+        for i in range(lq):
+            seen = max(0, min(lk, lk - lq + i + 1)) if causal else lk
+            if seen == 0:
+                continue
+            for h in range(n):
+                s = (kv[c:c + seen, h, :128] @ q[a + i, h, :128]
+                     + k_pe[c:c + seen] @ q[a + i, h, 128:]) * softmax_scale
+                m = s.max()
+                w = np.exp(s - m)
+                lse[a + i, h] = m + np.log(w.sum())
+                out[a + i, h] = (w / w.sum()) @ kv[c:c + seen, h, 128:]
+        a, c = a + lq, c + lk
+    return out, lse
+
+
+def cache_fork(ref_counts, block_table, parents, shared_lens, child_lens, page=64):
+    """``(counts, child page lists, copies)`` of a fork that can be made;
+    copies are ``(source page, destination page, rows)``. ``None`` when there
+    are too few free pages."""
+    ref = np.array(ref_counts)
+    free = [i for i in range(len(ref)) if ref[i] == 0]
+    children, copies = [], []
+    for p, s, n in zip(parents, shared_lens, child_lens):
+        row = [int(block_table[p][j]) for j in range(s // page)]
+        while len(row) < -(-n // page):
+            if not free:
+                return None
+            row.append(free.pop(0))
+        if s % page:
+            copies.append((int(block_table[p][s // page]), row[s // page], s % page))
+        children.append(row)
+    for row in children:
+        for i in row:
+            ref[i] += 1
+    return ref, children, copies
+
+
+def cache_free(ref_counts, block_table, seq_lens, rows, page=64):
+    """``(counts, pages that became free)``."""
+    ref = np.array(ref_counts)
+    for r in rows:
+        for j in range(-(-int(seq_lens[r]) // page)):
+            ref[block_table[r][j]] -= 1
+    return ref, int(((np.asarray(ref_counts) > 0) & (ref == 0)).sum())
+
+
+def cache_compact(ref_counts):
+    """``(counts, page map, moves, live pages)``; moves are (from, to)."""
+    ref = np.array(ref_counts)
+    live = int((ref != 0).sum())
+    src = [i for i in range(live, len(ref)) if ref[i] != 0]
+    dst = [i for i in range(live) if ref[i] == 0]
+    page_map = np.where(ref != 0, np.arange(len(ref)), -1)
+    for a, b in zip(src, dst):
+        page_map[a] = b
+        ref[b], ref[a] = ref[a], 0
+    return ref, page_map, list(zip(src, dst)), live

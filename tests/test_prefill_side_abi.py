@@ -1,0 +1,145 @@
+"""Refusals of the prefill-side entry points, on the host (no GPU needed)."""
+
+import ctypes
+
+import pytest
+
+from mla_latent_cache_paged_gb300 import binding, build
+
+X = 0x10000000          # an address that a refused call never reads
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load_library()
+
+
+def _expand(lib, fp8=False, **kw):
+    a = dict(cache=X, scale=0.5, blocks=10, table=X, mb=4, first=None, cu=X, batch=2, total=100,
+             heads=16, uk=X, uv=X, kv=X, pe=X, ws=X, nbytes=8192)
+    a.update(kw)
+    tail = (a["blocks"], a["table"], a["mb"], a["first"], a["cu"], a["batch"], a["total"],
+            a["heads"], a["uk"], a["uv"], a["kv"], a["pe"], a["ws"], a["nbytes"], None)
+    if fp8:
+        return lib.mla_expand_kv_fp8(a["cache"], a["scale"], *tail)
+    return lib.mla_expand_kv(a["cache"], *tail)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(heads=129), binding.MLA_ERR_UNSUPPORTED),
+    (dict(heads=0), binding.MLA_ERR_INVALID_ARG),
+    (dict(batch=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(total=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(blocks=0), binding.MLA_ERR_INVALID_ARG),
+    (dict(mb=0), binding.MLA_ERR_INVALID_ARG),
+    (dict(cache=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(cache=X + 8), binding.MLA_ERR_INVALID_ARG),
+    (dict(kv=X + 16), binding.MLA_ERR_INVALID_ARG),
+    (dict(pe=X + 4), binding.MLA_ERR_INVALID_ARG),
+    (dict(uk=X + 2), binding.MLA_ERR_INVALID_ARG),
+    (dict(uv=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(cu=X + 2), binding.MLA_ERR_INVALID_ARG),
+    (dict(first=X + 1), binding.MLA_ERR_INVALID_ARG),
+    (dict(ws=None), binding.MLA_ERR_WORKSPACE),
+    (dict(ws=X + 128), binding.MLA_ERR_WORKSPACE),
+    (dict(nbytes=8191), binding.MLA_ERR_WORKSPACE),
+    (dict(total=0, kv=None), binding.MLA_OK),
+    (dict(batch=0, cu=None), binding.MLA_OK),
+])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_expand_refusals(lib, kw, code, fp8):
+    assert _expand(lib, fp8, **kw) == code
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("inf"), float("nan")])
+def test_expand_fp8_scale(lib, scale):
+    assert _expand(lib, True, scale=scale) == binding.MLA_ERR_INVALID_ARG
+
+
+def _fork(lib, **kw):
+    a = dict(cache=X, layers=1, stride=0, blocks=100, size=2, ref=X, out=X, table=X, rows=4, mb=8,
+             parents=X, shared=X, room=X, children=3, child=X + 4096, ws=X, nbytes=1 << 20)
+    a.update(kw)
+    return lib.mla_cache_fork(*(a[k] for k in ("cache", "layers", "stride", "blocks", "size", "ref",
+                                               "out", "table", "rows", "mb", "parents", "shared",
+                                               "room", "children", "child", "ws", "nbytes")), None)
+
+
+PAGE = 64 * 576 * 2
+COMMON = [
+    (dict(cache=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(cache=X + 8), binding.MLA_ERR_INVALID_ARG),
+    (dict(layers=0), binding.MLA_ERR_INVALID_ARG),
+    (dict(layers=2, stride=100 * PAGE - 16), binding.MLA_ERR_INVALID_ARG),
+    (dict(layers=2, stride=100 * PAGE + 8), binding.MLA_ERR_INVALID_ARG),
+    (dict(blocks=0), binding.MLA_ERR_INVALID_ARG),
+    (dict(blocks=(1 << 23) - 1), binding.MLA_ERR_UNSUPPORTED),
+    (dict(size=4), binding.MLA_ERR_UNSUPPORTED),
+    (dict(ref=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(out=X + 100), binding.MLA_ERR_INVALID_ARG),      # overlaps the counts read
+    (dict(rows=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(mb=0), binding.MLA_ERR_INVALID_ARG),
+    (dict(ws=None), binding.MLA_ERR_WORKSPACE),
+    (dict(ws=X + 64), binding.MLA_ERR_WORKSPACE),
+    (dict(nbytes=8192), binding.MLA_ERR_WORKSPACE),
+]
+
+
+@pytest.mark.parametrize("kw,code", COMMON + [
+    (dict(children=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(children=8193), binding.MLA_ERR_UNSUPPORTED),
+    (dict(parents=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(shared=X + 2), binding.MLA_ERR_INVALID_ARG),
+    (dict(child=X), binding.MLA_ERR_INVALID_ARG),          # overlaps the parents' table
+    (dict(child=X + 4 * 8 * 4 - 4), binding.MLA_ERR_INVALID_ARG),
+    (dict(child=X - 4 * 8 * 3 + 4), binding.MLA_ERR_INVALID_ARG),
+    (dict(table=None), binding.MLA_ERR_INVALID_ARG),
+])
+def test_fork_refusals(lib, kw, code):
+    assert _fork(lib, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", COMMON + [
+    (dict(table_out=X + 4), binding.MLA_ERR_INVALID_ARG),
+    (dict(lens=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(page_map=X + 1), binding.MLA_ERR_INVALID_ARG),
+    (dict(live=X + 2), binding.MLA_ERR_INVALID_ARG),
+])
+def test_compact_refusals(lib, kw, code):
+    a = dict(cache=X, layers=1, stride=0, blocks=100, size=2, ref=X, out=X, table=X, table_out=X,
+             rows=4, mb=8, lens=X, page_map=None, live=None, ws=X, nbytes=1 << 20)
+    a.update(kw)
+    rc = lib.mla_cache_compact(*(a[k] for k in ("cache", "layers", "stride", "blocks", "size", "ref",
+                                                "out", "table", "table_out", "rows", "mb", "lens",
+                                                "page_map", "live", "ws", "nbytes")), None)
+    assert rc == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(blocks=0), binding.MLA_ERR_INVALID_ARG),
+    (dict(blocks=(1 << 23) - 1), binding.MLA_ERR_UNSUPPORTED),
+    (dict(out=X + 100), binding.MLA_ERR_INVALID_ARG),
+    (dict(count=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(free_rows=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(freed=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(lens=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(ws=X + 4), binding.MLA_ERR_WORKSPACE),
+])
+def test_free_refusals(lib, kw, code):
+    a = dict(ref=X, out=X, blocks=100, table=X, rows=4, mb=8, lens=X, free_rows=X, count=2, freed=X,
+             ws=X, nbytes=8192)
+    a.update(kw)
+    rc = lib.mla_cache_free(*(a[k] for k in ("ref", "out", "blocks", "table", "rows", "mb", "lens",
+                                             "free_rows", "count", "freed", "ws", "nbytes")), None)
+    assert rc == code
+
+
+def test_cache_workspace_sizes(lib):
+    size = lib.mla_cache_workspace_bytes
+    assert size(1, 0) > 8192 and size(1, 0) % 256 == 0
+    assert size(1 << 20, 0) >= 8192 + 3 * 4 * (1 << 19)
+    assert size(100, 8192) > size(100, 0)
+    for blocks, children in [(0, 0), (-1, 0), ((1 << 23) - 1, 0), (10, -1), (10, 8193)]:
+        assert size(blocks, children) == 0
+    assert ctypes.sizeof(ctypes.c_size_t) == 8
