@@ -535,6 +535,76 @@ int mla_expand_kv_fp8(const void* latent_cache_fp8, float k_scale, int64_t num_b
                       void* k_pe, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * mla_prefill -- attention of many query tokens in the expanded form
+ * ("forward_mha" of the vLLM mla_attention API docs: flash attention of
+ * q [T, N, 192] over k = cat[k_nope, k_pe] and v, ragged batches by
+ * cu_seqlens, returning the LSE so that context chunks can be merged).
+ *
+ * Sequence b has queries [cu_seqlens_q[b], cu_seqlens_q[b+1]) and keys
+ * [cu_seqlens_k[b], cu_seqlens_k[b+1]), Lq and Lk of them. Query i sees key j
+ * if j <= Lk - Lq + i (`causal`: the last query sits at the last key's
+ * position) or always; over those keys
+ *     s   = softmax_scale * (q[i, n, 0:128] . kv[j, n, 0:128]
+ *                            + q[i, n, 128:192] . k_pe[j])
+ *     lse[i, n] = ln sum_j exp(s),  out[i, n] = sum_j exp(s - lse) kv[j, n, 128:256]
+ * A query that sees no key gets out = 0, lse = -inf. A value outside what a
+ * query sees, whatever it holds, does not reach its result. Context that does
+ * not fit in one call: attend to it chunk by chunk and combine the results
+ * with mla_dcp_combine (out and lse stacked chunk-major).
+ *
+ * A plan is plain data computed on the host: mla_prefill reads it, never
+ * changes it, and rejects one whose workspace layout does not follow from
+ * its sizes.
+ */
+typedef struct mla_prefill_plan {
+    int32_t  batch;               /* B */
+    int32_t  num_heads;           /* N */
+    int32_t  total_q;             /* rows of q, out and lse */
+    int32_t  num_kv_splits;       /* S >= 1: parts that each sequence's keys are cut into */
+    int32_t  num_sms;
+    uint32_t reserved0;
+    uint64_t workspace_bytes;
+    uint64_t partial_offset;      /* byte offset of fp32 [total_q, N, S, 128] (S > 1) */
+    uint64_t lse_partial_offset;  /* byte offset of fp32 [total_q, N, S] (S > 1) */
+    uint32_t reserved[6];
+} mla_prefill_plan_t;
+
+/*
+ * mla_prefill_plan -- choose S, size the workspace. Host only.
+ *   batch, num_heads   B >= 0, 1 <= N <= 128.
+ *   total_q            rows of q; max_q_len, max_k_len: the longest sequence's
+ *                      (they steer S alone; longer ones give the same results).
+ *   num_kv_splits      S in 1..64, or 0: the planner splits the keys when the
+ *                      query tiles alone leave SMs idle.
+ *   num_sms            SMs of the target device, >= 1.
+ */
+int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q_len, int max_k_len,
+                     int num_kv_splits, int num_sms, mla_prefill_plan_t* plan);
+
+/*
+ *   q              device, bf16 [total_q, N, 192] ([q_nope | q_pe]), 16-byte aligned.
+ *   kv             device, bf16 [total_k, N, 256] ([k_nope | v]), 16-byte aligned.
+ *   k_pe           device, bf16 [total_k, 64], one row for all heads, 16-byte aligned.
+ *   cu_seqlens_q, cu_seqlens_k   device, int32 [B + 1], not decreasing. A
+ *                  sequence with bounds outside [0, total_q] or [0, total_k]
+ *                  is recorded (MLA_ERR_BAD_SEQ_LEN): it has no rows, or no keys.
+ *   softmax_scale  finite, > 0.
+ *   out            device, bf16 [total_q, N, 128], 32-byte aligned, rounded to
+ *                  nearest even; lse: device, fp32 [total_q, N], or NULL. Rows
+ *                  that belong to no sequence are left as they were.
+ *   workspace      device, >= plan->workspace_bytes, 256-byte aligned,
+ *                  initialised once with mla_workspace_init; calls that
+ *                  share one must not overlap on the device.
+ * The softmax weights are rounded to bf16 for the tensor cores; scores, sums
+ * and accumulators are fp32. Results do not depend on timing. One launch (two
+ * with S > 1) on `stream`, no synchronisation.
+ */
+int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const void* kv, const void* k_pe,
+                int total_k, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int causal,
+                float softmax_scale, void* out, float* lse, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/*
  * Page bookkeeping of the latent cache: requests that share pages.
  *
  * State: `ref_counts` int32 [num_blocks], one count per page: how many

@@ -49,7 +49,7 @@ EXPORTED_SYMBOLS = (
     "mla_decode_multi_token", "mla_debug_loader_pages", "mla_multi_token_row_lens",
     "mla_decode_fp8", "mla_merge_splits_v_up_proj", "mla_decode_v_up_proj",
     "mla_expand_kv", "mla_expand_kv_fp8", "mla_cache_workspace_bytes", "mla_cache_fork",
-    "mla_cache_free", "mla_cache_compact",
+    "mla_cache_free", "mla_cache_compact", "mla_prefill_plan", "mla_prefill",
 )
 
 
@@ -82,6 +82,21 @@ class MlaDecodePlan(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_ if name != "reserved"}
+
+
+class MlaPrefillPlan(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("total_q", ctypes.c_int32),
+        ("num_kv_splits", ctypes.c_int32),
+        ("num_sms", ctypes.c_int32),
+        ("reserved0", ctypes.c_uint32),
+        ("workspace_bytes", ctypes.c_uint64),
+        ("partial_offset", ctypes.c_uint64),
+        ("lse_partial_offset", ctypes.c_uint64),
+        ("reserved", ctypes.c_uint32 * 6),
+    ]
 
 
 _LIB = None
@@ -138,6 +153,10 @@ def load_library(path=None):
     lib.mla_cache_free.argtypes = [vp, vp, i64, vp, i32, i32, vp, vp, i32, vp, vp, sz, vp]
     lib.mla_cache_compact.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp, vp, i32, i32, vp, vp, vp,
                                       vp, sz, vp]
+    lib.mla_prefill_plan.argtypes = [i32, i32, i32, i32, i32, i32, i32,
+                                     ctypes.POINTER(MlaPrefillPlan)]
+    lib.mla_prefill.argtypes = [ctypes.POINTER(MlaPrefillPlan), vp, vp, vp, i32, vp, vp, i32, f32,
+                                vp, vp, vp, sz, vp]
     for name in EXPORTED_SYMBOLS:
         if name != "mla_status_string":
             getattr(lib, name).restype = ctypes.c_int
@@ -611,6 +630,65 @@ def mla_expand_kv_fp8(latent_cache_fp8, block_table, cu_seqlens_k, w_uk_t, w_uv,
     return _expand_kv("mla_expand_kv_fp8", torch.uint8, latent_cache_fp8, block_table,
                       cu_seqlens_k, w_uk_t, w_uv, k_scale, total_k, first_token, kv, k_pe,
                       workspace, stream)
+
+
+def make_prefill_plan(batch, num_heads, total_q, max_q_len, max_k_len, *, num_kv_splits=0,
+                      num_sms=None):
+    """Call mla_prefill_plan (host only; no device work)."""
+    if num_sms is None:
+        import torch
+        num_sms = (torch.cuda.get_device_properties(0).multi_processor_count
+                   if torch.cuda.is_available() else 152)
+    plan = MlaPrefillPlan()
+    _check(load_library().mla_prefill_plan(int(batch), int(num_heads), int(total_q),
+                                           int(max_q_len), int(max_k_len), int(num_kv_splits),
+                                           int(num_sms), ctypes.byref(plan)), "mla_prefill_plan")
+    return plan
+
+
+def mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, softmax_scale, *, causal=True, plan=None,
+                num_kv_splits=0, out=None, lse=None, return_lse=True, workspace=None, stream=None):
+    """Expanded-form attention of packed sequences: ``q [Tq, N, 192]`` over
+    ``kv [Tk, N, 256] = [k_nope | v]`` and ``k_pe [Tk, 64]``; query i of a
+    sequence sees its keys up to ``Lk - Lq + i`` (``causal``) or all of them.
+    Returns ``(out bf16 [Tq, N, 128], lse fp32 [Tq, N] | None)``; rows past
+    ``cu_seqlens_q[B]`` are not written."""
+    import torch
+    _check_tensor(q, "q", torch.bfloat16)
+    if q.dim() != 3 or q.shape[2] != 192:
+        raise ValueError("q must be [total_q, N, 192]")
+    T, N, _ = q.shape
+    dev = q.device
+    _check_tensors(dev, ("kv", kv, torch.bfloat16, None),
+                   ("cu_seqlens_q", cu_seqlens_q, torch.int32, None))
+    if kv.dim() != 3 or tuple(kv.shape[1:]) != (N, 256):
+        raise ValueError(f"kv must be [total_k, {N}, 256]")
+    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 1:
+        raise ValueError("cu_seqlens_q must be [B + 1]")
+    B, Tk = cu_seqlens_q.shape[0] - 1, kv.shape[0]
+    if plan is None:
+        plan = make_prefill_plan(B, N, T, T, Tk, num_kv_splits=num_kv_splits)
+    elif (plan.batch, plan.num_heads, plan.total_q) != (B, N, T):
+        raise ValueError(f"the plan is for (B, N, total_q) = "
+                         f"{plan.batch, plan.num_heads, plan.total_q}, not {B, N, T}")
+    if out is None:
+        out = _empty((T, N, 128), torch.bfloat16, dev, stream)
+    if lse is None and return_lse:
+        lse = _empty((T, N), torch.float32, dev, stream)
+    if workspace is None:
+        workspace = _empty((int(plan.workspace_bytes),), torch.uint8, dev, stream)
+        _call(dev, stream, "mla_workspace_init", workspace.data_ptr(), workspace.numel())
+    _check_tensors(dev, ("k_pe", k_pe, torch.bfloat16, (Tk, ROPE_DIM)),
+                   ("cu_seqlens_k", cu_seqlens_k, torch.int32, (B + 1,)),
+                   ("out", out, torch.bfloat16, (T, N, 128)),
+                   ("workspace", workspace, torch.uint8, None))
+    if lse is not None:
+        _check_tensors(dev, ("lse", lse, torch.float32, (T, N)))
+    _call(dev, stream, "mla_prefill", ctypes.byref(plan), q.data_ptr(), kv.data_ptr(),
+          k_pe.data_ptr(), Tk, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), 1 if causal else 0,
+          float(softmax_scale), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+          workspace.data_ptr(), workspace.numel())
+    return out, lse
 
 
 def new_cache_workspace(num_blocks, children=0, device=None, stream=None):

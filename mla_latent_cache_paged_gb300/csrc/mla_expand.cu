@@ -339,12 +339,14 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
             // read the half's previous rows is done: its last accumulator was
             // waited for below.
             const RowSource src = find_row<kEntryBytes>(p, t < INT_MAX ? int(t) : INT_MAX);
+            __syncwarp();
             if (h == 0) {
 #pragma unroll 1
                 for (int g = 0; g < kLkv / 64; ++g) {
                     uint32_t w[32];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) load16<kEntryBytes>(src.entry, g * 4 + k, w + 8 * k);
+                    __syncwarp();
                     ptx::tmem_st32(tmem + kTmemA + lane_addr + uint32_t(g * 32), w);
                 }
                 ptx::tc_fence_before();

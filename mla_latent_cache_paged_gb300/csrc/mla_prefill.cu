@@ -1,0 +1,959 @@
+// Expanded-form latent attention for many query tokens (mla_prefill): ragged
+// sequences, causal or not, head dims 192 (keys: 128 of the token's own head
+// and 64 shared by all heads) and 128 (values).
+//
+//   s_ij  = scale * (q_i[0:128] . k_nope_j + q_i[128:192] . k_pe_j)
+//   lse_i = ln sum_j exp(s_ij),  out_i = sum_j exp(s_ij - lse_i) v_j
+// over the keys that query i sees: j <= Lk - Lq + i (causal) or all Lk. k_pe
+// is read where it lies, once per key tile; no per-head copy of it exists.
+//
+// A work item is 256 query rows (two tiles of 128) of one head of one
+// sequence (and one split of its keys). Persistent CTAs, one per SM, take
+// items in a fixed order. Per 128-key step and tile:
+//   S = Q K^T      tcgen05.mma 128 x 128 x 192, Q and K in shared memory
+//   P = 2^(S c - m c)   128 threads, one query row each (= TMEM lane), fp32;
+//                  P as bf16 over S in TMEM. The reference maximum m moves
+//                  only when it would grow by more than 2^8, so rescaling O
+//                  (a TMEM read-modify-write) is rare; the sum is kept in
+//                  fp32 of the unrounded weights. P's rounding to bf16 is
+//                  what the tensor cores' operand type costs.
+//   O += P V       128 x 128 x 128, P the A operand in TMEM, V in shared memory
+// The two tiles share every key and value block and run half a step apart:
+// the tensor pipe works on one while the softmax works on the other. TMEM:
+// S/P 2 x 128 columns, O 2 x 128 columns.
+//
+// Bound: the tensor pipe, 2 * 320 flops per visible (query, key, head) pair;
+// per 128-key step of a 256-row item 2,560 clocks of it, against 1,024-2,048
+// clocks of exponentials (32,768 of them) and 80 KB of loads (32 bytes per
+// clock per SM, from L2: the items of a group of heads run together, so that
+// their keys and values stay there).
+//
+// Keys and values of a 128-key step that lie past the sequence's end belong to
+// the next sequence, and those past a row's causal limit are its own future:
+// scores there are replaced by -inf, but a weight of 0 does not keep a NaN or
+// infinity of V out of the product. So, in the steps where some row's limit
+// falls, a helper warp clears V's rows past the end and replaces non-finite
+// values by 0 before the tensor pipe reads them; if it replaced any, the
+// epilogue adds them to the rows that do see them.
+//
+// Warps: 0-3 and 4-7 = softmax and epilogue of the tiles, 8 = loads (TMA), 9 =
+// MMAs, 10 = helper, 11 = item scheduler. Every wait is bounded
+// (MLA_ERR_TIMEOUT).
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "mla_device.cuh"
+#include "tc_ptx.cuh"
+#include "tensor_map.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTileRows = 128;
+constexpr int kItemRows = 2 * kTileRows;
+constexpr int kStep = 128;                    // keys per step
+constexpr int kQk = 192, kV = 128, kKvHead = 256;
+constexpr int kBlock = 16384;                 // 128 x 64 (Q, K) or 64 x 128 (V) bf16
+constexpr int kQBlocks = 3;                   // per tile
+constexpr int kRing = 8;                      // blocks: K of a step takes 3, V takes 2
+constexpr int kOffRing = 2 * kQBlocks * kBlock;
+constexpr int kOffBar = kOffRing + kRing * kBlock;
+constexpr int kItemSlots = 4;
+constexpr int kSmemBytes = kOffBar + 1024;    // base is 1 KB aligned
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+constexpr uint32_t kTmemS = 0;                // 2 x 128 columns; P overwrites the first 64 of each
+constexpr uint32_t kTmemO = 256;              // 2 x 128 columns
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kRescaleThreshold = 8.0f;     // log2 units
+constexpr uint64_t kTimeoutNs = 1000000000ull;
+constexpr uint32_t kSuspendNs = 20000;
+constexpr int kMaxSplits = 64;
+// Keys and values of the heads that run together (a third of the L2).
+constexpr int64_t kGroupBytes = int64_t(40) << 20;
+
+enum PrefillSite : int32_t { kSiteItem = 70, kSiteItemFree, kSiteQ, kSiteQFree, kSiteRing,
+                             kSiteRingFree, kSiteS, kSiteP, kSitePv, kSiteRaw, kSiteDrain };
+
+struct Item {
+    int32_t head;         // -1: no more items
+    int32_t split;
+    int32_t q_row;        // packed row of the item's first query
+    int32_t q_rows;       // its queries (1..256)
+    int32_t k_row;        // packed row of the sequence's first key
+    int32_t lk;           // the sequence's keys
+    int32_t limit0;       // last key that the item's first query sees (causal: row i sees limit0 + i)
+    int32_t step_lo;      // steps of this split, per tile [step_lo, step_hi[t])
+    int32_t step_hi[2];
+    int32_t fix_from;     // first step whose values need the helper
+    int32_t pad;
+};
+
+struct Bars {
+    uint64_t ring_full[kRing], ring_empty[kRing];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2];       // scores of the step complete
+    uint64_t p_ready[2];      // 128 arrivals: weights in TMEM, O rescaled
+    uint64_t pv_done[2];      // P.V of the step complete
+    // A step whose values the helper works on: its V blocks land here (steps
+    // alternate), and the helper completes their ring_full.
+    uint64_t raw_full[2];
+    uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+    uint64_t drain;
+    Item items[kItemSlots];
+    int32_t bad_item[kItemSlots];   // sequence number of an item with replaced values
+    uint32_t tmem_base;
+    int32_t abort;
+};
+static_assert(sizeof(Bars) <= 1024, "barrier block");
+constexpr int kItemConsumers = 8 + 3;   // softmax warps, loads, MMAs, helper
+
+struct PrefillParams {
+    const uint16_t* kv;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    int batch, heads, total_q, total_k;
+    int causal;
+    int splits;
+    int group;                // heads that run together
+    float scale_log2;
+    uint16_t* out;            // bf16 [total_q, N, 128]
+    float* lse;               // fp32 [total_q, N] or null
+    float* o_part;            // splits > 1: fp32 [total_q, N, S, 128]
+    float* lse_part;          //             fp32 [total_q, N, S]
+    int32_t* status;
+};
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Bars* bars, int32_t* status,
+                                     int32_t site, bool ignore_abort = false) {
+    if (ptx::mbar_test_wait(bar, parity)) return true;
+    volatile int32_t* abort = &bars->abort;
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+        for (int i = 0; i < 4; ++i)
+            if (ptx::mbar_try_wait_sleep(bar, parity, kSuspendNs)) return true;
+        if (!ignore_abort && *abort != 0) return false;
+        if (ptx::globaltimer() - t0 > kTimeoutNs) {
+            *abort = 1;
+            record_error(status, MLA_ERR_TIMEOUT, site);
+            return false;
+        }
+    }
+}
+
+// 32 lanes x 128 columns.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+    uint32_t lo[64], hi[64];
+    ptx::tmem_ld64(taddr, lo);
+    ptx::tmem_ld64(taddr + 64, hi);
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+        v[i] = __uint_as_float(lo[i]);
+        v[64 + i] = __uint_as_float(hi[i]);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// Rows and keys of sequence b; one whose bounds make no sense has none.
+__device__ __forceinline__ void sequence(const PrefillParams& p, int b, int* q0, int* lq, int* k0,
+                                         int* lk) {
+    const int qa = p.cu_q[b], qe = p.cu_q[b + 1], ka = p.cu_k[b], ke = p.cu_k[b + 1];
+    *q0 = qa;
+    *k0 = ka;
+    *lq = *lk = 0;
+    if (qa < 0 || qe < qa || qe > p.total_q) {
+        record_error(p.status, MLA_ERR_BAD_SEQ_LEN, qe);
+        return;
+    }
+    *lq = qe - qa;
+    if (ka < 0 || ke < ka || ke > p.total_k) {
+        record_error(p.status, MLA_ERR_BAD_SEQ_LEN, ke);
+        return;
+    }
+    *lk = ke - ka;
+}
+
+__device__ __forceinline__ int item_tiles(int lq) { return lq / kItemRows + (lq % kItemRows != 0); }
+
+// Everything an item's roles need, from its place in the order: heads in
+// groups, in a group the row tiles from the last to the first (a causal
+// sequence's last rows see the most keys, and the longest items go first),
+// then heads, then splits. The whole warp works on it.
+__device__ __forceinline__ Item find_item(const PrefillParams& p, int64_t index, int64_t tiles) {
+    const int lane = threadIdx.x & 31;
+    const int64_t per_group = tiles * p.group * p.splits;
+    const int g = int(index / per_group);
+    const int64_t rem = index - g * per_group;
+    const int heads = min(p.group, p.heads - g * p.group);
+    const int per_tile = heads * p.splits;
+    int64_t tile = tiles - 1 - rem / per_tile;
+    const int rest = int(rem % per_tile);
+    Item it;
+    it.head = g * p.group + rest / p.splits;
+    it.split = rest % p.splits;
+    // The sequence that holds this tile.
+    int q0 = 0, lq = 0, k0 = 0, lk = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        int n = 0;
+        if (b0 + lane < p.batch) {
+            sequence(p, b0 + lane, &q0, &lq, &k0, &lk);
+            n = item_tiles(lq);
+        }
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        const int all = __shfl_sync(0xffffffffu, inc, 31);
+        if (tile < all) {
+            const int src = __ffs(__ballot_sync(0xffffffffu, inc > tile)) - 1;
+            const int before = __shfl_sync(0xffffffffu, inc - n, src);
+            tile -= before;
+            q0 = __shfl_sync(0xffffffffu, q0, src);
+            lq = __shfl_sync(0xffffffffu, lq, src);
+            k0 = __shfl_sync(0xffffffffu, k0, src);
+            lk = __shfl_sync(0xffffffffu, lk, src);
+            break;
+        }
+        tile -= all;
+    }
+    const int first = int(tile) * kItemRows;
+    it.q_row = q0 + first;
+    it.q_rows = min(kItemRows, lq - first);
+    it.k_row = k0;
+    it.lk = lk;
+    it.limit0 = p.causal ? lk - lq + first : lk - 1;
+    // Keys that the last row of each tile sees, then this split's steps.
+    int steps[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int rows = min(kTileRows, it.q_rows - t * kTileRows);
+        int keys = 0;
+        if (rows > 0) {
+            keys = p.causal ? it.limit0 + t * kTileRows + rows : lk;
+            keys = max(0, min(keys, lk));
+        }
+        steps[t] = keys / kStep + (keys % kStep != 0);
+    }
+    const int most = max(steps[0], steps[1]);
+    const int chunk = (most + p.splits - 1) / p.splits;
+    it.step_lo = min(most, it.split * chunk);
+    const int hi = min(most, it.step_lo + chunk);
+    it.step_hi[0] = max(it.step_lo, min(hi, steps[0]));
+    it.step_hi[1] = max(it.step_lo, min(hi, steps[1]));
+    // Steps before this one lie wholly within every row's limit.
+    const int whole = p.causal ? max(0, min(it.limit0 + 1, lk)) : lk;
+    it.fix_from = max(it.step_lo, whole / kStep);
+    it.pad = 0;
+    return it;
+}
+
+// The item consumers' side of the item ring.
+struct ItemReader {
+    uint32_t full, empty;
+    uint32_t n = 0;
+    __device__ __forceinline__ bool next(Bars* bars, int32_t* status, Item* out) {
+        const uint32_t s = n % kItemSlots;
+        if (!wait(full + 8 * s, (n / kItemSlots) & 1, bars, status, kSiteItem)) return false;
+        *out = bars->items[s];
+        return true;
+    }
+    __device__ __forceinline__ void release() {
+        ptx::mbar_arrive(empty + 8 * (n % kItemSlots));
+        ++n;
+    }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap map_q,
+                   const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ CUtensorMap map_pe) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t sbase = ptx::smem_addr(smem);
+    Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
+    const uint32_t b0 = sbase + kOffBar;
+#define MLA_BAR(field) (b0 + uint32_t(offsetof(Bars, field)))
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if ((sbase & 1023u) != 0) {   // the swizzled tiles need it
+        if (threadIdx.x == 0) record_error(p.status, MLA_ERR_UNSUPPORTED, 0);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRing; ++s) {
+            ptx::mbar_init(MLA_BAR(ring_full) + 8 * s, 1);
+            ptx::mbar_init(MLA_BAR(ring_empty) + 8 * s, 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(MLA_BAR(q_full) + 8 * t, 1);
+            ptx::mbar_init(MLA_BAR(q_empty) + 8 * t, 1);
+            ptx::mbar_init(MLA_BAR(s_full) + 8 * t, 1);
+            ptx::mbar_init(MLA_BAR(p_ready) + 8 * t, 128);
+            ptx::mbar_init(MLA_BAR(pv_done) + 8 * t, 1);
+        }
+        for (int t = 0; t < 2; ++t) ptx::mbar_init(MLA_BAR(raw_full) + 8 * t, 1);
+        for (int s = 0; s < kItemSlots; ++s) {
+            ptx::mbar_init(MLA_BAR(item_full) + 8 * s, 1);
+            ptx::mbar_init(MLA_BAR(item_empty) + 8 * s, kItemConsumers);
+            bars->bad_item[s] = -1;
+        }
+        ptx::mbar_init(MLA_BAR(drain), 1);
+        bars->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) {
+        ptx::tmem_alloc(ptx::smem_addr(&bars->tmem_base), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    ItemReader items{MLA_BAR(item_full), MLA_BAR(item_empty)};
+    Item it;
+
+    // Registers: 384 threads x 168 at launch = 64,512; the softmax warps take
+    // 208 (a row's 128 scores stay in registers), the others 88:
+    // 256 x 208 + 128 x 88 = 64,512.
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8) {
+            // ------------------------------------------------------- loads
+            if (ptx::elect_one()) {
+                uint32_t blocks = 0, q_loads[2] = {0, 0}, raws = 0, raw_slots = 0;
+                bool ok = true;
+                // The next ring slot, once it is free; its load completes on
+                // ring_full, or on `raw` for the helper.
+                auto slot = [&](uint32_t raw, uint32_t* addr, uint32_t* bar) {
+                    const uint32_t s = blocks % kRing, turn = blocks / kRing;
+                    if (turn > 0 &&
+                        !wait(MLA_BAR(ring_empty) + 8 * s, (turn - 1) & 1, bars, p.status,
+                              kSiteRingFree))
+                        return false;
+                    *addr = sbase + uint32_t(kOffRing) + s * kBlock;
+                    *bar = raw != 0 ? raw : MLA_BAR(ring_full) + 8 * s;
+                    if (raw == 0) ptx::mbar_arrive_expect_tx(*bar, kBlock);
+                    raw_slots = (raw_slots & ~(1u << s)) | (raw != 0 ? 1u << s : 0u);
+                    ++blocks;
+                    return true;
+                };
+                while (ok && items.next(bars, p.status, &it)) {
+                    if (it.head < 0) break;
+                    const int steps = max(it.step_hi[0], it.step_hi[1]);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok || it.step_hi[t] <= it.step_lo) continue;
+                        if (q_loads[t] > 0)
+                            ok = wait(MLA_BAR(q_empty) + 8 * t, (q_loads[t] - 1) & 1, bars,
+                                      p.status, kSiteQFree);
+                        if (!ok) continue;
+                        const uint32_t bar = MLA_BAR(q_full) + 8 * t;
+                        ptx::mbar_arrive_expect_tx(bar, kQBlocks * kBlock);
+                        for (int c = 0; c < kQBlocks; ++c)
+                            ptx::tma_load_2d(sbase + uint32_t((t * kQBlocks + c) * kBlock), &map_q,
+                                             it.head * kQk + 64 * c, it.q_row + t * kTileRows, bar);
+                        ++q_loads[t];
+                    }
+                    uint32_t addr, bar;
+                    for (int j = it.step_lo; j < steps && ok; ++j) {
+                        const int row = it.k_row + j * kStep;
+                        for (int c = 0; c < 3 && ok; ++c) {
+                            ok = slot(0, &addr, &bar);
+                            if (!ok) break;
+                            if (c < 2)
+                                ptx::tma_load_2d(addr, &map_k, it.head * kKvHead + 64 * c, row, bar);
+                            else
+                                ptx::tma_load_2d(addr, &map_pe, 0, row, bar);
+                        }
+                        const uint32_t raw =
+                            j >= it.fix_from ? MLA_BAR(raw_full) + 8 * (raws & 1) : 0;
+                        for (int c = 0; c < 2 && ok; ++c) {
+                            ok = slot(raw, &addr, &bar);
+                            if (!ok) break;
+                            // (two steps back on this barrier: their slots were
+                            // released, so that phase is complete)
+                            if (raw != 0 && c == 0) {
+                                ptx::mbar_arrive_expect_tx(raw, 2 * kBlock);
+                                ++raws;
+                            }
+                            const int x = it.head * kKvHead + 128, y = row + 64 * c;
+                            ptx::tma_load_2d(addr, &map_v, x, y, bar);
+                            ptx::tma_load_2d(addr + 8192, &map_v, x + 64, y, bar);
+                        }
+                    }
+                    items.release();
+                }
+                // Loads still in flight (after an abort) land before the CTA exits.
+                for (uint32_t i = blocks > kRing ? blocks - kRing : 0; i < blocks; ++i)
+                    if (!(raw_slots >> (i % kRing) & 1))
+                        wait(MLA_BAR(ring_full) + 8 * (i % kRing), (i / kRing) & 1, bars, p.status,
+                             kSiteDrain, true);
+                for (uint32_t i = raws > 2 ? raws - 2 : 0; i < raws; ++i)
+                    wait(MLA_BAR(raw_full) + 8 * (i & 1), (i >> 1) & 1, bars, p.status, kSiteDrain,
+                         true);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (q_loads[t] > 0)
+                        wait(MLA_BAR(q_full) + 8 * t, (q_loads[t] - 1) & 1, bars, p.status,
+                             kSiteDrain, true);
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // -------------------------------------------------------- MMAs
+            if (ptx::elect_one()) {
+                constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kStep, false);
+                constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(kV, true);
+                uint32_t block = 0;            // first ring block of the step's keys
+                uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+                bool ok = true;
+                auto ring_wait = [&](uint32_t i) {
+                    return wait(MLA_BAR(ring_full) + 8 * (i % kRing), (i / kRing) & 1, bars,
+                                p.status, kSiteRing);
+                };
+                auto ring_addr = [&](uint32_t i) {
+                    return sbase + uint32_t(kOffRing) + (i % kRing) * kBlock;
+                };
+                // Scores of tile t for the step whose keys start at ring block kb.
+                auto scores = [&](int t, uint32_t kb) {
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        if (!ring_wait(kb + c)) return false;
+                        ptx::tc_fence_after();
+                        const uint32_t a = sbase + uint32_t((t * kQBlocks + c) * kBlock);
+                        const uint32_t b = ring_addr(kb + c);
+                        ptx::mma4_ss(tmem + kTmemS + 128 * t, ptx::desc_sw128(a, 16, 1024),
+                                     ptx::desc_sw128(a + 32, 16, 1024),
+                                     ptx::desc_sw128(a + 64, 16, 1024),
+                                     ptx::desc_sw128(a + 96, 16, 1024),
+                                     ptx::desc_sw128(b, 16, 1024),
+                                     ptx::desc_sw128(b + 32, 16, 1024),
+                                     ptx::desc_sw128(b + 64, 16, 1024),
+                                     ptx::desc_sw128(b + 96, 16, 1024), idesc_s, c > 0 ? 1u : 0u);
+                    }
+                    ptx::mma_commit(MLA_BAR(s_full) + 8 * t);
+                    return true;
+                };
+                // O of tile t += P V, V at ring blocks vb, vb + 1.
+                auto values = [&](int t, uint32_t vb, bool first) {
+                    if (!wait(MLA_BAR(p_ready) + 8 * t, p_uses[t] & 1, bars, p.status, kSiteP))
+                        return false;
+                    ++p_uses[t];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (!ring_wait(vb + c)) return false;
+                        ptx::tc_fence_after();
+                        const uint32_t a = tmem + kTmemS + 128 * t + 32 * c;
+                        const uint32_t b = ring_addr(vb + c);
+                        ptx::mma4_ts(tmem + kTmemO + 128 * t, a, a + 8, a + 16, a + 24,
+                                     ptx::desc_sw128(b, 8192, 1024),
+                                     ptx::desc_sw128(b + 2048, 8192, 1024),
+                                     ptx::desc_sw128(b + 4096, 8192, 1024),
+                                     ptx::desc_sw128(b + 6144, 8192, 1024), idesc_o,
+                                     c > 0 || !first ? 1u : 0u);
+                    }
+                    ptx::mma_commit(MLA_BAR(pv_done) + 8 * t);
+                    return true;
+                };
+                auto release = [&](uint32_t i, int n) {
+                    for (int c = 0; c < n; ++c)
+                        ptx::mma_commit(MLA_BAR(ring_empty) + 8 * ((i + c) % kRing));
+                };
+                while (ok && items.next(bars, p.status, &it)) {
+                    if (it.head < 0) break;
+                    const int steps = max(it.step_hi[0], it.step_hi[1]);
+                    // First the scores of the first step; then, per step, P.V
+                    // of the step and the scores of the next, tile after tile.
+                    for (int j = it.step_lo - 1; j < steps && ok; ++j) {
+                        const uint32_t vb = block + 3;
+                        const uint32_t kb = j < it.step_lo ? block : block + 5;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!ok) continue;
+                            if (j >= it.step_lo && j < it.step_hi[t])
+                                ok = values(t, vb, j == it.step_lo);
+                            if (j >= it.step_lo && t == 1) release(vb, 2);
+                            if (ok && j + 1 < it.step_hi[t]) {
+                                if (j < it.step_lo) {
+                                    ok = wait(MLA_BAR(q_full) + 8 * t, q_uses[t] & 1, bars,
+                                              p.status, kSiteQ);
+                                    ++q_uses[t];
+                                }
+                                ok = ok && scores(t, kb);
+                                if (ok && j + 2 == it.step_hi[t])
+                                    ptx::mma_commit(MLA_BAR(q_empty) + 8 * t);
+                            }
+                        }
+                        if (ok && j + 1 < steps) release(kb, 3);
+                        if (j >= it.step_lo) block += 5;
+                    }
+                    items.release();
+                }
+                // Every MMA issued above has completed before TMEM is freed.
+                ptx::mma_commit(MLA_BAR(drain));
+                wait(MLA_BAR(drain), 0, bars, p.status, kSiteDrain, true);
+            }
+            __syncwarp();
+        } else if (warp == 10) {
+            // ------------------------------------------------------ helper
+            uint32_t block = 0, raws = 0;
+            bool ok = true;
+            while (ok) {
+                ok = __all_sync(0xffffffffu, items.next(bars, p.status, &it));
+                if (!ok || it.head < 0) break;
+                const int steps = max(it.step_hi[0], it.step_hi[1]);
+                if (it.fix_from > it.step_lo)
+                    block += 5 * uint32_t(min(it.fix_from, steps) - it.step_lo);
+                for (int j = it.fix_from; j < steps; ++j, block += 5, ++raws) {
+                    ok = __all_sync(0xffffffffu,
+                                    wait(MLA_BAR(raw_full) + 8 * (raws & 1), (raws >> 1) & 1, bars,
+                                         p.status, kSiteRaw));
+                    if (!ok) break;
+                    const int end = it.lk - j * kStep;      // rows of the step that exist
+                    uint32_t top = 0;                       // largest magnitudes, two at a time
+                    for (int c = 0; c < 2; ++c) {
+                        // Two 64 x 64 boxes of 128-byte rows; a row is 8 pieces of 16 bytes.
+                        uint4* v = reinterpret_cast<uint4*>(
+                            smem + kOffRing + ((block + 3 + c) % kRing) * kBlock);
+#pragma unroll 4
+                        for (int k = lane; k < kBlock / 16; k += 32) {
+                            const int row = 64 * c + ((k >> 3) & 63);
+                            if (row >= end) {
+                                v[k] = make_uint4(0, 0, 0, 0);
+                            } else {
+                                const uint4 x = v[k];
+                                top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu,
+                                                                      x.y & 0x7fff7fffu),
+                                                             __vmaxu2(x.z & 0x7fff7fffu,
+                                                                      x.w & 0x7fff7fffu)));
+                            }
+                        }
+                    }
+                    const bool bad = (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u;
+                    if (__any_sync(0xffffffffu, bad)) {
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t* v = reinterpret_cast<uint32_t*>(
+                                smem + kOffRing + ((block + 3 + c) % kRing) * kBlock);
+                            for (int k = lane; k < kBlock / 4; k += 32) {
+                                uint32_t x = v[k];
+                                if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+                                if ((x & 0x7f800000u) == 0x7f800000u) x &= 0x0000ffffu;
+                                v[k] = x;
+                            }
+                        }
+                        if (lane == 0) bars->bad_item[items.n % kItemSlots] = int32_t(items.n);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane < 2)
+                        ptx::mbar_arrive(MLA_BAR(ring_full) + 8 * ((block + 3 + lane) % kRing));
+                }
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(MLA_BAR(item_empty) + 8 * (items.n % kItemSlots));
+                ++items.n;
+            }
+        } else {
+            // --------------------------------------------------- scheduler
+            int tiles = 0;
+            {
+                int q0, lq, k0, lk;
+                for (int b = lane; b < p.batch; b += 32) {
+                    sequence(p, b, &q0, &lq, &k0, &lk);
+                    tiles += item_tiles(lq);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+            }
+            const int64_t total = int64_t(tiles) * p.heads * p.splits;
+            uint32_t n = 0;
+            for (int64_t k = 0;; ++k) {
+                // Odd turns run backwards, so that who had a long item of one
+                // turn has a short one of the next.
+                const int64_t index = k * gridDim.x +
+                                      ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                const bool more = k * int64_t(gridDim.x) < total;
+                if (more && index >= total) continue;
+                Item next;
+                next.head = -1;
+                if (more) next = find_item(p, index, tiles);
+                const uint32_t s = n % kItemSlots, turn = n / kItemSlots;
+                const bool ok = turn == 0 || wait(MLA_BAR(item_empty) + 8 * s, (turn - 1) & 1, bars,
+                                                  p.status, kSiteItemFree);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (lane == 0) {
+                    bars->items[s] = next;
+                    ptx::mbar_arrive(MLA_BAR(item_full) + 8 * s);
+                }
+                __syncwarp();
+                ++n;
+                if (!more) break;
+            }
+        }
+    } else {
+        // ------------------------------------------------ softmax, epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = warp >> 2;
+        const int row = (warp & 3) * 32 + lane;            // of the tile, = TMEM lane
+        const uint32_t ts = tmem + kTmemS + 128 * t + (uint32_t((warp & 3) * 32) << 16);
+        const uint32_t to = tmem + kTmemO + 128 * t + (uint32_t((warp & 3) * 32) << 16);
+        uint32_t s_uses = 0;
+        bool ok = true;
+        while (ok) {
+            ok = __all_sync(0xffffffffu, items.next(bars, p.status, &it));
+            if (!ok || it.head < 0) break;
+            const int in_item = t * kTileRows + row;
+            const int limit = p.causal ? min(it.limit0 + in_item, it.lk - 1) : it.lk - 1;
+            float m = -INFINITY, sum = 0.f;
+            const int hi = t == 0 ? it.step_hi[0] : it.step_hi[1];
+            for (int j = it.step_lo; j < hi; ++j) {
+                ok = __all_sync(0xffffffffu, wait(MLA_BAR(s_full) + 8 * t, s_uses & 1, bars,
+                                                  p.status, kSiteS));
+                if (!ok) break;
+                ++s_uses;
+                ptx::tc_fence_after();
+                float v[128];
+                tmem_ld128(ts, v);
+                const int seen = limit - j * kStep + 1;     // keys of the step this row sees
+                if (__any_sync(0xffffffffu, seen < kStep)) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) v[c] = c < seen ? v[c] : -INFINITY;
+                }
+                float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                for (int c = 4; c < 124; c += 8) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        m4[i] = ptx::fmax3(m4[i], v[c + i], v[c + 4 + i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], v[124 + i]);
+                const float m_new = fmaxf(fmaxf(m, ptx::fmax3(m4[0], m4[1], m4[2])), m4[3]);
+                if (j == it.step_lo) {
+                    m = m_new;
+                } else if (__any_sync(0xffffffffu,
+                                      (m_new - m) * p.scale_log2 > kRescaleThreshold)) {
+                    // (m = -inf: no key seen so far, O and the sum are 0)
+                    const float alpha = m == -INFINITY ? 1.f : ptx::ex2((m - m_new) * p.scale_log2);
+                    m = m_new;
+                    sum *= alpha;
+                    ok = __all_sync(0xffffffffu, wait(MLA_BAR(pv_done) + 8 * t, s_uses & 1, bars,
+                                                      p.status, kSitePv));
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < kV; c += 32) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(to + c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        ptx::tmem_st32(to + c, o);
+                    }
+                }
+                // One FMA per weight, 2^(v c - fl(m c)); its exponent is off by
+                // the rounding of m c, |m c| 2^-24 at most. Where that could
+                // count (2^-14 at 1024; an overflow at 2^31) m is taken off
+                // the scores first.
+                float shift = m == -INFINITY ? 0.f : -m * p.scale_log2;
+                if (__any_sync(0xffffffffu, fabsf(shift) > 1024.f)) {
+                    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) v[c] -= base;
+                    shift = 0.f;
+                }
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float a = ptx::ex2(fmaf(v[g * 64 + 2 * i], p.scale_log2, shift));
+                        const float b = ptx::ex2(fmaf(v[g * 64 + 2 * i + 1], p.scale_log2, shift));
+                        part[(2 * i) & 3] += a;
+                        part[(2 * i + 1) & 3] += b;
+                        w[i] = pack_bf16(a, b);
+                    }
+                    ptx::tmem_st32(ts + 32 * g, w);
+                }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(MLA_BAR(p_ready) + 8 * t);
+            }
+            if (!ok) break;
+            // Epilogue.
+            bool repair = false;
+            if (hi > it.step_lo) {
+                ok = __all_sync(0xffffffffu, wait(MLA_BAR(pv_done) + 8 * t, (s_uses - 1) & 1, bars,
+                                                  p.status, kSitePv));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                // (the last P.V waited for the helper, so its word is there)
+                if (hi > it.fix_from)
+                    repair = *reinterpret_cast<volatile int32_t*>(
+                                 &bars->bad_item[items.n % kItemSlots]) == int32_t(items.n);
+            }
+            const bool mine = in_item < it.q_rows;
+            const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (a NaN sum stays NaN)
+            const int64_t out_row = int64_t(it.q_row + in_item) * p.heads + it.head;
+            if (mine) {
+                const float lse =
+                    sum == 0.f ? -INFINITY : m * (p.scale_log2 * kLn2) + logf(sum);
+                if (p.splits > 1) p.lse_part[out_row * p.splits + it.split] = lse;
+                else if (p.lse != nullptr) p.lse[out_row] = lse;
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int c = 0; c < kV; c += 32) {
+                uint32_t o[32];
+                if (hi > it.step_lo) {
+                    ptx::tmem_ld32(to + c, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                }
+                if (mine) {
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
+                    if (repair) {
+                        // The values the helper took out of the product, for
+                        // the keys this row sees: its weight is > 0, so a NaN
+                        // or infinity comes through whatever the weight.
+                        const int last = min(limit, hi * kStep - 1);
+#pragma unroll 1
+                        for (int k = it.fix_from * kStep; k <= last; ++k) {
+                            const uint4* vr = reinterpret_cast<const uint4*>(
+                                p.kv + (int64_t(it.k_row + k) * p.heads + it.head) * kKvHead +
+                                128 + c);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 x = __ldg(vr + i);
+                                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((u[e] & 0x7f80u) == 0x7f80u)
+                                        f[8 * i + 2 * e] += __uint_as_float(u[e] << 16);
+                                    if ((u[e] & 0x7f800000u) == 0x7f800000u)
+                                        f[8 * i + 2 * e + 1] +=
+                                            __uint_as_float(u[e] & 0xffff0000u);
+                                }
+                            }
+                        }
+                    }
+                    if (p.splits > 1) {
+                        float* dst = p.o_part + (out_row * p.splits + it.split) * kV + c;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(f[i + k]);
+                            ptx::st_global_v8(dst + i, w);
+                        }
+                    } else {
+                        uint16_t* dst = p.out + out_row * kV + c;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 16) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                w[k] = pack_bf16(f[i + 2 * k], f[i + 2 * k + 1]);
+                            ptx::st_global_v8(dst + i, w);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(MLA_BAR(item_empty) + 8 * (items.n % kItemSlots));
+            ++items.n;
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 9) ptx::tmem_dealloc(tmem, 512);
+#undef MLA_BAR
+}
+
+// The splits' partial rows into the result, with the identity of
+// mla_merge_splits; only rows that a sequence holds are written. One warp per
+// (row, head), four columns per lane.
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= int64_t(p.total_q) * p.heads) return;
+    // The row's sequence: the last b with cu_q[b] <= q.
+    const int q = int(row / p.heads);
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu_q[mid] <= q) lo = mid; else hi = mid;
+    }
+    const int begin = p.cu_q[lo], end = p.cu_q[lo + 1];
+    if (begin < 0 || q < begin || q >= end || end > p.total_q) return;
+    const float* ls = p.lse_part + row * p.splits;
+    float m = -INFINITY;
+    for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ls[s]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float z = 0.f;
+    for (int s = 0; s < p.splits; ++s) {
+        const float l = ls[s];
+        if (l == -INFINITY) continue;
+        const float w = expf(l - m);   // (NaN where a partial is NaN)
+        const float4 v = *reinterpret_cast<const float4*>(
+            p.o_part + (row * p.splits + s) * kV + lane * 4);
+        z += w;
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+    }
+    const float inv = z != 0.f ? 1.f / z : 0.f;
+    uint2 o;
+    o.x = pack_bf16(acc.x * inv, acc.y * inv);
+    o.y = pack_bf16(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(p.out + row * kV + lane * 4) = o;
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
+
+// A split should have at least this many key steps: fewer cost more in items
+// and merging than the extra CTAs bring.
+constexpr int kMinSplitSteps = 4;
+
+void layout(mla_prefill_plan_t* p) {
+    p->partial_offset = kStatusBytes;
+    p->lse_partial_offset = kStatusBytes;
+    p->workspace_bytes = kStatusBytes;
+    if (p->num_kv_splits > 1) {
+        const uint64_t rows = uint64_t(p->total_q) * p->num_heads * p->num_kv_splits;
+        p->lse_partial_offset = p->partial_offset + round256(rows * kV * 4);
+        p->workspace_bytes = p->lse_partial_offset + round256(rows * 4);
+    }
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q_len,
+                                int max_k_len, int num_kv_splits, int num_sms,
+                                mla_prefill_plan_t* plan) {
+    if (!plan || batch < 0 || num_heads < 1 || total_q < 0 || max_q_len < 0 || max_k_len < 0 ||
+        num_kv_splits < 0 || num_sms < 1)
+        return MLA_ERR_INVALID_ARG;
+    if (num_heads > kMaxHeads || num_kv_splits > kMaxSplits) return MLA_ERR_UNSUPPORTED;
+    mla_prefill_plan_t p;
+    std::memset(&p, 0, sizeof(p));
+    p.batch = batch;
+    p.num_heads = num_heads;
+    p.total_q = total_q;
+    p.num_sms = num_sms;
+    p.num_kv_splits = num_kv_splits;
+    if (num_kv_splits == 0) {
+        // Split only while the items leave SMs idle.
+        const int64_t per_seq = (int64_t(max_q_len) + kItemRows - 1) / kItemRows;
+        int64_t tiles = batch * per_seq;
+        const int64_t bound = int64_t(total_q) / kItemRows + batch;
+        if (tiles > bound) tiles = bound;
+        const int64_t items = tiles * num_heads;
+        const int64_t steps = (int64_t(max_k_len) + kStep - 1) / kStep;
+        int64_t s = items > 0 ? num_sms / items : 1;
+        if (s > steps / kMinSplitSteps) s = steps / kMinSplitSteps;
+        if (s > kMaxSplits) s = kMaxSplits;
+        p.num_kv_splits = s < 1 ? 1 : int(s);
+    }
+    layout(&p);
+    *plan = p;
+    return MLA_OK;
+}
+
+extern "C" int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const void* kv,
+                           const void* k_pe, int total_k, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, int causal, float softmax_scale, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!plan) return MLA_ERR_INVALID_ARG;
+    if (plan->batch < 0 || plan->num_heads < 1 || plan->num_heads > kMaxHeads ||
+        plan->total_q < 0 || plan->num_kv_splits < 1 || plan->num_kv_splits > kMaxSplits ||
+        plan->num_sms < 1 || total_k < 0)
+        return MLA_ERR_INVALID_ARG;
+    mla_prefill_plan_t check = *plan;
+    layout(&check);
+    if (check.partial_offset != plan->partial_offset ||
+        check.lse_partial_offset != plan->lse_partial_offset ||
+        check.workspace_bytes != plan->workspace_bytes)
+        return MLA_ERR_INVALID_ARG;
+    const float scale_log2 = softmax_scale * 1.4426950408889634f;
+    if (!(scale_log2 > 0.f) || !std::isfinite(scale_log2)) return MLA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < plan->workspace_bytes || !aligned(workspace, 256))
+        return MLA_ERR_WORKSPACE;
+    if (plan->batch == 0 || plan->total_q == 0) return MLA_OK;
+    if (!q || !out || !cu_seqlens_q || !cu_seqlens_k || (total_k > 0 && (!kv || !k_pe)))
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(k_pe, 16) || !aligned(out, 32) ||
+        (lse && !aligned(lse, 4)) || !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4))
+        return MLA_ERR_INVALID_ARG;
+    PrefillParams p{};
+    char* ws = static_cast<char*>(workspace);
+    p.kv = static_cast<const uint16_t*>(kv);
+    p.cu_q = cu_seqlens_q;
+    p.cu_k = cu_seqlens_k;
+    p.batch = plan->batch;
+    p.heads = plan->num_heads;
+    p.total_q = plan->total_q;
+    p.total_k = total_k;
+    p.causal = causal ? 1 : 0;
+    p.splits = plan->num_kv_splits;
+    p.scale_log2 = scale_log2;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.o_part = reinterpret_cast<float*>(ws + plan->partial_offset);
+    p.lse_part = reinterpret_cast<float*>(ws + plan->lse_partial_offset);
+    p.status = reinterpret_cast<int32_t*>(ws);
+    const int64_t head_bytes = int64_t(total_k) * kKvHead * 2;
+    const int64_t group = head_bytes > 0 ? kGroupBytes / head_bytes : p.heads;
+    p.group = group < 1 ? 1 : group > p.heads ? p.heads : int(group);
+    // (Without keys the maps over them are never read through; the queries
+    // stand in.)
+    CUtensorMap mq, mk, mv, mpe;
+    const void* kv_base = total_k > 0 ? kv : q;
+    const void* pe_base = total_k > 0 ? k_pe : q;
+    const uint64_t k_rows = total_k > 0 ? uint64_t(total_k) : 1;
+    const uint64_t kv_cols = total_k > 0 ? uint64_t(p.heads) * kKvHead : 64;
+    if (!encode_2d(&mq, q, uint64_t(p.heads) * kQk, uint64_t(p.total_q), kTileRows) ||
+        !encode_2d(&mk, kv_base, kv_cols, k_rows, kStep) ||
+        !encode_2d(&mv, kv_base, kv_cols, k_rows, kStep / 2) ||
+        !encode_2d(&mpe, pe_base, kRope, k_rows, kStep))
+        return MLA_ERR_CUDA;
+    if (cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemBytes) != cudaSuccess)
+        return MLA_ERR_CUDA;
+    const int64_t most = (int64_t(p.total_q) / kItemRows + p.batch) * p.heads * p.splits;
+    const unsigned grid = unsigned(most < plan->num_sms ? most : plan->num_sms);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    mla_prefill_kernel<<<grid, kThreads, kSmemBytes, st>>>(p, mq, mk, mv, mpe);
+    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    if (p.splits > 1) {
+        const int64_t rows = int64_t(p.total_q) * p.heads;
+        prefill_merge_kernel<<<unsigned((rows + 7) / 8), 256, 0, st>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    }
+    return MLA_OK;
+}

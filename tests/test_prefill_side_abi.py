@@ -143,3 +143,101 @@ def test_cache_workspace_sizes(lib):
     for blocks, children in [(0, 0), (-1, 0), ((1 << 23) - 1, 0), (10, -1), (10, 8193)]:
         assert size(blocks, children) == 0
     assert ctypes.sizeof(ctypes.c_size_t) == 8
+
+
+def _plan(lib, batch=2, heads=16, total_q=600, max_q=300, max_k=1000, splits=0, sms=152):
+    plan = binding.MlaPrefillPlan()
+    rc = lib.mla_prefill_plan(batch, heads, total_q, max_q, max_k, splits, sms, ctypes.byref(plan))
+    return rc, plan
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(heads=0), binding.MLA_ERR_INVALID_ARG),
+    (dict(heads=129), binding.MLA_ERR_UNSUPPORTED),
+    (dict(batch=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(total_q=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(max_q=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(max_k=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(splits=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(splits=65), binding.MLA_ERR_UNSUPPORTED),
+    (dict(sms=0), binding.MLA_ERR_INVALID_ARG),
+    (dict(batch=0, total_q=0, max_q=0, max_k=0), binding.MLA_OK),
+])
+def test_prefill_plan_refusals(lib, kw, code):
+    assert _plan(lib, **kw)[0] == code
+    assert lib.mla_prefill_plan(1, 1, 1, 1, 1, 0, 152, None) == binding.MLA_ERR_INVALID_ARG
+
+
+def test_prefill_plan_layout_and_splits(lib):
+    rc, p = _plan(lib, splits=1)
+    assert rc == 0 and p.workspace_bytes == binding.STATUS_BYTES
+    rc, p = _plan(lib, splits=5)
+    rows = 600 * 16 * 5
+    assert p.partial_offset == binding.STATUS_BYTES
+    assert p.lse_partial_offset == p.partial_offset + rows * 512
+    assert p.workspace_bytes >= p.lse_partial_offset + rows * 4 and p.workspace_bytes % 256 == 0
+    # split only while SMs would idle, and only keys that are long enough
+    assert _plan(lib, batch=1, heads=16, total_q=1, max_q=1, max_k=8192)[1].num_kv_splits > 1
+    assert _plan(lib, batch=1, heads=16, total_q=1, max_q=1, max_k=300)[1].num_kv_splits == 1
+    assert _plan(lib, batch=8, heads=128, total_q=8, max_q=1, max_k=8192)[1].num_kv_splits == 1
+
+
+def test_prefill_plan_struct_matches_the_header(tmp_path):
+    import os
+    import subprocess
+    src = tmp_path / "layout.c"
+    src.write_text(
+        '#include <stdio.h>\n#include <stddef.h>\n#include "mla_decode.h"\n'
+        "int main(void){printf(\"%zu %zu %zu %zu\\n\", sizeof(mla_prefill_plan_t),"
+        " offsetof(mla_prefill_plan_t, num_sms), offsetof(mla_prefill_plan_t, workspace_bytes),"
+        " offsetof(mla_prefill_plan_t, reserved));return 0;}\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c99", "-I", build.INCLUDE, str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    P = binding.MlaPrefillPlan
+    assert got == [ctypes.sizeof(P), P.num_sms.offset, P.workspace_bytes.offset, P.reserved.offset]
+    assert os.path.exists(build.INCLUDE)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(plan=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(q=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(q=X + 8), binding.MLA_ERR_INVALID_ARG),
+    (dict(kv=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(kv=X + 8), binding.MLA_ERR_INVALID_ARG),
+    (dict(pe=X + 8), binding.MLA_ERR_INVALID_ARG),
+    (dict(total_k=-1), binding.MLA_ERR_INVALID_ARG),
+    (dict(cu_q=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(cu_k=X + 2), binding.MLA_ERR_INVALID_ARG),
+    (dict(scale=0.0), binding.MLA_ERR_INVALID_ARG),
+    (dict(scale=-1.0), binding.MLA_ERR_INVALID_ARG),
+    (dict(scale=float("inf")), binding.MLA_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), binding.MLA_ERR_INVALID_ARG),
+    (dict(scale=3e38), binding.MLA_ERR_INVALID_ARG),
+    (dict(out=X + 16), binding.MLA_ERR_INVALID_ARG),
+    (dict(out=None), binding.MLA_ERR_INVALID_ARG),
+    (dict(lse=X + 2), binding.MLA_ERR_INVALID_ARG),
+    (dict(ws=None), binding.MLA_ERR_WORKSPACE),
+    (dict(ws=X + 128), binding.MLA_ERR_WORKSPACE),
+    (dict(nbytes=8192), binding.MLA_ERR_WORKSPACE),
+])
+def test_prefill_refusals(lib, kw, code):
+    plan = _plan(lib, splits=3)[1]
+    a = dict(plan=ctypes.byref(plan), q=X, kv=X, pe=X, total_k=2000, cu_q=X, cu_k=X, causal=1,
+             scale=0.1, out=X, lse=None, ws=X, nbytes=int(plan.workspace_bytes))
+    a.update(kw)
+    assert lib.mla_prefill(*(a[k] for k in ("plan", "q", "kv", "pe", "total_k", "cu_q", "cu_k",
+                                            "causal", "scale", "out", "lse", "ws", "nbytes")),
+                           None) == code
+
+
+@pytest.mark.parametrize("field,value", [("workspace_bytes", 8192), ("partial_offset", 0),
+                                         ("lse_partial_offset", 8192), ("num_kv_splits", 0),
+                                         ("num_kv_splits", 2), ("num_heads", 200), ("batch", -1),
+                                         ("total_q", -5), ("num_sms", 0)])
+def test_prefill_refuses_an_edited_plan(lib, field, value):
+    plan = _plan(lib, splits=3)[1]
+    setattr(plan, field, value)
+    assert lib.mla_prefill(ctypes.byref(plan), X, X, X, 2000, X, X, 1, 0.1, X, None, X, 1 << 30,
+                           None) == binding.MLA_ERR_INVALID_ARG
