@@ -536,79 +536,90 @@ def mla_v_up_proj(x, w_uv, *, workspace, out=None, stream=None):
     return out
 
 
-def _on(device, stream):
-    """The torch stream a call runs on: `stream`, else the device's current one."""
-    import torch
-    return stream if stream is not None else torch.cuda.current_stream(device)
-
-
 def _empty(shape, dtype, device, stream, fill=None):
     """A new tensor that belongs to the stream the call runs on."""
     import torch
-    make = torch.empty if fill is None else (lambda *a, **k: torch.full(*a, fill, **k))
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=device)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty(shape, dtype, device, None, fill)
+    if fill is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.full(shape, fill, dtype=dtype, device=device)
 
 
-def _check_tensors(device, *args):
-    """Each (name, tensor, dtype, shape or None) is a contiguous tensor of
-    that type and shape on `device`."""
-    for name, t, dtype, shape in args:
-        _check_tensor(t, name, dtype, shape)
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _arg(name, t, dtype, device, shape=None):
+    """The address of `t`, a contiguous tensor of that type (and shape) on
+    `device`. The small calls take a few microseconds on the GPU, so the
+    checks of what is right come first and cost least."""
+    try:
+        if (t.dtype is dtype and t.device == device and (shape is None or t.shape == shape)
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _check_tensor(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-def _call(device, stream, name, *args):
-    """Call a library function with `device` current; raises on a status."""
+def _ndim(name, t, ndim, what):
+    """The shape of a tensor of `ndim` dimensions."""
+    shape = getattr(t, "shape", None)
+    if shape is None:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if len(shape) != ndim:
+        raise ValueError(f"{name} must be {what}")
+    return shape
+
+
+def _device_of(name, t):
+    """The CUDA device that a call's other tensors have to be on."""
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _call(device, stream, fn, *args):
+    """Call a library function with `device` current, on `stream` or the
+    device's current one; raises on a status."""
     import torch
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, _on(device, stream).cuda_stream)
-    else:
+    if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
-            rc = fn(*args, _on(device, stream).cuda_stream)
-    _check(rc, name)
+            return _call(device, stream, fn, *args)
+    raw = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+           else stream.cuda_stream)
+    rc = fn(*args, raw)
+    if rc != MLA_OK:
+        raise MlaError(rc, fn.__name__)
 
 
-def _expand_kv(name, cache_dtype, latent_cache, block_table, cu_seqlens_k, w_uk_t, w_uv, k_scale,
+def _expand_kv(fn, cache_dtype, latent_cache, block_table, cu_seqlens_k, w_uk_t, w_uv, k_scale,
                total_k, first_token, kv, k_pe, workspace, stream):
     import torch
-    dev = latent_cache.device
-    _check_tensors(dev, ("latent_cache", latent_cache, cache_dtype, None),
-                   ("block_table", block_table, torch.int32, None),
-                   ("cu_seqlens_k", cu_seqlens_k, torch.int32, None),
-                   ("w_uk_t", w_uk_t, torch.bfloat16, None), ("w_uv", w_uv, torch.bfloat16, None),
-                   ("workspace", workspace, torch.uint8, None))
-    if latent_cache.dim() != 3 or latent_cache.shape[1:] != (PAGE_SIZE, HEAD_DIM):
-        raise ValueError("latent_cache must be [num_blocks, 64, 576]")
-    if cu_seqlens_k.dim() != 1 or cu_seqlens_k.shape[0] < 1:
-        raise ValueError("cu_seqlens_k must be [B + 1]")
-    B = cu_seqlens_k.shape[0] - 1
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_blocks_per_seq]")
-    N = w_uk_t.shape[0]
-    if tuple(w_uk_t.shape) != (N, 128, 512) or tuple(w_uv.shape) != (N, 512, 128):
-        raise ValueError("w_uk_t must be [N, 128, 512] and w_uv [N, 512, 128]")
-    if first_token is not None:
-        _check_tensors(dev, ("first_token", first_token, torch.int32, (B,)))
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _device_of("latent_cache", latent_cache)
+    blocks = _ndim("latent_cache", latent_cache, 3, "[num_blocks, 64, 576]")[0]
+    B = _ndim("cu_seqlens_k", cu_seqlens_k, 1, "[B + 1]")[0] - 1
+    rows, mb = _ndim("block_table", block_table, 2, "[B, max_blocks_per_seq]")
+    N = _ndim("w_uk_t", w_uk_t, 3, "[N, 128, 512]")[0]
     T = int(total_k)
+    if B < 0:
+        raise ValueError("cu_seqlens_k must be [B + 1]")
     if T < 0:
         raise ValueError("total_k must not be negative")
     if kv is None:
-        kv = _empty((T, N, 256), torch.bfloat16, dev, stream)
+        kv = _empty((T, N, 256), bf16, dev, stream)
     if k_pe is None:
-        k_pe = _empty((T, ROPE_DIM), torch.bfloat16, dev, stream)
-    _check_tensors(dev, ("kv", kv, torch.bfloat16, (T, N, 256)),
-                   ("k_pe", k_pe, torch.bfloat16, (T, ROPE_DIM)))
-    scale = () if k_scale is None else (float(k_scale),)
-    _call(dev, stream, name, latent_cache.data_ptr(), *scale, latent_cache.shape[0],
-          block_table.data_ptr(), block_table.shape[1],
-          first_token.data_ptr() if first_token is not None else None, cu_seqlens_k.data_ptr(), B,
-          T, N, w_uk_t.data_ptr(), w_uv.data_ptr(), kv.data_ptr(), k_pe.data_ptr(),
-          workspace.data_ptr(), workspace.numel())
+        k_pe = _empty((T, ROPE_DIM), bf16, dev, stream)
+    _call(dev, stream, fn,
+          _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM)),
+          *(() if k_scale is None else (float(k_scale),)), blocks,
+          _arg("block_table", block_table, i32, dev, (B, mb)), mb,
+          None if first_token is None else _arg("first_token", first_token, i32, dev, (B,)),
+          _arg("cu_seqlens_k", cu_seqlens_k, i32, dev), B, T, N,
+          _arg("w_uk_t", w_uk_t, bf16, dev, (N, 128, 512)),
+          _arg("w_uv", w_uv, bf16, dev, (N, 512, 128)), _arg("kv", kv, bf16, dev, (T, N, 256)),
+          _arg("k_pe", k_pe, bf16, dev, (T, ROPE_DIM)),
+          _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
     return kv, k_pe
 
 
@@ -619,15 +630,16 @@ def mla_expand_kv(latent_cache, block_table, cu_seqlens_k, w_uk_t, w_uv, *, tota
     [total_k, N, 256] = [k_nope | v], k_pe bf16 [total_k, 64])``; rows from
     ``cu_seqlens_k[B]`` on are not written."""
     import torch
-    return _expand_kv("mla_expand_kv", torch.bfloat16, latent_cache, block_table, cu_seqlens_k,
-                      w_uk_t, w_uv, None, total_k, first_token, kv, k_pe, workspace, stream)
+    return _expand_kv(load_library().mla_expand_kv, torch.bfloat16, latent_cache, block_table,
+                      cu_seqlens_k, w_uk_t, w_uv, None, total_k, first_token, kv, k_pe, workspace,
+                      stream)
 
 
 def mla_expand_kv_fp8(latent_cache_fp8, block_table, cu_seqlens_k, w_uk_t, w_uv, k_scale, *,
                       total_k, workspace, first_token=None, kv=None, k_pe=None, stream=None):
     """``mla_expand_kv`` over an fp8 cache (uint8 E4M3 codes, per-tensor ``k_scale``)."""
     import torch
-    return _expand_kv("mla_expand_kv_fp8", torch.uint8, latent_cache_fp8, block_table,
+    return _expand_kv(load_library().mla_expand_kv_fp8, torch.uint8, latent_cache_fp8, block_table,
                       cu_seqlens_k, w_uk_t, w_uv, k_scale, total_k, first_token, kv, k_pe,
                       workspace, stream)
 
@@ -654,40 +666,34 @@ def mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, softmax_scale, *, causa
     Returns ``(out bf16 [Tq, N, 128], lse fp32 [Tq, N] | None)``; rows past
     ``cu_seqlens_q[B]`` are not written."""
     import torch
-    _check_tensor(q, "q", torch.bfloat16)
-    if q.dim() != 3 or q.shape[2] != 192:
-        raise ValueError("q must be [total_q, N, 192]")
-    T, N, _ = q.shape
-    dev = q.device
-    _check_tensors(dev, ("kv", kv, torch.bfloat16, None),
-                   ("cu_seqlens_q", cu_seqlens_q, torch.int32, None))
-    if kv.dim() != 3 or tuple(kv.shape[1:]) != (N, 256):
-        raise ValueError(f"kv must be [total_k, {N}, 256]")
-    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 1:
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _device_of("q", q)
+    T, N, _ = _ndim("q", q, 3, "[total_q, N, 192]")
+    Tk = _ndim("kv", kv, 3, "[total_k, N, 256]")[0]
+    B = _ndim("cu_seqlens_q", cu_seqlens_q, 1, "[B + 1]")[0] - 1
+    if B < 0:
         raise ValueError("cu_seqlens_q must be [B + 1]")
-    B, Tk = cu_seqlens_q.shape[0] - 1, kv.shape[0]
     if plan is None:
         plan = make_prefill_plan(B, N, T, T, Tk, num_kv_splits=num_kv_splits)
-    elif (plan.batch, plan.num_heads, plan.total_q) != (B, N, T):
+    elif plan.batch != B or plan.num_heads != N or plan.total_q != T:
         raise ValueError(f"the plan is for (B, N, total_q) = "
                          f"{plan.batch, plan.num_heads, plan.total_q}, not {B, N, T}")
     if out is None:
-        out = _empty((T, N, 128), torch.bfloat16, dev, stream)
+        out = _empty((T, N, 128), bf16, dev, stream)
     if lse is None and return_lse:
         lse = _empty((T, N), torch.float32, dev, stream)
     if workspace is None:
         workspace = _empty((int(plan.workspace_bytes),), torch.uint8, dev, stream)
-        _call(dev, stream, "mla_workspace_init", workspace.data_ptr(), workspace.numel())
-    _check_tensors(dev, ("k_pe", k_pe, torch.bfloat16, (Tk, ROPE_DIM)),
-                   ("cu_seqlens_k", cu_seqlens_k, torch.int32, (B + 1,)),
-                   ("out", out, torch.bfloat16, (T, N, 128)),
-                   ("workspace", workspace, torch.uint8, None))
-    if lse is not None:
-        _check_tensors(dev, ("lse", lse, torch.float32, (T, N)))
-    _call(dev, stream, "mla_prefill", ctypes.byref(plan), q.data_ptr(), kv.data_ptr(),
-          k_pe.data_ptr(), Tk, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), 1 if causal else 0,
-          float(softmax_scale), out.data_ptr(), lse.data_ptr() if lse is not None else None,
-          workspace.data_ptr(), workspace.numel())
+        _call(dev, stream, load_library().mla_workspace_init, workspace.data_ptr(),
+              workspace.numel())
+    _call(dev, stream, load_library().mla_prefill, ctypes.byref(plan),
+          _arg("q", q, bf16, dev, (T, N, 192)), _arg("kv", kv, bf16, dev, (Tk, N, 256)),
+          _arg("k_pe", k_pe, bf16, dev, (Tk, ROPE_DIM)), Tk,
+          _arg("cu_seqlens_q", cu_seqlens_q, i32, dev),
+          _arg("cu_seqlens_k", cu_seqlens_k, i32, dev, (B + 1,)), 1 if causal else 0,
+          float(softmax_scale), _arg("out", out, bf16, dev, (T, N, 128)),
+          None if lse is None else _arg("lse", lse, torch.float32, dev, (T, N)),
+          _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
     return out, lse
 
 
@@ -701,28 +707,29 @@ def new_cache_workspace(num_blocks, children=0, device=None, stream=None):
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     ws = _empty((nbytes,), torch.uint8, dev, stream)
-    _call(dev, stream, "mla_workspace_init", ws.data_ptr(), nbytes)
+    _call(dev, stream, load_library().mla_workspace_init, ws.data_ptr(), nbytes)
     return ws
 
 
-def _cache_view(latent_cache):
+def _cache_view(latent_cache, device):
     """(pointer, layers, layer stride in bytes, blocks, bytes per entry) of a
     cache [num_blocks, 64, 576] or [layers, num_blocks, 64, 576], bf16 or
     uint8; each layer contiguous, the layers any distance apart."""
     import torch
     t = latent_cache
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("latent_cache must be a CUDA tensor")
-    if t.dtype not in (torch.bfloat16, torch.uint8):
+    if _device_of("latent_cache", t) != device:
+        raise ValueError(f"latent_cache must be on {device}, got {t.device}")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.uint8:
         raise TypeError(f"latent_cache must be bfloat16 or uint8, got {t.dtype}")
-    if t.dim() not in (3, 4) or t.shape[-2:] != (PAGE_SIZE, HEAD_DIM):
-        raise ValueError("latent_cache must be [num_blocks, 64, 576] or [layers, num_blocks, 64, 576]")
-    one = t if t.dim() == 3 else t[0]
-    if not one.is_contiguous():
+    shape, size = t.shape, t.element_size()
+    if len(shape) not in (3, 4) or shape[-2:] != (PAGE_SIZE, HEAD_DIM):
+        raise ValueError("latent_cache must be [num_blocks, 64, 576] or "
+                         "[layers, num_blocks, 64, 576]")
+    if not t.is_contiguous() and (len(shape) == 3 or not t[0].is_contiguous()):
         raise ValueError("each layer of latent_cache must be contiguous")
-    size = t.element_size()
-    return (t.data_ptr(), 1 if t.dim() == 3 else t.shape[0],
-            0 if t.dim() == 3 else t.stride(0) * size, one.shape[0], size)
+    if len(shape) == 3:
+        return t.data_ptr(), 1, 0, shape[0], size
+    return t.data_ptr(), shape[0], t.stride(0) * size, shape[1], size
 
 
 def mla_cache_fork(latent_cache, ref_counts, block_table, parents, shared_lens, child_lens, *,
@@ -734,29 +741,23 @@ def mla_cache_fork(latent_cache, ref_counts, block_table, parents, shared_lens, 
     ``ref_counts`` itself unless ``ref_counts_out`` is given, and a new child
     table's unused entries are -1. All or nothing: see the header."""
     import torch
-    dev = ref_counts.device
-    ptr, layers, stride, blocks, size = _cache_view(latent_cache)
-    _check_tensors(dev, ("ref_counts", ref_counts, torch.int32, (blocks,)),
-                   ("block_table", block_table, torch.int32, None),
-                   ("parents", parents, torch.int32, None),
-                   ("workspace", workspace, torch.uint8, None))
-    if latent_cache.device != dev:
-        raise ValueError(f"latent_cache must be on {dev}, got {latent_cache.device}")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [rows, max_blocks_per_seq]")
-    C, (rows, mb) = parents.numel(), block_table.shape
+    i32 = torch.int32
+    dev = _device_of("ref_counts", ref_counts)
+    view = _cache_view(latent_cache, dev)
+    blocks = view[3]
+    rows, mb = _ndim("block_table", block_table, 2, "[rows, max_blocks_per_seq]")
+    C = _ndim("parents", parents, 1, "[children]")[0]
     if child_table is None:
-        child_table = _empty((C, mb), torch.int32, dev, stream, fill=-1)
+        child_table = _empty((C, mb), i32, dev, stream, fill=-1)
     out = ref_counts if ref_counts_out is None else ref_counts_out
-    _check_tensors(dev, ("parents", parents, torch.int32, (C,)),
-                   ("shared_lens", shared_lens, torch.int32, (C,)),
-                   ("child_lens", child_lens, torch.int32, (C,)),
-                   ("child_table", child_table, torch.int32, (C, mb)),
-                   ("ref_counts_out", out, torch.int32, (blocks,)))
-    _call(dev, stream, "mla_cache_fork", ptr, layers, stride, blocks, size, ref_counts.data_ptr(),
-          out.data_ptr(), block_table.data_ptr(), rows, mb, parents.data_ptr(),
-          shared_lens.data_ptr(), child_lens.data_ptr(), C, child_table.data_ptr(),
-          workspace.data_ptr(), workspace.numel())
+    _call(dev, stream, load_library().mla_cache_fork, *view,
+          _arg("ref_counts", ref_counts, i32, dev, (blocks,)),
+          _arg("ref_counts_out", out, i32, dev, (blocks,)),
+          _arg("block_table", block_table, i32, dev), rows, mb,
+          _arg("parents", parents, i32, dev), _arg("shared_lens", shared_lens, i32, dev, (C,)),
+          _arg("child_lens", child_lens, i32, dev, (C,)), C,
+          _arg("child_table", child_table, i32, dev, (C, mb)),
+          _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
     return child_table, out
 
 
@@ -766,25 +767,20 @@ def mla_cache_free(ref_counts, block_table, seq_lens, free_rows, *, workspace, r
     Returns ``(counts, num_freed int32 [1])``; the counts are ``ref_counts``
     itself unless ``ref_counts_out`` is given."""
     import torch
-    dev = ref_counts.device
-    _check_tensors(dev, ("ref_counts", ref_counts, torch.int32, None),
-                   ("block_table", block_table, torch.int32, None),
-                   ("free_rows", free_rows, torch.int32, None),
-                   ("workspace", workspace, torch.uint8, None))
-    if block_table.dim() != 2 or ref_counts.dim() != 1 or free_rows.dim() != 1:
-        raise ValueError("block_table must be [rows, max_blocks_per_seq], ref_counts and "
-                         "free_rows one-dimensional")
-    rows, mb = block_table.shape
+    i32 = torch.int32
+    dev = _device_of("ref_counts", ref_counts)
+    blocks = _ndim("ref_counts", ref_counts, 1, "[num_blocks]")[0]
+    rows, mb = _ndim("block_table", block_table, 2, "[rows, max_blocks_per_seq]")
+    count = _ndim("free_rows", free_rows, 1, "[count]")[0]
     out = ref_counts if ref_counts_out is None else ref_counts_out
     if num_freed is None:
-        num_freed = _empty((1,), torch.int32, dev, stream)
-    _check_tensors(dev, ("seq_lens", seq_lens, torch.int32, (rows,)),
-                   ("ref_counts_out", out, torch.int32, ref_counts.shape),
-                   ("num_freed", num_freed, torch.int32, (1,)))
-    _call(dev, stream, "mla_cache_free", ref_counts.data_ptr(), out.data_ptr(),
-          ref_counts.shape[0], block_table.data_ptr(), rows, mb, seq_lens.data_ptr(),
-          free_rows.data_ptr(), free_rows.shape[0], num_freed.data_ptr(), workspace.data_ptr(),
-          workspace.numel())
+        num_freed = _empty((1,), i32, dev, stream)
+    _call(dev, stream, load_library().mla_cache_free, _arg("ref_counts", ref_counts, i32, dev),
+          _arg("ref_counts_out", out, i32, dev, (blocks,)), blocks,
+          _arg("block_table", block_table, i32, dev), rows, mb,
+          _arg("seq_lens", seq_lens, i32, dev, (rows,)), _arg("free_rows", free_rows, i32, dev),
+          count, _arg("num_freed", num_freed, i32, dev, (1,)),
+          _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
     return out, num_freed
 
 
@@ -795,31 +791,26 @@ def mla_cache_compact(latent_cache, ref_counts, block_table, seq_lens, *, worksp
     ``(block table, counts, page_map int32 [num_blocks], num_live int32 [1])``;
     table and counts are changed in place unless ``*_out`` are given."""
     import torch
-    dev = ref_counts.device
-    ptr, layers, stride, blocks, size = _cache_view(latent_cache)
-    if latent_cache.device != dev:
-        raise ValueError(f"latent_cache must be on {dev}, got {latent_cache.device}")
-    _check_tensors(dev, ("ref_counts", ref_counts, torch.int32, (blocks,)),
-                   ("block_table", block_table, torch.int32, None),
-                   ("workspace", workspace, torch.uint8, None))
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [rows, max_blocks_per_seq]")
-    rows, mb = block_table.shape
+    i32 = torch.int32
+    dev = _device_of("ref_counts", ref_counts)
+    view = _cache_view(latent_cache, dev)
+    blocks = view[3]
+    rows, mb = _ndim("block_table", block_table, 2, "[rows, max_blocks_per_seq]")
     out = ref_counts if ref_counts_out is None else ref_counts_out
     table = block_table if block_table_out is None else block_table_out
     if page_map is None:
-        page_map = _empty((blocks,), torch.int32, dev, stream)
+        page_map = _empty((blocks,), i32, dev, stream)
     if num_live is None:
-        num_live = _empty((1,), torch.int32, dev, stream)
-    _check_tensors(dev, ("seq_lens", seq_lens, torch.int32, (rows,)),
-                   ("ref_counts_out", out, torch.int32, (blocks,)),
-                   ("block_table_out", table, torch.int32, (rows, mb)),
-                   ("page_map", page_map, torch.int32, (blocks,)),
-                   ("num_live", num_live, torch.int32, (1,)))
-    _call(dev, stream, "mla_cache_compact", ptr, layers, stride, blocks, size,
-          ref_counts.data_ptr(), out.data_ptr(), block_table.data_ptr(), table.data_ptr(), rows,
-          mb, seq_lens.data_ptr(), page_map.data_ptr(), num_live.data_ptr(), workspace.data_ptr(),
-          workspace.numel())
+        num_live = _empty((1,), i32, dev, stream)
+    _call(dev, stream, load_library().mla_cache_compact, *view,
+          _arg("ref_counts", ref_counts, i32, dev, (blocks,)),
+          _arg("ref_counts_out", out, i32, dev, (blocks,)),
+          _arg("block_table", block_table, i32, dev),
+          _arg("block_table_out", table, i32, dev, (rows, mb)), rows, mb,
+          _arg("seq_lens", seq_lens, i32, dev, (rows,)),
+          _arg("page_map", page_map, i32, dev, (blocks,)),
+          _arg("num_live", num_live, i32, dev, (1,)),
+          _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
     return table, out, page_map, num_live
 
 
