@@ -92,13 +92,16 @@ struct Item {
 };
 
 struct Bars {
-    uint64_t ring_full[kRing], ring_empty[kRing];
+    // Steps alternate between the two of a pair; the single ones complete
+    // once per step (nobody can be two steps behind them).
+    uint64_t k_full[2], v_full[2];
+    uint64_t k_empty, v_empty;
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];       // scores of the step complete
     uint64_t p_ready[2];      // 128 arrivals: weights in TMEM, O rescaled
     uint64_t pv_done[2];      // P.V of the step complete
-    // A step whose values the helper works on: its V blocks land here (steps
-    // alternate), and the helper completes their ring_full.
+    // A step whose values the helper works on: its V blocks land here, and the
+    // helper completes v_full.
     uint64_t raw_full[2];
     uint64_t item_full[kItemSlots], item_empty[kItemSlots];
     uint64_t drain;
@@ -133,7 +136,7 @@ struct PrefillParams {
 // sleep made the whole kernel 1.7 times slower).
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Bars* bars, int32_t* status,
                                      int32_t site, bool ignore_abort = false) {
-    if (ptx::mbar_try_wait_sleep(bar, parity, kSuspendNs)) return true;
+    if (ptx::mbar_test_wait(bar, parity)) return true;
     volatile int32_t* abort = &bars->abort;
     const uint64_t t0 = ptx::globaltimer();
     while (true) {
@@ -327,18 +330,18 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
         return;
     }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kRing; ++s) {
-            ptx::mbar_init(MLA_BAR(ring_full) + 8 * s, 1);
-            ptx::mbar_init(MLA_BAR(ring_empty) + 8 * s, 1);
-        }
+        ptx::mbar_init(MLA_BAR(k_empty), 1);
+        ptx::mbar_init(MLA_BAR(v_empty), 1);
         for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(MLA_BAR(k_full) + 8 * t, 1);
+            ptx::mbar_init(MLA_BAR(v_full) + 8 * t, 1);
+            ptx::mbar_init(MLA_BAR(raw_full) + 8 * t, 1);
             ptx::mbar_init(MLA_BAR(q_full) + 8 * t, 1);
             ptx::mbar_init(MLA_BAR(q_empty) + 8 * t, 1);
             ptx::mbar_init(MLA_BAR(s_full) + 8 * t, 1);
-            ptx::mbar_init(MLA_BAR(p_ready) + 8 * t, 128);
+            ptx::mbar_init(MLA_BAR(p_ready) + 8 * t, 4);
             ptx::mbar_init(MLA_BAR(pv_done) + 8 * t, 1);
         }
-        for (int t = 0; t < 2; ++t) ptx::mbar_init(MLA_BAR(raw_full) + 8 * t, 1);
         for (int s = 0; s < kItemSlots; ++s) {
             ptx::mbar_init(MLA_BAR(item_full) + 8 * s, 1);
             ptx::mbar_init(MLA_BAR(item_empty) + 8 * s, kItemConsumers);
@@ -360,81 +363,86 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
     Item it;
 
     // Registers: 384 threads x 168 at launch = 64,512; the softmax warps take
-    // 208 (a row's 128 scores stay in registers), the others 88:
-    // 256 x 208 + 128 x 88 = 64,512.
+    // 200 (a row's 128 scores stay in registers), the others 104:
+    // 256 x 200 + 128 x 104 = 64,512.
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == 8) {
             // ------------------------------------------------------- loads
             if (ptx::elect_one()) {
-                uint32_t blocks = 0, q_loads[2] = {0, 0}, raws = 0, raw_slots = 0;
-                bool ok = true;
-                // The next ring slot, once it is free; its load completes on
-                // ring_full, or on `raw` for the helper.
-                auto slot = [&](uint32_t raw, uint32_t* addr, uint32_t* bar) {
-                    const uint32_t s = blocks % kRing, turn = blocks / kRing;
-                    if (turn > 0 &&
-                        !wait(MLA_BAR(ring_empty) + 8 * s, (turn - 1) & 1, bars, p.status,
-                              kSiteRingFree))
-                        return false;
-                    *addr = sbase + uint32_t(kOffRing) + s * kBlock;
-                    *bar = raw != 0 ? raw : MLA_BAR(ring_full) + 8 * s;
-                    if (raw == 0) ptx::mbar_arrive_expect_tx(*bar, kBlock);
-                    raw_slots = (raw_slots & ~(1u << s)) | (raw != 0 ? 1u << s : 0u);
-                    ++blocks;
-                    return true;
+                // Ring blocks in order: step g's keys at 5g..5g+2, its values at
+                // 5g+3 and 5g+4. Eight blocks back from keys 1 and 2 lie the
+                // values of step g-2, from the values the keys of step g-1
+                // (and from key 0 those of step g-2, waited for by then).
+                uint32_t step = 0, q_loads[2] = {0, 0}, raws = 0;
+                bool ok = true, raw_last[2] = {false, false};
+                auto addr = [&](uint32_t i) {
+                    return sbase + uint32_t(kOffRing) + (i % kRing) * kBlock;
                 };
                 while (ok && items.next(bars, p.status, &it)) {
                     if (it.head < 0) break;
                     const int steps = max(it.step_hi[0], it.step_hi[1]);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (!ok || it.step_hi[t] <= it.step_lo) continue;
-                        if (q_loads[t] > 0)
-                            ok = wait(MLA_BAR(q_empty) + 8 * t, (q_loads[t] - 1) & 1, bars,
-                                      p.status, kSiteQFree);
-                        if (!ok) continue;
-                        const uint32_t bar = MLA_BAR(q_full) + 8 * t;
-                        ptx::mbar_arrive_expect_tx(bar, kQBlocks * kBlock);
-                        for (int c = 0; c < kQBlocks; ++c)
-                            ptx::tma_load_2d(sbase + uint32_t((t * kQBlocks + c) * kBlock), &map_q,
-                                             it.head * kQk + 64 * c, it.q_row + t * kTileRows, bar);
-                        ++q_loads[t];
-                    }
-                    uint32_t addr, bar;
-                    for (int j = it.step_lo; j < steps && ok; ++j) {
+                    for (int j = it.step_lo; j < steps && ok; ++j, ++step) {
                         const int row = it.k_row + j * kStep;
-                        for (int c = 0; c < 3 && ok; ++c) {
-                            ok = slot(0, &addr, &bar);
-                            if (!ok) break;
-                            if (c < 2)
-                                ptx::tma_load_2d(addr, &map_k, it.head * kKvHead + 64 * c, row, bar);
-                            else
-                                ptx::tma_load_2d(addr, &map_pe, 0, row, bar);
-                        }
-                        const uint32_t raw =
-                            j >= it.fix_from ? MLA_BAR(raw_full) + 8 * (raws & 1) : 0;
-                        for (int c = 0; c < 2 && ok; ++c) {
-                            ok = slot(raw, &addr, &bar);
-                            if (!ok) break;
-                            // (two steps back on this barrier: their slots were
-                            // released, so that phase is complete)
-                            if (raw != 0 && c == 0) {
-                                ptx::mbar_arrive_expect_tx(raw, 2 * kBlock);
-                                ++raws;
+                        const uint32_t bar = MLA_BAR(k_full) + 8 * (step & 1);
+                        ptx::mbar_arrive_expect_tx(bar, 3 * kBlock);
+                        ptx::tma_load_2d(addr(5 * step), &map_k, it.head * kKvHead, row, bar);
+                        if (step >= 2)
+                            ok = wait(MLA_BAR(v_empty), step & 1, bars, p.status, kSiteRingFree);
+                        // (after an abort the phase's other bytes still come, so
+                        // that the drain below ends)
+                        ptx::tma_load_2d(addr(5 * step + (ok ? 1 : 0)), &map_k,
+                                         it.head * kKvHead + 64, row, bar);
+                        ptx::tma_load_2d(addr(5 * step + (ok ? 2 : 0)), &map_pe, 0, row, bar);
+                        if (j == it.step_lo) {
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                if (!ok || it.step_hi[t] <= it.step_lo) continue;
+                                if (q_loads[t] > 0)
+                                    ok = wait(MLA_BAR(q_empty) + 8 * t, (q_loads[t] - 1) & 1, bars,
+                                              p.status, kSiteQFree);
+                                if (!ok) continue;
+                                const uint32_t q_bar = MLA_BAR(q_full) + 8 * t;
+                                ptx::mbar_arrive_expect_tx(q_bar, kQBlocks * kBlock);
+                                for (int c = 0; c < kQBlocks; ++c)
+                                    ptx::tma_load_2d(sbase + uint32_t((t * kQBlocks + c) * kBlock),
+                                                     &map_q, it.head * kQk + 64 * c,
+                                                     it.q_row + t * kTileRows, q_bar);
+                                ++q_loads[t];
                             }
+                        }
+                        if (step >= 1)
+                            ok = ok && wait(MLA_BAR(k_empty), (step - 1) & 1, bars, p.status,
+                                            kSiteRingFree);
+                        if (!ok) {
+                            ++step;
+                            raw_last[(step - 1) & 1] = true;   // no values were asked for
+                            break;
+                        }
+                        const bool raw = j >= it.fix_from;
+                        const uint32_t v_bar = raw ? MLA_BAR(raw_full) + 8 * (raws & 1)
+                                                   : MLA_BAR(v_full) + 8 * (step & 1);
+                        raw_last[step & 1] = raw;
+                        raws += raw ? 1 : 0;
+                        ptx::mbar_arrive_expect_tx(v_bar, 2 * kBlock);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
                             const int x = it.head * kKvHead + 128, y = row + 64 * c;
-                            ptx::tma_load_2d(addr, &map_v, x, y, bar);
-                            ptx::tma_load_2d(addr + 8192, &map_v, x + 64, y, bar);
+                            const uint32_t dst = addr(5 * step + 3 + c);
+                            ptx::tma_load_2d(dst, &map_v, x, y, v_bar);
+                            ptx::tma_load_2d(dst + 8192, &map_v, x + 64, y, v_bar);
                         }
                     }
                     items.release();
                 }
                 // Loads still in flight (after an abort) land before the CTA exits.
-                for (uint32_t i = blocks > kRing ? blocks - kRing : 0; i < blocks; ++i)
-                    if (!(raw_slots >> (i % kRing) & 1))
-                        wait(MLA_BAR(ring_full) + 8 * (i % kRing), (i / kRing) & 1, bars, p.status,
+                for (uint32_t g = step > 2 ? step - 2 : 0; g < step; ++g) {
+                    wait(MLA_BAR(k_full) + 8 * (g & 1), (g >> 1) & 1, bars, p.status, kSiteDrain,
+                         true);
+                    if (!raw_last[g & 1])
+                        wait(MLA_BAR(v_full) + 8 * (g & 1), (g >> 1) & 1, bars, p.status,
                              kSiteDrain, true);
+                }
                 for (uint32_t i = raws > 2 ? raws - 2 : 0; i < raws; ++i)
                     wait(MLA_BAR(raw_full) + 8 * (i & 1), (i >> 1) & 1, bars, p.status, kSiteDrain,
                          true);
@@ -450,88 +458,97 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
             if (ptx::elect_one()) {
                 constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kStep, false);
                 constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(kV, true);
-                uint32_t block = 0;            // first ring block of the step's keys
+                // An operand's descriptor: the layout's constant bits and the
+                // block's address. (A thread that issues MMAs waits for the
+                // tensor pipe to take each; what it does in between is time
+                // that the pipe may run dry, so descriptors cost two adds,
+                // barriers are tested before they are slept on, and a step has
+                // one release for its keys and one for its values.)
+                const uint64_t desc_k = ptx::desc_sw128(0, 16, 1024);
+                const uint64_t desc_v = ptx::desc_sw128(0, 8192, 1024);
+                uint32_t step = 0;
                 uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
                 bool ok = true;
-                auto ring_wait = [&](uint32_t i) {
-                    return wait(MLA_BAR(ring_full) + 8 * (i % kRing), (i / kRing) & 1, bars,
-                                p.status, kSiteRing);
+                auto ring = [&](uint32_t i) {      // address >> 4
+                    return (sbase + uint32_t(kOffRing) + (i % kRing) * kBlock) >> 4;
                 };
-                auto ring_addr = [&](uint32_t i) {
-                    return sbase + uint32_t(kOffRing) + (i % kRing) * kBlock;
-                };
-                // Scores of tile t for the step whose keys start at ring block kb.
-                auto scores = [&](int t, uint32_t kb) {
+                // Scores of tile t for step g.
+                auto scores = [&](int t, uint32_t g) {
 #pragma unroll
                     for (int c = 0; c < 3; ++c) {
-                        if (!ring_wait(kb + c)) return false;
-                        ptx::tc_fence_after();
-                        const uint32_t a = sbase + uint32_t((t * kQBlocks + c) * kBlock);
-                        const uint32_t b = ring_addr(kb + c);
-                        ptx::mma4_ss(tmem + kTmemS + 128 * t, ptx::desc_sw128(a, 16, 1024),
-                                     ptx::desc_sw128(a + 32, 16, 1024),
-                                     ptx::desc_sw128(a + 64, 16, 1024),
-                                     ptx::desc_sw128(a + 96, 16, 1024),
-                                     ptx::desc_sw128(b, 16, 1024),
-                                     ptx::desc_sw128(b + 32, 16, 1024),
-                                     ptx::desc_sw128(b + 64, 16, 1024),
-                                     ptx::desc_sw128(b + 96, 16, 1024), idesc_s, c > 0 ? 1u : 0u);
+                        const uint64_t a =
+                            desc_k + ((sbase + uint32_t((t * kQBlocks + c) * kBlock)) >> 4);
+                        const uint64_t b = desc_k + ring(5 * g + c);
+                        ptx::mma4_ss(tmem + kTmemS + 128 * t, a, a + 2, a + 4, a + 6, b, b + 2,
+                                     b + 4, b + 6, idesc_s, c > 0 ? 1u : 0u);
                     }
                     ptx::mma_commit(MLA_BAR(s_full) + 8 * t);
-                    return true;
                 };
-                // O of tile t += P V, V at ring blocks vb, vb + 1.
-                auto values = [&](int t, uint32_t vb, bool first) {
-                    if (!wait(MLA_BAR(p_ready) + 8 * t, p_uses[t] & 1, bars, p.status, kSiteP))
-                        return false;
-                    ++p_uses[t];
+                // O of tile t += P V of step g.
+                auto values = [&](int t, uint32_t g, bool first) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        if (!ring_wait(vb + c)) return false;
-                        ptx::tc_fence_after();
                         const uint32_t a = tmem + kTmemS + 128 * t + 32 * c;
-                        const uint32_t b = ring_addr(vb + c);
-                        ptx::mma4_ts(tmem + kTmemO + 128 * t, a, a + 8, a + 16, a + 24,
-                                     ptx::desc_sw128(b, 8192, 1024),
-                                     ptx::desc_sw128(b + 2048, 8192, 1024),
-                                     ptx::desc_sw128(b + 4096, 8192, 1024),
-                                     ptx::desc_sw128(b + 6144, 8192, 1024), idesc_o,
-                                     c > 0 || !first ? 1u : 0u);
+                        const uint64_t b = desc_v + ring(5 * g + 3 + c);
+                        ptx::mma4_ts(tmem + kTmemO + 128 * t, a, a + 8, a + 16, a + 24, b, b + 128,
+                                     b + 256, b + 384, idesc_o, c > 0 || !first ? 1u : 0u);
                     }
                     ptx::mma_commit(MLA_BAR(pv_done) + 8 * t);
-                    return true;
-                };
-                auto release = [&](uint32_t i, int n) {
-                    for (int c = 0; c < n; ++c)
-                        ptx::mma_commit(MLA_BAR(ring_empty) + 8 * ((i + c) % kRing));
                 };
                 while (ok && items.next(bars, p.status, &it)) {
                     if (it.head < 0) break;
                     const int steps = max(it.step_hi[0], it.step_hi[1]);
-                    // First the scores of the first step; then, per step, P.V
-                    // of the step and the scores of the next, tile after tile.
-                    for (int j = it.step_lo - 1; j < steps && ok; ++j) {
-                        const uint32_t vb = block + 3;
-                        const uint32_t kb = j < it.step_lo ? block : block + 5;
+                    if (steps > it.step_lo) {
+                        // The scores of the first step.
+                        ok = wait(MLA_BAR(k_full) + 8 * (step & 1), (step >> 1) & 1, bars, p.status,
+                                  kSiteRing);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!ok || it.step_hi[t] <= it.step_lo) continue;
+                            ok = wait(MLA_BAR(q_full) + 8 * t, q_uses[t] & 1, bars, p.status,
+                                      kSiteQ);
+                            ++q_uses[t];
+                            if (!ok) continue;
+                            ptx::tc_fence_after();
+                            scores(t, step);
+                            if (it.step_hi[t] == it.step_lo + 1)
+                                ptx::mma_commit(MLA_BAR(q_empty) + 8 * t);
+                        }
+                        if (ok) ptx::mma_commit(MLA_BAR(k_empty));
+                    }
+                    // Per step: P.V of the step and the scores of the next,
+                    // tile after tile.
+                    for (int j = it.step_lo; j < steps && ok; ++j, ++step) {
+                        bool have_v = false, have_k = false;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (!ok) continue;
-                            if (j >= it.step_lo && j < it.step_hi[t])
-                                ok = values(t, vb, j == it.step_lo);
-                            if (j >= it.step_lo && t == 1) release(vb, 2);
-                            if (ok && j + 1 < it.step_hi[t]) {
-                                if (j < it.step_lo) {
-                                    ok = wait(MLA_BAR(q_full) + 8 * t, q_uses[t] & 1, bars,
-                                              p.status, kSiteQ);
-                                    ++q_uses[t];
-                                }
-                                ok = ok && scores(t, kb);
-                                if (ok && j + 2 == it.step_hi[t])
+                            if (j < it.step_hi[t]) {
+                                ok = wait(MLA_BAR(p_ready) + 8 * t, p_uses[t] & 1, bars, p.status,
+                                          kSiteP);
+                                if (!have_v)
+                                    ok = ok && wait(MLA_BAR(v_full) + 8 * (step & 1),
+                                                    (step >> 1) & 1, bars, p.status, kSiteRing);
+                                if (!ok) continue;
+                                have_v = true;
+                                ++p_uses[t];
+                                ptx::tc_fence_after();
+                                values(t, step, j == it.step_lo);
+                            }
+                            if (t == 1) ptx::mma_commit(MLA_BAR(v_empty));
+                            if (j + 1 < it.step_hi[t]) {
+                                if (!have_k)
+                                    ok = wait(MLA_BAR(k_full) + 8 * ((step + 1) & 1),
+                                              ((step + 1) >> 1) & 1, bars, p.status, kSiteRing);
+                                if (!ok) continue;
+                                have_k = true;
+                                ptx::tc_fence_after();
+                                scores(t, step + 1);
+                                if (j + 2 == it.step_hi[t])
                                     ptx::mma_commit(MLA_BAR(q_empty) + 8 * t);
                             }
                         }
-                        if (ok && j + 1 < steps) release(kb, 3);
-                        if (j >= it.step_lo) block += 5;
+                        if (ok && j + 1 < steps) ptx::mma_commit(MLA_BAR(k_empty));
                     }
                     items.release();
                 }
@@ -542,15 +559,14 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
             __syncwarp();
         } else if (warp == 10) {
             // ------------------------------------------------------ helper
-            uint32_t block = 0, raws = 0;
+            uint32_t step = 0, raws = 0;
             bool ok = true;
             while (ok) {
                 ok = __all_sync(0xffffffffu, items.next(bars, p.status, &it));
                 if (!ok || it.head < 0) break;
                 const int steps = max(it.step_hi[0], it.step_hi[1]);
-                if (it.fix_from > it.step_lo)
-                    block += 5 * uint32_t(min(it.fix_from, steps) - it.step_lo);
-                for (int j = it.fix_from; j < steps; ++j, block += 5, ++raws) {
+                step += uint32_t(min(it.fix_from, steps) - it.step_lo);
+                for (int j = it.fix_from; j < steps; ++j, ++step, ++raws) {
                     ok = __all_sync(0xffffffffu,
                                     wait(MLA_BAR(raw_full) + 8 * (raws & 1), (raws >> 1) & 1, bars,
                                          p.status, kSiteRaw));
@@ -560,7 +576,7 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                     for (int c = 0; c < 2; ++c) {
                         // Two 64 x 64 boxes of 128-byte rows; a row is 8 pieces of 16 bytes.
                         uint4* v = reinterpret_cast<uint4*>(
-                            smem + kOffRing + ((block + 3 + c) % kRing) * kBlock);
+                            smem + kOffRing + ((5 * step + 3 + c) % kRing) * kBlock);
                         const bool cut = end < 64 * (c + 1);
 #pragma unroll 1
                         for (int k0 = lane; k0 < kBlock / 16; k0 += 8 * 32) {
@@ -585,7 +601,7 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                     if (__any_sync(0xffffffffu, bad)) {
                         for (int c = 0; c < 2; ++c) {
                             uint32_t* v = reinterpret_cast<uint32_t*>(
-                                smem + kOffRing + ((block + 3 + c) % kRing) * kBlock);
+                                smem + kOffRing + ((5 * step + 3 + c) % kRing) * kBlock);
                             for (int k = lane; k < kBlock / 4; k += 32) {
                                 uint32_t x = v[k];
                                 if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
@@ -597,8 +613,7 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane < 2)
-                        ptx::mbar_arrive(MLA_BAR(ring_full) + 8 * ((block + 3 + lane) % kRing));
+                    if (lane == 0) ptx::mbar_arrive(MLA_BAR(v_full) + 8 * (step & 1));
                 }
                 if (!ok) break;
                 __syncwarp();
@@ -645,7 +660,7 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
         }
     } else {
         // ------------------------------------------------ softmax, epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int t = warp >> 2;
         const int row = (warp & 3) * 32 + lane;            // of the tile, = TMEM lane
         const uint32_t ts = tmem + kTmemS + 128 * t + (uint32_t((warp & 3) * 32) << 16);
@@ -737,7 +752,8 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                 unpack_f32(add_f32x2(part[0], part[1]), &part_a, &part_b);
                 sum += part_a + part_b;
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(MLA_BAR(p_ready) + 8 * t);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(MLA_BAR(p_ready) + 8 * t);
             }
             if (!ok) break;
             // Epilogue.
