@@ -505,7 +505,7 @@ int mla_decode_v_up_proj(const mla_decode_plan_t* plan, const void* q, const voi
  *   latent_cache   device, bf16 [num_blocks, 64, 576] (mla_expand_kv), or
  *                  E4M3 codes with entry = k_scale * e4m3(code), k_scale
  *                  finite and > 0 (mla_expand_kv_fp8: k_scale multiplies the
- *                  fp32 sums). 16-byte aligned.
+ *                  fp32 sums). 32-byte aligned.
  *   block_table    device, int32 [batch, max_blocks_per_seq].
  *   first_token    device, int32 [batch], or NULL (all 0).
  *   cu_seqlens_k   device, int32 [batch + 1], not decreasing, from 0 on; rows of

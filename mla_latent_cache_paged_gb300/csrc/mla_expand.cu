@@ -23,6 +23,13 @@
 // run kSkew chunks behind the first's, so one accumulator is read out while
 // the tensor pipe works on the other.
 //
+// What bounds it now: the shared-memory pipe. Per weight chunk and 256 rows the
+// MMAs read 48 KB (the chunk twice, the second half's rows once) and the loads
+// write 16 KB, 512 clocks at 128 bytes a clock and as many as the MMAs take;
+// the result's stores pass through the same pipe. 7,865 tokens, N = 128: 204 us
+// (1,290 TFLOP/s, 2.5 TB/s written), 165 us with the stores left out; 500
+// tokens, N = 16: 14 us (bf16 cache), 15 us (fp8).
+//
 // Work: the (token tile, head, half) items in that order, cut into one
 // contiguous range per CTA, so each CTA gathers one or two token tiles.
 // Warps: 0 = weight loads (TMA), 1 = MMAs, 2-5 and 6-9 = gather and epilogue
@@ -68,7 +75,7 @@ struct Bars {
     uint64_t empty[kStages];
     uint64_t a_ready[2];      // 128 arrivals: this half's rows are staged
     uint64_t acc_full[2];
-    uint64_t acc_empty[2];    // 128 arrivals: accumulator read out
+    uint64_t acc_empty[2];    // 4 warps: accumulator read out
     uint64_t drain;
     uint32_t tmem_base;
     int32_t abort;
@@ -149,23 +156,37 @@ __device__ __forceinline__ uint32_t widen2(uint32_t codes16) {
     return uint32_t(f32_to_bf16_bits_rn(f.x)) | (uint32_t(f32_to_bf16_bits_rn(f.y)) << 16);
 }
 
-// 16 entries (8 words of bf16 pairs) from column 16 * i of a row; zeros
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+// 32 bytes (32-byte aligned).
+__device__ __forceinline__ void load32(const char* p, uint32_t* r) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+}
+
+// 64 entries (32 words of bf16 pairs) from column 64 g of a row; zeros
 // without one.
 template <int kEntryBytes>
-__device__ __forceinline__ void load16(const char* entry, int i, uint32_t* w) {
-    if (entry == nullptr) {
+__device__ __forceinline__ void load64(const char* entry, int g, uint32_t* w) {
+    uint32_t c[16 * kEntryBytes];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = 0;
-    } else if constexpr (kEntryBytes == 2) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(entry) + 2 * i);
-        const uint4 b = __ldg(reinterpret_cast<const uint4*>(entry) + 2 * i + 1);
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    for (int k = 0; k < 16 * kEntryBytes; ++k) c[k] = 0;
+    if (entry != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 2 * kEntryBytes; ++k)
+            load32(entry + g * 64 * kEntryBytes + k * 32, c + 8 * k);
+    }
+    if constexpr (kEntryBytes == 2) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) w[k] = c[k];
     } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(entry) + i);
-        const uint32_t c[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 16; ++k) {
             w[2 * k] = widen2(c[k] & 0xffffu);
             w[2 * k + 1] = widen2(c[k] >> 16);
         }
@@ -204,7 +225,7 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
         for (int h = 0; h < 2; ++h) {
             ptx::mbar_init(a_ready(h), 128);
             ptx::mbar_init(acc_full(h), 1);
-            ptx::mbar_init(acc_empty(h), 128);
+            ptx::mbar_init(acc_empty(h), 4);
         }
         ptx::mbar_init(drain, 1);
         bars->abort = 0;
@@ -261,63 +282,73 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
         if (ptx::elect_one()) {
             constexpr uint32_t idesc_k = ptx::idesc_bf16_f32(kHalf, false);
             constexpr uint32_t idesc_v = ptx::idesc_bf16_f32(kHalf, true);
+            // (The thread that issues MMAs waits for the tensor pipe to take
+            // each; what it does in between should be little. A descriptor is
+            // the layout's constant bits plus the address, and only the first
+            // half waits for a weight chunk.)
+            const uint64_t desc_k = ptx::desc_sw128(0, 16, 1024);
+            const uint64_t desc_v = ptx::desc_sw128(0, 8192, 1024);
+            const uint32_t ring = (sbase + uint32_t(kOffRing)) >> 4;
+            const uint64_t a_base = desc_k + ((sbase + uint32_t(kOffA)) >> 4);
             bool ok = true;
-            uint32_t base = 0;             // chunks of the segments before this one
-            uint32_t tiles[2] = {0, 0};    // column tiles begun per half
-            uint32_t seg[2] = {0, 0};      // token tiles begun per half
+            uint32_t slot0 = 0, slot1 = 0, turn = 0;   // ring slot per half, parity of the first's
+            uint32_t tiles[2] = {0, 0};                // column tiles begun per half
+            uint32_t seg[2] = {0, 0};                  // token tiles begun per half
             for (int64_t it = begin; it < end && ok;) {
                 const int64_t e = tile_end(it);
                 const bool two = two_halves(it);
-                const int chunks = int(e - it) * kChunks;
-                const int steps = chunks + (two ? kSkew : 0);
-                for (int step = 0; step < steps && ok; ++step) {
+                ok = wait(a_ready(0), seg[0]++ & 1, bars, p.status, kSiteA);
+                if (two) ok = ok && wait(a_ready(1), seg[1]++ & 1, bars, p.status, kSiteA);
+                for (; it < e && ok; ++it) {
+                    // W_UK_T: 16 k = 32 bytes per step; W_UV: 16 k-rows = 2 KB
+                    // per step, its two 64-column blocks 8 KB apart.
+                    const bool is_v = (it & 1) != 0;
+                    const uint64_t w_base = (is_v ? desc_v : desc_k) + ring;
+                    const uint32_t st = is_v ? 128 : 2;
+                    const uint32_t idesc = is_v ? idesc_v : idesc_k;
+                    // First half's chunk k, second half's chunk k - kSkew; the
+                    // tile's last chunks of the second half go out before the
+                    // next tile's first of the first half, so that three
+                    // chunks' MMAs cover the readout of each accumulator.
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int ch = step - (h == 0 ? 0 : kSkew);
-                        if (ch < 0 || ch >= chunks || (h == 1 && !two)) continue;
-                        const int c = ch % kChunks;
-                        const uint32_t g = base + uint32_t(ch);
-                        const int s = int(g % kStages);
-                        if (ch == 0)
-                            ok = ok && wait(a_ready(h), seg[h]++ & 1, bars, p.status, kSiteA);
-                        if (c == 0) {
-                            if (tiles[h] > 0)
-                                ok = ok && wait(acc_empty(h), (tiles[h] - 1) & 1, bars, p.status,
-                                                kSiteAccEmpty);
-                            ++tiles[h];
+                    for (int k = 0; k < kChunks + kSkew; ++k) {
+                        if (k < kChunks) {
+                            if (k == 0 && tiles[0]++ > 0)
+                                ok = wait(acc_empty(0), tiles[0] & 1, bars, p.status,
+                                          kSiteAccEmpty);
+                            ok = ok && wait(full(slot0), turn, bars, p.status, kSiteFull);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            const uint64_t w = w_base + slot0 * (kStageBytes / 16);
+                            const uint32_t a = tmem + kTmemA + uint32_t(k * 32);
+                            ptx::mma4_ts(tmem + kTmemAcc, a, a + 8, a + 16, a + 24, w, w + st,
+                                         w + 2 * st, w + 3 * st, idesc, k > 0 ? 1u : 0u);
+                            if (!two) ptx::mma_commit(empty(slot0));
+                            if (k == kChunks - 1) ptx::mma_commit(acc_full(0));
+                            if (++slot0 == kStages) {
+                                slot0 = 0;
+                                turn ^= 1;
+                            }
                         }
-                        ok = ok && wait(full(s), (g / kStages) & 1, bars, p.status,
-                                        kSiteFull);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        const bool is_v = ((int(it & 1) + ch / kChunks) & 1) != 0;
-                        const uint32_t w = sbase + uint32_t(kOffRing + s * kStageBytes);
-                        // W_UK_T: 16 k = 32 bytes per step; W_UV: 16 k-rows =
-                        // 2 KB per step, its two 64-column blocks 8 KB apart.
-                        const uint32_t st = is_v ? 2048 : 32, lbo = is_v ? 8192 : 16;
-                        const uint64_t d0 = ptx::desc_sw128(w, lbo, 1024);
-                        const uint64_t d1 = ptx::desc_sw128(w + st, lbo, 1024);
-                        const uint64_t d2 = ptx::desc_sw128(w + 2 * st, lbo, 1024);
-                        const uint64_t d3 = ptx::desc_sw128(w + 3 * st, lbo, 1024);
-                        const uint32_t acc = tmem + kTmemAcc + uint32_t(h * kHalf);
-                        if (h == 0) {
-                            const uint32_t a = tmem + kTmemA + uint32_t(c * 32);
-                            ptx::mma4_ts(acc, a, a + 8, a + 16, a + 24, d0, d1, d2, d3,
-                                         is_v ? idesc_v : idesc_k, c > 0 ? 1u : 0u);
-                        } else {
-                            const uint32_t a = sbase + uint32_t(kOffA + c * 16384);
-                            ptx::mma4_ss(acc, ptx::desc_sw128(a, 16, 1024),
-                                         ptx::desc_sw128(a + 32, 16, 1024),
-                                         ptx::desc_sw128(a + 64, 16, 1024),
-                                         ptx::desc_sw128(a + 96, 16, 1024), d0, d1, d2, d3,
-                                         is_v ? idesc_v : idesc_k, c > 0 ? 1u : 0u);
+                        if (two && k >= kSkew) {
+                            if (k == kSkew && tiles[1]++ > 0) {
+                                ok = wait(acc_empty(1), tiles[1] & 1, bars, p.status,
+                                          kSiteAccEmpty);
+                                if (!ok) break;
+                                ptx::tc_fence_after();
+                            }
+                            const uint64_t w = w_base + slot1 * (kStageBytes / 16);
+                            const uint64_t a = a_base + uint32_t((k - kSkew) * 1024);
+                            ptx::mma4_ss(tmem + kTmemAcc + uint32_t(kHalf), a, a + 2, a + 4, a + 6,
+                                         w, w + st, w + 2 * st, w + 3 * st, idesc,
+                                         k > kSkew ? 1u : 0u);
+                            ptx::mma_commit(empty(slot1));
+                            if (k == kChunks + kSkew - 1) ptx::mma_commit(acc_full(1));
+                            if (++slot1 == kStages) slot1 = 0;
                         }
-                        if (h == 1 || !two) ptx::mma_commit(empty(s));
-                        if (c == kChunks - 1) ptx::mma_commit(acc_full(h));
                     }
                 }
-                base += uint32_t(chunks);
-                it = e;
+                if (!two) slot1 = slot0;
             }
             // Every MMA issued above has completed before TMEM is freed.
             ptx::mma_commit(drain);
@@ -327,7 +358,8 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
     } else {
         const int h = warp >= 6 ? 1 : 0;
         const int lanes = (warp & 3) * 32;                 // TMEM lanes this warp reads
-        const int r = lanes + (threadIdx.x & 31);          // row of the half
+        const int lane = threadIdx.x & 31;
+        const int r = lanes + lane;                        // row of the half
         const uint32_t lane_addr = uint32_t(lanes) << 16;
         bool ok = true;
         uint32_t done = 0;
@@ -341,30 +373,60 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
             const RowSource src = find_row<kEntryBytes>(p, t < INT_MAX ? int(t) : INT_MAX);
             __syncwarp();
             if (h == 0) {
+                // (TMEM takes a row per lane; whole 32-byte sectors at a time.)
 #pragma unroll 1
                 for (int g = 0; g < kLkv / 64; ++g) {
                     uint32_t w[32];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) load16<kEntryBytes>(src.entry, g * 4 + k, w + 8 * k);
+                    load64<kEntryBytes>(src.entry, g, w);
                     __syncwarp();
                     ptx::tmem_st32(tmem + kTmemA + lane_addr + uint32_t(g * 32), w);
                 }
                 ptx::tc_fence_before();
             } else {
-#pragma unroll 4
-                for (int k = 0; k < kLkv / 16; ++k) {
-                    uint32_t w[8];
-                    load16<kEntryBytes>(src.entry, k, w);
-                    // columns 16k..: chunk k / 4, 16-byte pieces 2 (k % 4) and the next
-                    const uint32_t row = sbase + uint32_t(kOffA + (k >> 2) * 16384 + r * 128);
-                    const int pc = 2 * (k & 3);
+                // A warp takes its 32 rows one after the other, eight in
+                // flight, each lane a piece of the row: a lane per row reads
+                // 32 lines a load (it took 20,000 clocks a token tile). Column
+                // 8 j is 16-byte piece j % 8 of chunk j / 8.
+                constexpr int kLoads = kEntryBytes;     // 16-byte loads per lane and row
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32; i0 += 8) {
+                    uint4 v[8][kLoads];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         row + uint32_t(((pc + q) ^ (r & 7)) * 16)),
-                                     "r"(w[4 * q]), "r"(w[4 * q + 1]), "r"(w[4 * q + 2]),
-                                     "r"(w[4 * q + 3])
-                                     : "memory");
+                    for (int i = 0; i < 8; ++i) {
+                        const uint64_t entry = __shfl_sync(
+                            0xffffffffu, reinterpret_cast<uint64_t>(src.entry), i0 + i);
+#pragma unroll
+                        for (int k = 0; k < kLoads; ++k) {
+                            v[i][k] = make_uint4(0, 0, 0, 0);
+                            if (entry != 0)
+                                v[i][k] = __ldg(reinterpret_cast<const uint4*>(entry) + k * 32 + lane);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int q = lanes + i0 + i;
+                        const uint32_t row = sbase + uint32_t(kOffA + q * 128);
+                        auto put = [&](int j, const uint32_t* w) {
+                            st_shared16(row + uint32_t((j >> 3) * 16384 + (((j & 7) ^ (q & 7)) * 16)), w);
+                        };
+                        if constexpr (kEntryBytes == 2) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t w[4] = {v[i][k].x, v[i][k].y, v[i][k].z, v[i][k].w};
+                                put(k * 32 + lane, w);
+                            }
+                        } else {
+                            const uint32_t c[4] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w};
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                w[2 * k] = widen2(c[k] & 0xffffu);
+                                w[2 * k + 1] = widen2(c[k] >> 16);
+                            }
+                            put(2 * lane, w);
+                            put(2 * lane + 1, w + 4);
+                        }
+                    }
                 }
                 ptx::fence_proxy_async_smem();
             }
@@ -372,19 +434,17 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
             // The CTA with a token tile's first item writes its rows' k_pe.
             if (it % per_tile == 0 && src.exists) {
                 uint4* dst = reinterpret_cast<uint4*>(p.k_pe + t * kRope);
+                uint32_t w[32];
+                load64<kEntryBytes>(src.entry, kLkv / 64, w);
+                if constexpr (kEntryBytes == 1) {
 #pragma unroll
-                for (int k = 0; k < kRope / 16; ++k) {
-                    uint32_t w[8];
-                    load16<kEntryBytes>(src.entry, kLkv / 16 + k, w);
-                    if constexpr (kEntryBytes == 1) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)   // one rounding of scale * code
-                            w[i] = pack2(p.scale * bf16_bits_to_f32(w[i] & 0xffffu),
-                                         p.scale * bf16_bits_to_f32(w[i] >> 16));
-                    }
-                    dst[2 * k] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[2 * k + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    for (int i = 0; i < 32; ++i)   // one rounding of scale * code
+                        w[i] = pack2(p.scale * bf16_bits_to_f32(w[i] & 0xffffu),
+                                     p.scale * bf16_bits_to_f32(w[i] >> 16));
                 }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
             }
             int item = int(it % per_tile);
             for (; it < e; ++it, ++item) {
@@ -394,23 +454,27 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
                 if (!ok) break;
                 ++done;
                 ptx::tc_fence_after();
+                uint32_t lo[64], hi[64];
+                ptx::tmem_ld64(tmem + kTmemAcc + lane_addr + uint32_t(h * kHalf), lo);
+                ptx::tmem_ld64(tmem + kTmemAcc + lane_addr + uint32_t(h * kHalf + 64), hi);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(acc_empty(h));
                 uint32_t o[64];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t v[32];
-                    ptx::tmem_ld32(tmem + kTmemAcc + lane_addr + uint32_t(h * kHalf + g * 32), v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
-                        if constexpr (kEntryBytes == 1) {
-                            a *= p.scale;
-                            b *= p.scale;
-                        }
-                        o[g * 16 + i] = pack2(a, b);
+                for (int i = 0; i < 64; ++i) {
+                    float a = __uint_as_float(i < 32 ? lo[2 * i] : hi[2 * i - 64]);
+                    float b = __uint_as_float(i < 32 ? lo[2 * i + 1] : hi[2 * i - 63]);
+                    if constexpr (kEntryBytes == 1) {
+                        a *= p.scale;
+                        b *= p.scale;
                     }
+                    o[i] = pack2(a, b);
                 }
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(acc_empty(h));
+                // 32 bytes of a row per lane and store. (Swapping pieces between
+                // lanes so that a store fills whole 128-byte lines was 18%
+                // slower at N = 128: shuffles share the shared-memory pipe
+                // that feeds the MMAs, which is this kernel's bound.)
                 if (src.exists) {
                     uint16_t* dst = p.kv + (t * p.heads + (item >> 1)) * 256 + (item & 1) * kHalf;
 #pragma unroll
@@ -421,6 +485,7 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
                         ptx::st_global_v8(dst + i * 16, w);
                     }
                 }
+                __syncwarp();
             }
         }
     }
@@ -462,7 +527,7 @@ int expand(const void* cache, int entry_bytes, float scale, int64_t num_blocks,
     if (batch == 0 || total_k == 0) return MLA_OK;
     if (!cache || !block_table || !cu_seqlens_k || !w_uk_t || !w_uv || !kv || !k_pe)
         return MLA_ERR_INVALID_ARG;
-    if (!aligned(cache, 16) || !aligned(w_uk_t, 16) || !aligned(w_uv, 16) || !aligned(kv, 32) ||
+    if (!aligned(cache, 32) || !aligned(w_uk_t, 16) || !aligned(w_uv, 16) || !aligned(kv, 32) ||
         !aligned(k_pe, 16) || !aligned(block_table, 4) || !aligned(cu_seqlens_k, 4) ||
         (first_token && !aligned(first_token, 4)))
         return MLA_ERR_INVALID_ARG;

@@ -35,6 +35,7 @@ def _expand(lib, fp8=False, **kw):
     (dict(mb=0), binding.MLA_ERR_INVALID_ARG),
     (dict(cache=None), binding.MLA_ERR_INVALID_ARG),
     (dict(cache=X + 8), binding.MLA_ERR_INVALID_ARG),
+    (dict(cache=X + 16), binding.MLA_ERR_INVALID_ARG),
     (dict(kv=X + 16), binding.MLA_ERR_INVALID_ARG),
     (dict(pe=X + 4), binding.MLA_ERR_INVALID_ARG),
     (dict(uk=X + 2), binding.MLA_ERR_INVALID_ARG),
