@@ -632,7 +632,7 @@ int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const void* kv, c
  *                       bytes (mla_cache_free: a status header of 8192 bytes
  *                       is enough). Calls that share one must not overlap.
  * Device-detected errors go to its status word (mla_read_error). Each call is
- * two or three launches on `stream`, no synchronisation, and can be captured.
+ * one cooperative launch on `stream`, no synchronisation, and can be captured.
  *
  * mla_cache_workspace_bytes -- host only; 0 for arguments out of range.
  */

@@ -9,23 +9,24 @@
 //   fork     child c: shares pages 0..F-1 of its parent (F = S / 64 whole
 //            pages of the S shared tokens), copies the S % 64 rows of page F
 //            into a page of its own in every layer, and gets fresh pages up
-//            to ceil(L / 64).   count pass -> assign pass -> share + copy pass
+//            to ceil(L / 64).   count | assign | share + copy
 //   free     counts - 1 for each entry of the named rows.
 //   compact  M live pages. The k-th live page with id >= M goes to the k-th
 //            free id below M: the fewest moves that leave the live pages in
 //            [0, M), and no destination is another move's source, so the
-//            copies run in any order.   count pass -> list pass -> move pass
+//            copies run in any order.   count | list | move
 //
-// The passes are separate launches chained by programmatic dependent launch:
-// a grid-wide prefix sum needs all counts before the first rank. Each CTA of
-// the second pass sums the chunk counts below its own itself (num_blocks /
-// 1024 values), which costs less than a third launch for a scan.
-#include <cuda_runtime.h>
-
+// A grid-wide prefix sum needs all counts before the first rank, and the
+// copies need the ranks. Each operation is one cooperative launch with a
+// barrier (|) between its passes. Each CTA of the second pass sums the chunk
+// counts below its own itself (num_blocks / 1024 values). The grid is at most
+// kCtasPerSm CTAs per SM (all resident, as the barrier needs), and no more
+// than the work has use for.
 #include <climits>
 #include <cstdint>
 
 #include "mla_device.cuh"
+#include "tc_ptx.cuh"
 
 namespace mla {
 namespace {
@@ -37,12 +38,49 @@ constexpr int kChunk = kPageThreads * kChunkIters;   // pages whose counts one C
 constexpr int kMaxChildren = 8192;                   // their page offsets fit shared memory
 constexpr int kPieceBytes = 8192;                    // bytes of a page that one CTA copies at once
 
-__device__ __forceinline__ void grid_wait() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void grid_launch_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+constexpr int kCtasPerSm = 4;                        // at most 64 registers a thread
+constexpr uint64_t kBarrierTimeoutNs = 1000000000ull;
+constexpr int32_t kSiteGrid = 90;
+
+// Barriers of a cooperative grid on a word that is 0 between calls;
+// arrive_last ends a CTA's part, and the last one of the grid clears the word.
+// (After an expired wait the word stays as it is, as the workspace's other
+// counters do: the workspace is initialised again.)
+struct GridBarrier {
+    uint32_t* word;
+    int32_t* status;
+    uint32_t passed = 0;
+
+    __device__ __forceinline__ bool wait(int* ok) {
+        __syncthreads();
+        ++passed;
+        if (threadIdx.x == 0) {
+            __threadfence();
+            *ok = 1;
+            atomicAdd(word, 1u);
+            const uint64_t t0 = ptx::globaltimer();
+            while (arrivals() < passed * gridDim.x) {
+                if (ptx::globaltimer() - t0 > kBarrierTimeoutNs) {
+                    record_error(status, MLA_ERR_TIMEOUT, kSiteGrid);
+                    *ok = 0;
+                    break;
+                }
+            }
+            __threadfence();
+        }
+        __syncthreads();
+        return *ok != 0;
+    }
+    __device__ __forceinline__ void arrive_last() {
+        __syncthreads();
+        if (threadIdx.x == 0 && atomicAdd(word, 1u) == (passed + 1) * gridDim.x - 1) *word = 0;
+    }
+    __device__ __forceinline__ uint32_t arrivals() const {
+        uint32_t v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
+        return v;
+    }
+};
 
 struct CacheView {
     char* base;
@@ -52,17 +90,19 @@ struct CacheView {
 };
 
 // Where the passes of one call leave what the next ones need (in the
-// caller's workspace, behind the status header).
+// caller's workspace, behind the status header). What another CTA wrote is
+// read from L2 (__ldcg).
 struct PageScratch {
     int32_t* status;
+    uint32_t* barrier;
     int32_t* go;            // fork: 1 if the call goes ahead
                             // compact: [0] live pages M, [1] pages to move
     int32_t* chunk_count;   // [chunks] free (fork) or live (compact) pages of each chunk
     uint32_t* live_bits;    // compact: one bit per page
     int32_t* need;          // fork: [children] fresh pages, -1 for a child that cannot be made
-    int32_t* src;           // compact: [moves] ascending
-    int32_t* dst;           //          [moves] ascending
-    int32_t* moved_ref;     //          [moves] count of src[k]
+    int32_t* src;           // compact: [moves] ascending; fork: [children] page to copy from
+    int32_t* dst;           // compact: [moves] ascending; fork: [children] first fresh page
+    int32_t* moved_ref;     // compact: [moves] count of src[k]; fork: [children] rows to copy
 };
 
 __device__ __forceinline__ int warp_sum(int v) {
@@ -108,20 +148,37 @@ __device__ __forceinline__ int block_exclusive(int v, int* tmp, int* total) {
 // counts[0..n) summed over the CTA.
 __device__ __forceinline__ int sum_below(const int32_t* counts, int n, int* tmp) {
     int s = 0;
-    for (int i = threadIdx.x; i < n; i += kPageThreads) s += counts[i];
+    for (int i = threadIdx.x; i < n; i += kPageThreads) s += __ldcg(counts + i);
     return block_sum(s, tmp);
 }
 
-// Pages of this CTA's chunk whose count is zero (or not).
-__device__ __forceinline__ int count_chunk(const int32_t* ref, int64_t num_blocks, bool zero,
-                                           int* tmp) {
-    int n = 0;
+// Copy the first `bytes` (a multiple of 16) of page src to page dst in one
+// layer: the 8 KB pieces part, part + parts, ..., two pieces (four 16-byte
+// loads a thread) in flight before their stores.
+__device__ __forceinline__ void copy_page(const CacheView& cache, int layer, int src, int dst,
+                                          int bytes, int part, int parts) {
+    const char* s = cache.base + layer * cache.layer_stride + src * cache.page_bytes;
+    char* d = cache.base + layer * cache.layer_stride + dst * cache.page_bytes;
+    const int step = parts * kPieceBytes;
+    for (int o = part * kPieceBytes + int(threadIdx.x) * 16; o < bytes; o += 2 * step) {
+        uint4 v[4];
+        const int at[4] = {o, o + kPieceBytes / 2, o + step, o + step + kPieceBytes / 2};
 #pragma unroll
-    for (int i = 0; i < kChunkIters; ++i) {
-        const int64_t page = int64_t(blockIdx.x) * kChunk + i * kPageThreads + threadIdx.x;
-        if (page < num_blocks) n += (ref[page] == 0) == zero;
+        for (int i = 0; i < 4; ++i)
+            if (at[i] < bytes) v[i] = __ldcs(reinterpret_cast<const uint4*>(s + at[i]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (at[i] < bytes) __stcs(reinterpret_cast<uint4*>(d + at[i]), v[i]);
     }
-    return block_sum(n, tmp);
+}
+static_assert(kPieceBytes == 2 * 16 * kPageThreads, "a piece is two loads per thread");
+
+// Parts that one page's copy is cut into, so that few pages still use the
+// whole grid.
+__device__ __forceinline__ uint32_t parts_of(const CacheView& cache, uint32_t pages) {
+    const uint32_t most = uint32_t((cache.page_bytes + kPieceBytes - 1) / kPieceBytes);
+    const uint32_t want = (2 * gridDim.x + pages - 1) / pages;
+    return want < most ? want : most;
 }
 
 // ------------------------------------------------------------------- fork
@@ -142,21 +199,11 @@ struct ForkParams {
     int chunks;
 };
 
-// CTAs [0, chunks): free pages of a chunk. The others: one warp per child
-// checks it and writes how many fresh pages it needs.
-__global__ void __launch_bounds__(kPageThreads) fork_count_kernel(const ForkParams p) {
-    __shared__ int tmp[kWarps];
-    grid_launch_dependents();
-    if (int(blockIdx.x) < p.chunks) {
-        const int n = count_chunk(p.ref_in, p.num_blocks, true, tmp);
-        if (threadIdx.x == 0) p.ws.chunk_count[blockIdx.x] = n;
-        return;
-    }
-    const int c = (blockIdx.x - p.chunks) * kWarps + (threadIdx.x >> 5);
+// One warp checks one child and writes how many fresh pages it needs.
+__device__ __forceinline__ void check_child(const ForkParams& p, int c) {
     const int lane = threadIdx.x & 31;
-    if (c >= p.children) return;
     const int parent = p.parents[c], S = p.shared_lens[c], L = p.child_lens[c];
-    int bad = MLA_OK, detail = 0;
+    int bad = MLA_OK, detail = 0, from = 0;
     if (S < 0 || L < S || int64_t(L) > int64_t(p.max_blocks) * kPageSize) {
         bad = MLA_ERR_BAD_SEQ_LEN;
         detail = S < 0 ? S : L;
@@ -174,139 +221,149 @@ __global__ void __launch_bounds__(kPageThreads) fork_count_kernel(const ForkPara
             } else if (p.ref_in[page] == 0) {
                 bad = MLA_ERR_PAGE_STATE;
                 detail = page;
+            } else if (j == S / kPageSize) {
+                from = page;                  // (in one lane at most)
             }
         }
     }
     if (bad != MLA_OK) record_error(p.ws.status, bad, detail);
+    __syncwarp();
     const bool any = __any_sync(0xffffffffu, bad != MLA_OK);
-    if (lane == 0) p.ws.need[c] = any ? -1 : pages_of(L) - S / kPageSize;
+    from = int(__reduce_add_sync(0xffffffffu, uint32_t(from)));
+    if (lane == 0) {
+        p.ws.need[c] = any ? -1 : pages_of(L) - S / kPageSize;
+        p.ws.src[c] = from;
+        p.ws.moved_ref[c] = S % kPageSize;
+    }
 }
 
-// Every CTA: the children's page offsets, then its chunk's free pages to
-// their owners and the chunk's counts.
-__global__ void __launch_bounds__(kPageThreads) fork_assign_kernel(const ForkParams p) {
+__global__ void __launch_bounds__(kPageThreads, kCtasPerSm) fork_kernel(const ForkParams p) {
     __shared__ int tmp[kWarps];
+    __shared__ int barrier_ok;
     __shared__ int warp_free[kChunkIters * kWarps];
     extern __shared__ int off[];      // [children + 1]
-    grid_launch_dependents();
-    grid_wait();
-    int total = 0, invalid = 0;
-    bool over = false;
-    for (int c0 = 0; c0 < p.children; c0 += kPageThreads) {
-        const int c = c0 + threadIdx.x;
-        const int n = c < p.children ? p.ws.need[c] : 0;
-        if (n < 0) invalid = 1;
-        // (one child alone may ask for more than the pool; no sum here wraps)
-        int sum;
-        const int before = block_exclusive(n < 0 ? 0 : int(min(int64_t(n), p.num_blocks + 1)), tmp,
-                                           &sum);
-        if (c < p.children) off[c] = total + before;
-        over = over || int64_t(total) + sum > p.num_blocks;
-        total = over ? 0 : total + sum;
-    }
-    if (threadIdx.x == 0) off[p.children] = total;
-    invalid = block_sum(invalid, tmp);
-    const int free_below = sum_below(p.ws.chunk_count, int(blockIdx.x), tmp);
-    const int free_all = free_below + [&] {
-        int s = 0;
-        for (int i = blockIdx.x + threadIdx.x; i < p.chunks; i += kPageThreads)
-            s += p.ws.chunk_count[i];
-        return block_sum(s, tmp);
-    }();
-    const bool go = invalid == 0 && !over && total <= free_all;
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        p.ws.go[0] = go ? 1 : 0;
-        if (invalid == 0 && !go)
-            record_error(p.ws.status, MLA_ERR_NO_PAGES, over ? INT_MAX : total - free_all);
-    }
-
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int ref[kChunkIters];
-    uint32_t free_mask[kChunkIters];
+    GridBarrier grid{p.ws.barrier, p.ws.status};
+
+    // Free pages of each chunk; then one warp per child.
+    const int checkers = (p.children + kWarps - 1) / kWarps;
+    for (int u = blockIdx.x; u < p.chunks + checkers; u += gridDim.x) {
+        if (u < p.chunks) {
+            int n = 0;
 #pragma unroll
-    for (int i = 0; i < kChunkIters; ++i) {
-        const int64_t page = int64_t(blockIdx.x) * kChunk + i * kPageThreads + threadIdx.x;
-        ref[i] = page < p.num_blocks ? p.ref_in[page] : 1;
-        free_mask[i] = __ballot_sync(0xffffffffu, ref[i] == 0);
-        if (lane == 0) warp_free[i * kWarps + warp] = __popc(free_mask[i]);
+            for (int i = 0; i < kChunkIters; ++i) {
+                const int64_t page = int64_t(u) * kChunk + i * kPageThreads + threadIdx.x;
+                if (page < p.num_blocks) n += p.ref_in[page] == 0;
+            }
+            n = block_sum(n, tmp);
+            if (threadIdx.x == 0) p.ws.chunk_count[u] = n;
+        } else {
+            const int c = (u - p.chunks) * kWarps + warp;
+            if (c < p.children) check_child(p, c);
+        }
     }
-    __syncthreads();
+    if (!grid.wait(&barrier_ok)) return;
+
+    // CTAs with a chunk: the children's page offsets, then the chunk's free
+    // pages to their owners and the chunk's counts.
+    if (int(blockIdx.x) < p.chunks) {
+        int total = 0, invalid = 0;
+        bool over = false;
+        for (int c0 = 0; c0 < p.children; c0 += kPageThreads) {
+            const int c = c0 + threadIdx.x;
+            const int n = c < p.children ? __ldcg(p.ws.need + c) : 0;
+            if (n < 0) invalid = 1;
+            // (one child alone may ask for more than the pool; no sum here wraps)
+            int sum;
+            const int before = block_exclusive(
+                n < 0 ? 0 : int(min(int64_t(n), p.num_blocks + 1)), tmp, &sum);
+            if (c < p.children) off[c] = total + before;
+            over = over || int64_t(total) + sum > p.num_blocks;
+            total = over ? 0 : total + sum;
+        }
+        if (threadIdx.x == 0) off[p.children] = total;
+        invalid = block_sum(invalid, tmp);
+        const int free_all = sum_below(p.ws.chunk_count, p.chunks, tmp);
+        const bool go = invalid == 0 && !over && total <= free_all;
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            p.ws.go[0] = go ? 1 : 0;
+            if (invalid == 0 && !go)
+                record_error(p.ws.status, MLA_ERR_NO_PAGES, over ? INT_MAX : total - free_all);
+        }
+        for (int u = blockIdx.x; u < p.chunks; u += gridDim.x) {
+            const int free_below = sum_below(p.ws.chunk_count, u, tmp);
+            int ref[kChunkIters];
+            uint32_t free_mask[kChunkIters];
 #pragma unroll
-    for (int i = 0; i < kChunkIters; ++i) {
-        const int64_t page = int64_t(blockIdx.x) * kChunk + i * kPageThreads + threadIdx.x;
-        if (page >= p.num_blocks) continue;
-        if (ref[i] == 0 && go) {
-            int rank = free_below + __popc(free_mask[i] & ((1u << lane) - 1u));
-            for (int w = 0; w < i * kWarps + warp; ++w) rank += warp_free[w];
-            if (rank < total) {
-                // The child that owns rank: the last c with off[c] <= rank
-                // (children without fresh pages share their successor's offset).
-                int lo = 0, hi = p.children;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (off[mid] <= rank) lo = mid; else hi = mid;
+            for (int i = 0; i < kChunkIters; ++i) {
+                const int64_t page = int64_t(u) * kChunk + i * kPageThreads + threadIdx.x;
+                ref[i] = page < p.num_blocks ? p.ref_in[page] : 1;
+                free_mask[i] = __ballot_sync(0xffffffffu, ref[i] == 0);
+                if (lane == 0) warp_free[i * kWarps + warp] = __popc(free_mask[i]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kChunkIters; ++i) {
+                const int64_t page = int64_t(u) * kChunk + i * kPageThreads + threadIdx.x;
+                if (page >= p.num_blocks) continue;
+                if (ref[i] == 0 && go) {
+                    int rank = free_below + __popc(free_mask[i] & ((1u << lane) - 1u));
+                    for (int w = 0; w < i * kWarps + warp; ++w) rank += warp_free[w];
+                    if (rank < total) {
+                        // The child that owns rank: the last c with off[c] <=
+                        // rank (children without fresh pages share their
+                        // successor's offset).
+                        int lo = 0, hi = p.children;
+                        while (hi - lo > 1) {
+                            const int mid = (lo + hi) >> 1;
+                            if (off[mid] <= rank) lo = mid; else hi = mid;
+                        }
+                        const int j = rank - off[lo];
+                        p.child_table[int64_t(lo) * p.max_blocks + p.shared_lens[lo] / kPageSize +
+                                      j] = int32_t(page);
+                        if (j == 0) p.ws.dst[lo] = int32_t(page);
+                        ref[i] = 1;
+                    }
                 }
-                const int j = p.shared_lens[lo] / kPageSize + (rank - off[lo]);
-                p.child_table[int64_t(lo) * p.max_blocks + j] = int32_t(page);
-                ref[i] = 1;
+                p.ref_out[page] = ref[i];
             }
         }
-        p.ref_out[page] = ref[i];
     }
-}
+    if (!grid.wait(&barrier_ok)) return;
 
-// Copy `bytes` (a multiple of 16) of one piece of a page, two 16-byte loads
-// in flight per thread before their stores.
-__device__ __forceinline__ void copy_piece(const CacheView& cache, int layer, int src, int dst,
-                                           int piece, int64_t bytes) {
-    const char* s = cache.base + layer * cache.layer_stride + src * cache.page_bytes;
-    char* d = cache.base + layer * cache.layer_stride + dst * cache.page_bytes;
-    const int64_t o0 = int64_t(piece) * kPieceBytes + threadIdx.x * 16;
-    const int64_t o1 = o0 + kPieceBytes / 2;
-    uint4 a, b;
-    if (o0 < bytes) a = __ldcs(reinterpret_cast<const uint4*>(s + o0));
-    if (o1 < bytes) b = __ldcs(reinterpret_cast<const uint4*>(s + o1));
-    if (o0 < bytes) __stcs(reinterpret_cast<uint4*>(d + o0), a);
-    if (o1 < bytes) __stcs(reinterpret_cast<uint4*>(d + o1), b);
-}
-static_assert(kPieceBytes == 2 * 16 * kPageThreads, "a piece is two loads per thread");
-
-// One warp per child for its shared pages, then the whole grid copies the
-// partly filled pages piece by piece.
-__global__ void __launch_bounds__(kPageThreads) fork_copy_kernel(const ForkParams p) {
-    grid_wait();
-    if (p.ws.go[0] == 0) return;
-    const int lane = threadIdx.x & 31;
-    for (int c = blockIdx.x * kWarps + (threadIdx.x >> 5); c < p.children;
-         c += gridDim.x * kWarps) {
-        const int full = p.shared_lens[c] / kPageSize;
-        const int32_t* row = p.table + int64_t(p.parents[c]) * p.max_blocks;
-        for (int j = lane; j < full; j += 32) {
-            const int page = row[j];
-            p.child_table[int64_t(c) * p.max_blocks + j] = page;
-            atomicAdd(p.ref_out + page, 1);
+    // One warp per child for its shared pages; the whole grid copies the
+    // partly filled pages.
+    if (__ldcg(p.ws.go) != 0) {
+        for (int c = blockIdx.x * kWarps + warp; c < p.children; c += gridDim.x * kWarps) {
+            const int full = p.shared_lens[c] / kPageSize;
+            const int32_t* row = p.table + int64_t(p.parents[c]) * p.max_blocks;
+            for (int j = lane; j < full; j += 32) {
+                const int page = row[j];
+                p.child_table[int64_t(c) * p.max_blocks + j] = page;
+                atomicAdd(p.ref_out + page, 1);
+            }
+        }
+        const uint32_t layers = uint32_t(p.cache.layers);
+        const uint32_t parts = p.children > 0 ? parts_of(p.cache, p.children * layers) : 1;
+        const uint32_t per_child = layers * parts;
+        const int row_bytes = int(p.cache.page_bytes / kPageSize);
+        for (int64_t i = blockIdx.x; i < int64_t(p.children) * per_child; i += gridDim.x) {
+            const int c = int(i / per_child);
+            const uint32_t r = uint32_t(i - int64_t(c) * per_child);
+            const int bytes = __ldcg(p.ws.moved_ref + c) * row_bytes;
+            const int src = __ldcg(p.ws.src + c), dst = __ldcg(p.ws.dst + c);
+            if (bytes > 0)
+                copy_page(p.cache, int(r / parts), src, dst, bytes, int(r % parts), int(parts));
         }
     }
-    const int pieces = int((p.cache.page_bytes + kPieceBytes - 1) / kPieceBytes);
-    const int64_t items = int64_t(p.children) * p.cache.layers * pieces;
-    const int64_t row_bytes = p.cache.page_bytes / kPageSize;
-    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-        const int c = int(i / (int64_t(p.cache.layers) * pieces));
-        const int r = int(i - int64_t(c) * p.cache.layers * pieces);
-        const int S = p.shared_lens[c];
-        const int64_t bytes = (S % kPageSize) * row_bytes;
-        const int piece = r % pieces;
-        if (int64_t(piece) * kPieceBytes >= bytes) continue;
-        copy_piece(p.cache, r / pieces,
-                   p.table[int64_t(p.parents[c]) * p.max_blocks + S / kPageSize],
-                   p.child_table[int64_t(c) * p.max_blocks + S / kPageSize], piece, bytes);
-    }
+    grid.arrive_last();
 }
 
 // ------------------------------------------------------------------- free
 
 struct FreeParams {
     int32_t* status;
+    uint32_t* barrier;
     int64_t num_blocks;
     const int32_t* ref_in;
     int32_t* ref_out;
@@ -318,58 +375,59 @@ struct FreeParams {
     int32_t* num_freed;
 };
 
-__global__ void __launch_bounds__(kPageThreads) free_copy_kernel(const FreeParams p) {
-    grid_launch_dependents();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.num_freed = 0;
-    if (p.ref_in == p.ref_out) return;
-    for (int64_t i = int64_t(blockIdx.x) * kPageThreads + threadIdx.x; i < p.num_blocks;
-         i += int64_t(gridDim.x) * kPageThreads)
-        p.ref_out[i] = p.ref_in[i];
-}
-
-// CTA (x, r): entries 256x.. of row free_rows[r]. Lanes of a warp that name
-// the same page (a prompt that many rows share) take it off with one atomic.
-__global__ void __launch_bounds__(kPageThreads) free_rows_kernel(const FreeParams p) {
-    grid_wait();
+// The counts copied (unless in place), then 256 entries of a row at a time.
+// Lanes of a warp that name the same page take it off with one atomic.
+__global__ void __launch_bounds__(kPageThreads, kCtasPerSm) free_kernel(const FreeParams p) {
+    __shared__ int barrier_ok;
     const int lane = threadIdx.x & 31;
-    for (int r = blockIdx.y; r < p.count; r += gridDim.y) {
+    GridBarrier grid{p.barrier, p.status};
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.num_freed = 0;
+    if (p.ref_in != p.ref_out)
+        for (int64_t i = int64_t(blockIdx.x) * kPageThreads + threadIdx.x; i < p.num_blocks;
+             i += int64_t(gridDim.x) * kPageThreads)
+            p.ref_out[i] = p.ref_in[i];
+    if (!grid.wait(&barrier_ok)) return;
+    const int per_row = (p.max_blocks + kPageThreads - 1) / kPageThreads;
+    for (int64_t u = blockIdx.x; u < int64_t(p.count) * per_row; u += gridDim.x) {
+        const int r = int(u / per_row), j0 = int(u - int64_t(r) * per_row) * kPageThreads;
         const int row = p.free_rows[r];
         if (row < 0 || row >= p.rows) {
-            if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.status, MLA_ERR_BAD_ROW, row);
+            if (j0 == 0 && threadIdx.x == 0) record_error(p.status, MLA_ERR_BAD_ROW, row);
             continue;
         }
         const int L = p.seq_lens[row];
         if (L < 0 || int64_t(L) > int64_t(p.max_blocks) * kPageSize) {
-            if (blockIdx.x == 0 && threadIdx.x == 0)
-                record_error(p.status, MLA_ERR_BAD_SEQ_LEN, L);
+            if (j0 == 0 && threadIdx.x == 0) record_error(p.status, MLA_ERR_BAD_SEQ_LEN, L);
             continue;
         }
         const int n = pages_of(L);
-        for (int j0 = blockIdx.x * kPageThreads; j0 < n; j0 += gridDim.x * kPageThreads) {
-            const int j = j0 + threadIdx.x;
-            int page = j < n ? p.table[int64_t(row) * p.max_blocks + j] : -1;
-            if (j < n && (page < 0 || int64_t(page) >= p.num_blocks)) {
-                record_error(p.status, MLA_ERR_BAD_BLOCK_ID, page);
-                page = -1;
-            }
-            const uint32_t same = __match_any_sync(0xffffffffu, page);
-            bool freed = false;
-            if (page >= 0 && lane == __ffs(same) - 1) {
-                const int off = __popc(same);
-                const int old = atomicSub(p.ref_out + page, off);
-                freed = old > 0 && old <= off;
-                if (old < off) {
-                    // More entries than counts: the count stays at 0. What was
-                    // taken too much is put back, so whatever the order, the
-                    // sum of the atomics on this page is -(what it had).
-                    atomicAdd(p.ref_out + page, off - (old > 0 ? old : 0));
-                    record_error(p.status, MLA_ERR_PAGE_STATE, page);
-                }
-            }
-            const uint32_t f = __ballot_sync(0xffffffffu, freed);
-            if (lane == 0 && f != 0) atomicAdd(p.num_freed, __popc(f));
+        if (j0 >= n) continue;
+        const int j = j0 + threadIdx.x;
+        int page = j < n ? p.table[int64_t(row) * p.max_blocks + j] : -1;
+        if (j < n && (page < 0 || int64_t(page) >= p.num_blocks)) {
+            record_error(p.status, MLA_ERR_BAD_BLOCK_ID, page);
+            page = -1;
         }
+        __syncwarp();
+        const uint32_t same = __match_any_sync(0xffffffffu, page);
+        bool freed = false;
+        if (page >= 0 && lane == __ffs(same) - 1) {
+            const int off = __popc(same);
+            const int old = atomicSub(p.ref_out + page, off);
+            freed = old > 0 && old <= off;
+            if (old < off) {
+                // More entries than counts: the count stays at 0. What was
+                // taken too much is put back, so whatever the order, the sum
+                // of the atomics on this page is -(what it had).
+                atomicAdd(p.ref_out + page, off - (old > 0 ? old : 0));
+                record_error(p.status, MLA_ERR_PAGE_STATE, page);
+            }
+        }
+        __syncwarp();
+        const uint32_t f = __ballot_sync(0xffffffffu, freed);
+        if (lane == 0 && f != 0) atomicAdd(p.num_freed, __popc(f));
     }
+    grid.arrive_last();
 }
 
 // ---------------------------------------------------------------- compact
@@ -389,99 +447,99 @@ struct CompactParams {
     int chunks;
 };
 
-// Live pages of each chunk, and one bit per page: the list pass writes the
-// counts in place, so what it needs of other chunks it reads from the bits.
-__global__ void __launch_bounds__(kPageThreads) compact_count_kernel(const CompactParams p) {
-    __shared__ int tmp[kWarps];
-    grid_launch_dependents();
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kChunkIters; ++i) {
-        const int64_t page = int64_t(blockIdx.x) * kChunk + i * kPageThreads + threadIdx.x;
-        const bool live = page < p.num_blocks && p.ref_in[page] != 0;
-        const uint32_t bits = __ballot_sync(0xffffffffu, live);
-        if ((threadIdx.x & 31) == 0) p.ws.live_bits[page >> 5] = bits;
-        n += live;
-    }
-    n = block_sum(n, tmp);
-    if (threadIdx.x == 0) p.ws.chunk_count[blockIdx.x] = n;
-}
-
-__global__ void __launch_bounds__(kPageThreads) compact_list_kernel(const CompactParams p) {
-    __shared__ int tmp[kWarps];
-    __shared__ uint32_t live_bits[kChunk / 32];
-    grid_launch_dependents();
-    grid_wait();
-    const int live_before = sum_below(p.ws.chunk_count, int(blockIdx.x), tmp);
-    int rest = 0;
-    for (int i = blockIdx.x + threadIdx.x; i < p.chunks; i += kPageThreads)
-        rest += p.ws.chunk_count[i];
-    const int M = live_before + block_sum(rest, tmp);
-    // Live pages below M: those of the whole chunks before M's and of the
-    // words of M's chunk up to M.
-    const int m_chunk = M / kChunk;
-    int part = 0;
-    if (m_chunk < p.chunks && threadIdx.x < kChunk / 32) {
-        const int first = m_chunk * kChunk + threadIdx.x * 32;
-        const uint32_t bits = p.ws.live_bits[first >> 5];
-        const int take = M - first;   // bits of this word below M
-        part = __popc(take >= 32 ? bits : take > 0 ? bits & ((1u << take) - 1u) : 0u);
-    }
-    const int live_low = sum_below(p.ws.chunk_count, m_chunk, tmp) + block_sum(part, tmp);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        p.ws.go[0] = M;
-        p.ws.go[1] = M - live_low;
-        if (p.num_live != nullptr) *p.num_live = M;
-    }
-    if (threadIdx.x < kChunk / 32)
-        live_bits[threadIdx.x] = p.ws.live_bits[blockIdx.x * (kChunk / 32) + threadIdx.x];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kChunkIters; ++i) {
-        const int in = i * kPageThreads + threadIdx.x;
-        const int64_t page = int64_t(blockIdx.x) * kChunk + in;
-        if (page >= p.num_blocks) continue;
-        const uint32_t bits = live_bits[in >> 5];
-        int before = live_before + __popc(bits & ((1u << (in & 31)) - 1u));
-        for (int w = 0; w < (in >> 5); ++w) before += __popc(live_bits[w]);
-        const bool live = (bits >> (in & 31)) & 1u;
-        const int ref = p.ref_in[page];
-        int to = live ? int(page) : -1;
-        if (live && page >= M) {
-            const int k = before - live_low;
-            p.ws.src[k] = int(page);
-            p.ws.moved_ref[k] = ref;
-            p.ref_out[page] = 0;
-            continue;                      // its map entry is the move pass's
-        }
-        if (!live && page < M) {
-            p.ws.dst[int(page) - before] = int(page);   // its count is the move pass's
-        } else {
-            p.ref_out[page] = ref;
-        }
-        if (p.page_map != nullptr) p.page_map[page] = to;
-    }
-}
-
 // Index of `v` in the ascending list a[0..n), or -1.
 __device__ __forceinline__ int find(const int32_t* a, int n, int v) {
     int lo = 0, hi = n;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (a[mid] < v) lo = mid + 1; else hi = mid;
+        if (__ldcg(a + mid) < v) lo = mid + 1; else hi = mid;
     }
-    return lo < n && a[lo] == v ? lo : -1;
+    return lo < n && __ldcg(a + lo) == v ? lo : -1;
 }
 
-__global__ void __launch_bounds__(kPageThreads) compact_move_kernel(const CompactParams p) {
-    grid_wait();
-    const int M = p.ws.go[0], moves = p.ws.go[1];
+__global__ void __launch_bounds__(kPageThreads, kCtasPerSm) compact_kernel(const CompactParams p) {
+    __shared__ int tmp[kWarps];
+    __shared__ int barrier_ok;
+    __shared__ uint32_t live_bits[kChunk / 32];
+    GridBarrier grid{p.ws.barrier, p.ws.status};
+
+    // Live pages of each chunk, and one bit per page: the next pass writes
+    // the counts in place, so what it needs of other chunks it reads from the
+    // bits.
+    for (int u = blockIdx.x; u < p.chunks; u += gridDim.x) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kChunkIters; ++i) {
+            const int64_t page = int64_t(u) * kChunk + i * kPageThreads + threadIdx.x;
+            const bool live = page < p.num_blocks && p.ref_in[page] != 0;
+            const uint32_t bits = __ballot_sync(0xffffffffu, live);
+            if ((threadIdx.x & 31) == 0) p.ws.live_bits[page >> 5] = bits;
+            n += live;
+        }
+        n = block_sum(n, tmp);
+        if (threadIdx.x == 0) p.ws.chunk_count[u] = n;
+    }
+    if (!grid.wait(&barrier_ok)) return;
+
+    if (int(blockIdx.x) < p.chunks) {
+        const int M = sum_below(p.ws.chunk_count, p.chunks, tmp);
+        // Live pages below M: those of the whole chunks before M's and of the
+        // words of M's chunk up to M.
+        const int m_chunk = M / kChunk;
+        int part = 0;
+        if (m_chunk < p.chunks && threadIdx.x < kChunk / 32) {
+            const int first = m_chunk * kChunk + threadIdx.x * 32;
+            const uint32_t bits = __ldcg(p.ws.live_bits + (first >> 5));
+            const int take = M - first;   // bits of this word below M
+            part = __popc(take >= 32 ? bits : take > 0 ? bits & ((1u << take) - 1u) : 0u);
+        }
+        const int live_low = sum_below(p.ws.chunk_count, m_chunk, tmp) + block_sum(part, tmp);
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            p.ws.go[0] = M;
+            p.ws.go[1] = M - live_low;
+            if (p.num_live != nullptr) *p.num_live = M;
+        }
+        for (int u = blockIdx.x; u < p.chunks; u += gridDim.x) {
+            const int live_before = sum_below(p.ws.chunk_count, u, tmp);
+            if (threadIdx.x < kChunk / 32)
+                live_bits[threadIdx.x] = __ldcg(p.ws.live_bits + u * (kChunk / 32) + threadIdx.x);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kChunkIters; ++i) {
+                const int in = i * kPageThreads + threadIdx.x;
+                const int64_t page = int64_t(u) * kChunk + in;
+                if (page >= p.num_blocks) continue;
+                const uint32_t bits = live_bits[in >> 5];
+                int before = live_before + __popc(bits & ((1u << (in & 31)) - 1u));
+                for (int w = 0; w < (in >> 5); ++w) before += __popc(live_bits[w]);
+                const bool live = (bits >> (in & 31)) & 1u;
+                const int ref = p.ref_in[page];
+                if (live && page >= M) {
+                    const int k = before - live_low;
+                    p.ws.src[k] = int(page);
+                    p.ws.moved_ref[k] = ref;
+                    p.ref_out[page] = 0;
+                    continue;                      // its map entry is the move pass's
+                }
+                if (!live && page < M) {
+                    p.ws.dst[int(page) - before] = int(page);   // its count is the move pass's
+                } else {
+                    p.ref_out[page] = ref;
+                }
+                if (p.page_map != nullptr) p.page_map[page] = live ? int(page) : -1;
+            }
+            __syncthreads();
+        }
+    }
+    if (!grid.wait(&barrier_ok)) return;
+
+    const int M = __ldcg(p.ws.go), moves = __ldcg(p.ws.go + 1);
     const int64_t tid = int64_t(blockIdx.x) * kPageThreads + threadIdx.x;
     const int64_t threads = int64_t(gridDim.x) * kPageThreads;
     for (int64_t k = tid; k < moves; k += threads) {
-        const int dst = p.ws.dst[k];
-        p.ref_out[dst] = p.ws.moved_ref[k];
-        if (p.page_map != nullptr) p.page_map[p.ws.src[k]] = dst;
+        const int dst = __ldcg(p.ws.dst + k);
+        p.ref_out[dst] = __ldcg(p.ws.moved_ref + k);
+        if (p.page_map != nullptr) p.page_map[__ldcg(p.ws.src + k)] = dst;
     }
     const int64_t entries = int64_t(p.rows) * p.max_blocks;
     for (int64_t e = tid; e < entries; e += threads) {
@@ -498,26 +556,28 @@ __global__ void __launch_bounds__(kPageThreads) compact_move_kernel(const Compac
         } else if (page >= M) {
             const int k = find(p.ws.src, moves, page);
             if (k < 0) record_error(p.ws.status, MLA_ERR_PAGE_STATE, page);
-            else page = p.ws.dst[k];
+            else page = __ldcg(p.ws.dst + k);
         } else if (find(p.ws.dst, moves, page) >= 0) {
             record_error(p.ws.status, MLA_ERR_PAGE_STATE, page);   // it was free
         }
         p.table_out[e] = page;
     }
-    const int pieces = int((p.cache.page_bytes + kPieceBytes - 1) / kPieceBytes);
-    const int64_t per_move = int64_t(p.cache.layers) * pieces;
-    const int64_t items = moves * per_move;
-    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    const int64_t pages = int64_t(moves) * p.cache.layers;
+    const uint32_t parts =
+        pages > 0 ? parts_of(p.cache, uint32_t(min(pages, int64_t(1) << 30))) : 1;
+    const int64_t per_move = int64_t(p.cache.layers) * parts;
+    for (int64_t i = blockIdx.x; i < moves * per_move; i += gridDim.x) {
         const int k = int(i / per_move);
-        const int r = int(i - k * per_move);
-        copy_piece(p.cache, r / pieces, p.ws.src[k], p.ws.dst[k], r % pieces, p.cache.page_bytes);
+        const uint32_t r = uint32_t(i - k * per_move);
+        copy_page(p.cache, int(r / parts), __ldcg(p.ws.src + k), __ldcg(p.ws.dst + k),
+                  int(p.cache.page_bytes), int(r % parts), int(parts));
     }
+    grid.arrive_last();
 }
 
 // ------------------------------------------------------------------- host
 
 constexpr int kMaxCacheBlocks = (1 << 23) - 2;   // 256 of these still sum below 2^31
-constexpr int kCopyCtas = 152 * 8;               // eight CTAs fill an SM's threads
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -526,7 +586,9 @@ int chunks_of(int64_t num_blocks) { return int((num_blocks + kChunk - 1) / kChun
 // Scratch layout; returns its size behind the status header.
 size_t page_scratch(char* ws, int64_t num_blocks, int children, PageScratch* s) {
     const size_t chunks = size_t(chunks_of(num_blocks));
-    const size_t half = round256((size_t(num_blocks) / 2 + 1) * 4);   // moves <= half the pages
+    // moves <= half the pages
+    const size_t lists = size_t(num_blocks) / 2 + 1 > size_t(children)
+                             ? size_t(num_blocks) / 2 + 1 : size_t(children);
     size_t at = kStatusBytes;
     auto take = [&](size_t bytes) {
         char* p = ws + at;
@@ -535,29 +597,38 @@ size_t page_scratch(char* ws, int64_t num_blocks, int children, PageScratch* s) 
     };
     PageScratch t{};
     t.status = reinterpret_cast<int32_t*>(ws);
+    t.barrier = reinterpret_cast<uint32_t*>(ws + 4 * kPageBarrierWord);
     t.go = take(8);
     t.chunk_count = take(chunks * 4);
     t.live_bits = reinterpret_cast<uint32_t*>(take(chunks * (kChunk / 8)));
     t.need = take(size_t(children) * 4);
-    t.src = take(half);
-    t.dst = take(half);
-    t.moved_ref = take(half);
+    t.src = take(lists * 4);
+    t.dst = take(lists * 4);
+    t.moved_ref = take(lists * 4);
     if (s != nullptr) *s = t;
     return at;
 }
 
+// A cooperative launch of as many CTAs as the work has use for, at most
+// kCtasPerSm per SM.
 template <typename Kernel, typename Params>
-int launch(Kernel kernel, dim3 grid, size_t smem, void* stream, const Params& p, bool dependent) {
+int launch(Kernel kernel, int64_t want, size_t smem, void* stream, const Params& p) {
+    int device = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    if (e != cudaSuccess) return int(e);
+    const int64_t most = int64_t(sms) * kCtasPerSm;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(unsigned(want < 1 ? 1 : want < most ? want : most));
     cfg.blockDim = dim3(kPageThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = dependent ? 1 : 0;
+    cfg.numAttrs = 1;
     return int(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
@@ -597,8 +668,6 @@ int check_counts(const int32_t* in, const int32_t* out, int64_t num_blocks) {
 int check_workspace(const void* ws, size_t bytes, size_t need) {
     return ws && aligned(ws, 256) && bytes >= need ? MLA_OK : MLA_ERR_WORKSPACE;
 }
-
-int min_int(int64_t a, int64_t b) { return int(a < b ? a : b); }
 
 }  // namespace
 }  // namespace mla
@@ -654,17 +723,11 @@ extern "C" int mla_cache_fork(void* latent_cache, int num_layers, int64_t layer_
     p.children = children;
     p.child_table = child_table;
     p.chunks = chunks_of(num_blocks);
-    const int checkers = (children + kWarps - 1) / kWarps;
-    int e = launch(fork_count_kernel, dim3(unsigned(p.chunks + checkers)), 0, stream, p, false);
-    if (e == 0)
-        e = launch(fork_assign_kernel, dim3(unsigned(p.chunks)), size_t(children + 1) * 4, stream,
-                   p, true);
-    if (e == 0 && children > 0) {
-        const int64_t pieces = (p.cache.page_bytes + kPieceBytes - 1) / kPieceBytes;
-        e = launch(fork_copy_kernel,
-                   dim3(unsigned(min_int(int64_t(children) * num_layers * pieces, kCopyCtas))), 0,
-                   stream, p, true);
-    }
+    const int64_t checks = p.chunks + (children + kWarps - 1) / kWarps;
+    const int64_t copies =
+        int64_t(children) * num_layers * ((p.cache.page_bytes + kPieceBytes - 1) / kPieceBytes);
+    const int e = launch(fork_kernel, copies > checks ? copies : checks,
+                         size_t(children + 1) * 4, stream, p);
     return e == 0 ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -697,15 +760,13 @@ extern "C" int mla_cache_free(const int32_t* ref_counts, int32_t* ref_counts_out
     p.free_rows = free_rows;
     p.count = count;
     p.num_freed = num_freed;
+    p.barrier = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + 4 * kPageBarrierWord);
+    // (a thread copies four counts)
     const int64_t copy_ctas =
-        ref_counts == ref_counts_out ? 1 : (num_blocks + kPageThreads - 1) / kPageThreads;
-    int e = launch(free_copy_kernel, dim3(unsigned(min_int(copy_ctas, kCopyCtas))), 0, stream, p,
-                   false);
-    if (e == 0 && count > 0) {
-        const dim3 grid(unsigned(min_int((max_blocks_per_seq + kPageThreads - 1) / kPageThreads, 64)),
-                        unsigned(min_int(count, 32768)));
-        e = launch(free_rows_kernel, grid, 0, stream, p, true);
-    }
+        ref_counts == ref_counts_out ? 0 : (num_blocks + 4 * kPageThreads - 1) / (4 * kPageThreads);
+    const int64_t row_ctas =
+        int64_t(count) * ((max_blocks_per_seq + kPageThreads - 1) / kPageThreads);
+    const int e = launch(free_kernel, copy_ctas > row_ctas ? copy_ctas : row_ctas, 0, stream, p);
     return e == 0 ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -744,15 +805,10 @@ extern "C" int mla_cache_compact(void* latent_cache, int num_layers, int64_t lay
     p.num_live = num_live;
     p.chunks = chunks_of(num_blocks);
     const int64_t pieces = (p.cache.page_bytes + kPieceBytes - 1) / kPieceBytes;
-    const int64_t most_moves = num_blocks / 2;
     const int64_t entry_ctas =
         (int64_t(rows) * max_blocks_per_seq + kPageThreads - 1) / kPageThreads;
-    const int64_t copy_ctas = most_moves * num_layers * pieces;
-    int e = launch(compact_count_kernel, dim3(unsigned(p.chunks)), 0, stream, p, false);
-    if (e == 0) e = launch(compact_list_kernel, dim3(unsigned(p.chunks)), 0, stream, p, true);
+    const int64_t copy_ctas = num_blocks / 2 * num_layers * pieces;   // the most there can be
     const int64_t want = copy_ctas > entry_ctas ? copy_ctas : entry_ctas;
-    if (e == 0 && want > 0)
-        e = launch(compact_move_kernel, dim3(unsigned(min_int(want, kCopyCtas))), 0, stream, p,
-                   true);
+    const int e = launch(compact_kernel, want > p.chunks ? want : p.chunks, 0, stream, p);
     return e == 0 ? MLA_OK : MLA_ERR_CUDA;
 }
