@@ -562,10 +562,12 @@ typedef struct mla_prefill_plan {
     int32_t  total_q;             /* rows of q, out and lse */
     int32_t  num_kv_splits;       /* S >= 1: parts that each sequence's keys are cut into */
     int32_t  num_sms;
-    uint32_t reserved0;
+    int32_t  single_rows;         /* 0: tensor-core kernel; 1: CUDA-core kernel, one query
+                                     row at a time */
     uint64_t workspace_bytes;
-    uint64_t partial_offset;      /* byte offset of fp32 [total_q, N, S, 128] (S > 1) */
-    uint64_t lse_partial_offset;  /* byte offset of fp32 [total_q, N, S] (S > 1) */
+    uint64_t partial_offset;      /* byte offset of fp32 [total_q, N, S, 128] (S > 1,
+                                     single_rows = 0) */
+    uint64_t lse_partial_offset;  /* byte offset of fp32 [total_q, N, S] (likewise) */
     uint32_t reserved[6];
 } mla_prefill_plan_t;
 
@@ -573,9 +575,11 @@ typedef struct mla_prefill_plan {
  * mla_prefill_plan -- choose S, size the workspace. Host only.
  *   batch, num_heads   B >= 0, 1 <= N <= 128.
  *   total_q            rows of q; max_q_len, max_k_len: the longest sequence's
- *                      (they steer S alone; longer ones give the same results).
+ *                      (they steer the kernel and S alone: longer sequences are
+ *                      computed too, more slowly).
  *   num_kv_splits      S in 1..64, or 0: the planner splits the keys when the
- *                      query tiles alone leave SMs idle.
+ *                      query rows alone leave SMs idle. (With single_rows
+ *                      it becomes 1, 2, 4 or 8.)
  *   num_sms            SMs of the target device, >= 1.
  */
 int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q_len, int max_k_len,
@@ -595,9 +599,9 @@ int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q_len, int m
  *   workspace      device, >= plan->workspace_bytes, 256-byte aligned,
  *                  initialised once with mla_workspace_init; calls that
  *                  share one must not overlap on the device.
- * The softmax weights are rounded to bf16 for the tensor cores; scores, sums
- * and accumulators are fp32. Results do not depend on timing. One launch (two
- * with S > 1) on `stream`, no synchronisation.
+ * The softmax weights are rounded to bf16 for the tensor cores (with
+ * single_rows they stay fp32); scores, sums and accumulators are fp32. Results do not depend on timing. One launch (two
+ * with S > 1 and single_rows = 0) on `stream`, no synchronisation.
  */
 int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const void* kv, const void* k_pe,
                 int total_k, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int causal,

@@ -91,7 +91,7 @@ class MlaPrefillPlan(ctypes.Structure):
         ("total_q", ctypes.c_int32),
         ("num_kv_splits", ctypes.c_int32),
         ("num_sms", ctypes.c_int32),
-        ("reserved0", ctypes.c_uint32),
+        ("single_rows", ctypes.c_int32),
         ("workspace_bytes", ctypes.c_uint64),
         ("partial_offset", ctypes.c_uint64),
         ("lse_partial_offset", ctypes.c_uint64),

@@ -44,7 +44,7 @@
 #include <cstdint>
 #include <cstring>
 
-#include "mla_device.cuh"
+#include "mla_prefill.cuh"
 #include "tc_ptx.cuh"
 #include "tensor_map.cuh"
 
@@ -55,7 +55,7 @@ constexpr int kThreads = 384;
 constexpr int kTileRows = 128;
 constexpr int kItemRows = 2 * kTileRows;
 constexpr int kStep = 128;                    // keys per step
-constexpr int kQk = 192, kV = 128, kKvHead = 256;
+constexpr int kQk = kPrefillQk, kV = kPrefillV, kKvHead = kPrefillKv;
 constexpr int kBlock = 16384;                 // 128 x 64 (Q, K) or 64 x 128 (V) bf16
 constexpr int kQBlocks = 3;                   // per tile
 constexpr int kRing = 8;                      // blocks: K of a step takes 3, V takes 2
@@ -113,24 +113,6 @@ struct Bars {
 static_assert(sizeof(Bars) <= 1024, "barrier block");
 constexpr int kItemConsumers = 8 + 3;   // softmax warps, loads, MMAs, helper
 
-struct PrefillParams {
-    const uint16_t* kv;
-    const int32_t* cu_q;
-    const int32_t* cu_k;
-    int batch, heads, total_q, total_k;
-    int causal;
-    int splits;
-    int group;                // heads that run together
-    float scale_log2;
-    uint16_t* out;            // bf16 [total_q, N, 128]
-    float* lse;               // fp32 [total_q, N] or null
-    float* o_part;            // splits > 1: fp32 [total_q, N, S, 128]
-    float* lse_part;          //             fp32 [total_q, N, S]
-    int32_t* status;
-    unsigned long long* ticket;   // next item (in the status header; 0 between calls)
-    uint32_t* done;               // CTAs that have finished
-};
-
 // Bounded wait. A waiting thread sleeps in mbarrier.try_wait: threads that
 // poll take issue slots from the softmax warps (256 polls before the first
 // sleep made the whole kernel 1.7 times slower).
@@ -163,12 +145,6 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
     }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
 // Pairs of floats: one instruction for two (round to nearest, as the single ones).
 __device__ __forceinline__ uint64_t pack_f32(float a, float b) {
     uint64_t d;
@@ -187,25 +163,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
-}
-
-// Rows and keys of sequence b; one whose bounds make no sense has none.
-__device__ __forceinline__ void sequence(const PrefillParams& p, int b, int* q0, int* lq, int* k0,
-                                         int* lk) {
-    const int qa = p.cu_q[b], qe = p.cu_q[b + 1], ka = p.cu_k[b], ke = p.cu_k[b + 1];
-    *q0 = qa;
-    *k0 = ka;
-    *lq = *lk = 0;
-    if (qa < 0 || qe < qa || qe > p.total_q) {
-        record_error(p.status, MLA_ERR_BAD_SEQ_LEN, qe);
-        return;
-    }
-    *lq = qe - qa;
-    if (ka < 0 || ke < ka || ke > p.total_k) {
-        record_error(p.status, MLA_ERR_BAD_SEQ_LEN, ke);
-        return;
-    }
-    *lk = ke - ka;
 }
 
 __device__ __forceinline__ int item_tiles(int lq) { return lq / kItemRows + (lq % kItemRows != 0); }
@@ -950,6 +907,32 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
     if (lane == 0 && p.lse != nullptr) p.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
 }
 
+// The tensor kernel.
+int launch_prefill_tiles(PrefillParams p, int num_sms, cudaStream_t st) {
+    const int64_t head_bytes = int64_t(p.total_k) * kKvHead * 2;
+    const int64_t group = head_bytes > 0 ? kGroupBytes / head_bytes : p.heads;
+    p.group = group < 1 ? 1 : group > p.heads ? p.heads : int(group);
+    // (Without keys the maps over them are never read through; the queries
+    // stand in.)
+    CUtensorMap mq, mk, mv, mpe;
+    const void* kv_base = p.total_k > 0 ? p.kv : p.q;
+    const void* pe_base = p.total_k > 0 ? p.k_pe : p.q;
+    const uint64_t k_rows = p.total_k > 0 ? uint64_t(p.total_k) : 1;
+    const uint64_t kv_cols = p.total_k > 0 ? uint64_t(p.heads) * kKvHead : 64;
+    if (!encode_2d(&mq, p.q, uint64_t(p.heads) * kQk, uint64_t(p.total_q), kTileRows) ||
+        !encode_2d(&mk, kv_base, kv_cols, k_rows, kStep) ||
+        !encode_2d(&mv, kv_base, kv_cols, k_rows, kStep / 2) ||
+        !encode_2d(&mpe, pe_base, kRope, k_rows, kStep))
+        return int(cudaErrorInvalidValue);
+    const cudaError_t e = cudaFuncSetAttribute(
+        mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return int(e);
+    const int64_t most = (int64_t(p.total_q) / kItemRows + p.batch) * p.heads * p.splits;
+    const unsigned grid = unsigned(most < num_sms ? most : num_sms);
+    mla_prefill_kernel<<<grid, kThreads, kSmemBytes, st>>>(p, mq, mk, mv, mpe);
+    return int(cudaGetLastError());
+}
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
@@ -957,12 +940,16 @@ uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
 // A split should have at least this many key steps: fewer cost more in items
 // and merging than the extra CTAs bring.
 constexpr int kMinSplitSteps = 4;
+// The single-row kernel: CTAs an SM that its splits aim at, and the fewest
+// keys of a split.
+constexpr int kRowCtasPerSm = 4;
+constexpr int kMinSplitKeys = 128;
 
 void layout(mla_prefill_plan_t* p) {
     p->partial_offset = kStatusBytes;
     p->lse_partial_offset = kStatusBytes;
     p->workspace_bytes = kStatusBytes;
-    if (p->num_kv_splits > 1) {
+    if (p->num_kv_splits > 1 && !p->single_rows) {
         const uint64_t rows = uint64_t(p->total_q) * p->num_heads * p->num_kv_splits;
         p->lse_partial_offset = p->partial_offset + round256(rows * kV * 4);
         p->workspace_bytes = p->lse_partial_offset + round256(rows * 4);
@@ -988,18 +975,33 @@ extern "C" int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q
     p.total_q = total_q;
     p.num_sms = num_sms;
     p.num_kv_splits = num_kv_splits;
+    // One query row a sequence: HBM is the bound. (Measured, tensor kernel
+    // against single-row kernel: 8 sequences of 816 keys, 16 heads, one row
+    // each 21.6 and 9.8 us, two rows each 21.6 and 24.7 us; 64 sequences of
+    // 2,048 keys, one row 202 and 175 us.)
+    p.single_rows = max_q_len <= 1 ? 1 : 0;
     if (num_kv_splits == 0) {
-        // Split only while the items leave SMs idle.
-        const int64_t per_seq = (int64_t(max_q_len) + kItemRows - 1) / kItemRows;
+        const int rows = p.single_rows ? 1 : kItemRows;
+        const int64_t per_seq = (int64_t(max_q_len) + rows - 1) / rows;
         int64_t tiles = batch * per_seq;
-        const int64_t bound = int64_t(total_q) / kItemRows + batch;
+        const int64_t bound = int64_t(total_q) / rows + batch;
         if (tiles > bound) tiles = bound;
         const int64_t items = tiles * num_heads;
-        const int64_t steps = (int64_t(max_k_len) + kStep - 1) / kStep;
-        int64_t s = items > 0 ? num_sms / items : 1;
-        if (s > steps / kMinSplitSteps) s = steps / kMinSplitSteps;
+        // Split while the items leave room: of the tensor kernel's one CTA
+        // per SM, of the other's kRowCtasPerSm.
+        const int64_t slots = p.single_rows ? int64_t(num_sms) * kRowCtasPerSm : num_sms;
+        const int64_t most =
+            p.single_rows ? max_k_len / kMinSplitKeys : max_k_len / (kStep * kMinSplitSteps);
+        int64_t s = items > 0 ? slots / items : 1;
+        if (s > most) s = most;
         if (s > kMaxSplits) s = kMaxSplits;
         p.num_kv_splits = s < 1 ? 1 : int(s);
+    }
+    if (p.single_rows) {
+        // The splits are a cluster: 1, 2, 4 or 8.
+        int s = 1;
+        while (2 * s <= p.num_kv_splits && s < kMaxRowSplits) s *= 2;
+        p.num_kv_splits = s;
     }
     layout(&p);
     *plan = p;
@@ -1013,7 +1015,10 @@ extern "C" int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const 
     if (!plan) return MLA_ERR_INVALID_ARG;
     if (plan->batch < 0 || plan->num_heads < 1 || plan->num_heads > kMaxHeads ||
         plan->total_q < 0 || plan->num_kv_splits < 1 || plan->num_kv_splits > kMaxSplits ||
-        plan->num_sms < 1 || total_k < 0)
+        plan->num_sms < 1 || (plan->single_rows & ~1) != 0 || total_k < 0)
+        return MLA_ERR_INVALID_ARG;
+    if (plan->single_rows &&
+        (plan->num_kv_splits > kMaxRowSplits || (plan->num_kv_splits & (plan->num_kv_splits - 1))))
         return MLA_ERR_INVALID_ARG;
     mla_prefill_plan_t check = *plan;
     layout(&check);
@@ -1033,7 +1038,9 @@ extern "C" int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const 
         return MLA_ERR_INVALID_ARG;
     PrefillParams p{};
     char* ws = static_cast<char*>(workspace);
+    p.q = static_cast<const uint16_t*>(q);
     p.kv = static_cast<const uint16_t*>(kv);
+    p.k_pe = static_cast<const uint16_t*>(k_pe);
     p.cu_q = cu_seqlens_q;
     p.cu_k = cu_seqlens_k;
     p.batch = plan->batch;
@@ -1050,30 +1057,11 @@ extern "C" int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const 
     p.status = reinterpret_cast<int32_t*>(ws);
     p.ticket = reinterpret_cast<unsigned long long*>(ws + 4 * kTicketWord);
     p.done = reinterpret_cast<uint32_t*>(ws + 4 * kDoneCtasWord);
-    const int64_t head_bytes = int64_t(total_k) * kKvHead * 2;
-    const int64_t group = head_bytes > 0 ? kGroupBytes / head_bytes : p.heads;
-    p.group = group < 1 ? 1 : group > p.heads ? p.heads : int(group);
-    // (Without keys the maps over them are never read through; the queries
-    // stand in.)
-    CUtensorMap mq, mk, mv, mpe;
-    const void* kv_base = total_k > 0 ? kv : q;
-    const void* pe_base = total_k > 0 ? k_pe : q;
-    const uint64_t k_rows = total_k > 0 ? uint64_t(total_k) : 1;
-    const uint64_t kv_cols = total_k > 0 ? uint64_t(p.heads) * kKvHead : 64;
-    if (!encode_2d(&mq, q, uint64_t(p.heads) * kQk, uint64_t(p.total_q), kTileRows) ||
-        !encode_2d(&mk, kv_base, kv_cols, k_rows, kStep) ||
-        !encode_2d(&mv, kv_base, kv_cols, k_rows, kStep / 2) ||
-        !encode_2d(&mpe, pe_base, kRope, k_rows, kStep))
-        return MLA_ERR_CUDA;
-    if (cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes) != cudaSuccess)
-        return MLA_ERR_CUDA;
-    const int64_t most = (int64_t(p.total_q) / kItemRows + p.batch) * p.heads * p.splits;
-    const unsigned grid = unsigned(most < plan->num_sms ? most : plan->num_sms);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    mla_prefill_kernel<<<grid, kThreads, kSmemBytes, st>>>(p, mq, mk, mv, mpe);
-    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-    if (p.splits > 1) {
+    const int e = plan->single_rows ? launch_prefill_row(p, stream)
+                                    : launch_prefill_tiles(p, plan->num_sms, st);
+    if (e != 0) return MLA_ERR_CUDA;
+    if (p.splits > 1 && !plan->single_rows) {
         const int64_t rows = int64_t(p.total_q) * p.heads;
         prefill_merge_kernel<<<unsigned((rows + 7) / 8), 256, 0, st>>>(p);
         if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;

@@ -49,8 +49,10 @@ def _problem(seed, q_lens, k_lens, heads, q_scale=1.0):
             _bf16(rng, (sum(k_lens), 64)))
 
 
-def _run(q, kv, pe, q_lens, k_lens, causal, splits=0, spare=0, scale=SCALE, **kw):
-    """(out bits, lse) of one call; `spare` rows follow the last sequence."""
+def _run(q, kv, pe, q_lens, k_lens, causal, splits=0, spare=0, scale=SCALE, max_q=None, **kw):
+    """(out bits, lse) of one call; `spare` rows follow the last sequence.
+    `max_q` (the plan's longest query length) picks the kernel: 1 the CUDA-core
+    kernel for single rows, more the tensor cores'."""
     import torch
     heads = kv.shape[1]
     if spare:
@@ -59,8 +61,10 @@ def _run(q, kv, pe, q_lens, k_lens, causal, splits=0, spare=0, scale=SCALE, **kw
         pe = np.concatenate([pe, np.full((spare, 64), 0x7FC0, np.uint16)])
     out = _dev(np.full((q.shape[0], heads, 128), FILL, np.uint16))
     lse = torch.full((q.shape[0], heads), 77.0, device="cuda")
-    plan = binding.make_prefill_plan(len(q_lens), heads, q.shape[0], max(q_lens, default=0),
+    plan = binding.make_prefill_plan(len(q_lens), heads, q.shape[0],
+                                     max(q_lens, default=0) if max_q is None else max_q,
                                      max(k_lens, default=0), num_kv_splits=splits)
+    assert plan.single_rows == ((max(q_lens, default=0) if max_q is None else max_q) <= 1)
     ws = binding.new_workspace(plan)
     binding.mla_prefill(_dev(q), _dev(kv), _dev(pe), _int(_starts(q_lens)), _int(_starts(k_lens)),
                         scale, causal=causal, plan=plan, workspace=ws, out=out, lse=lse, **kw)
@@ -113,28 +117,31 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("max_q", [1, 1000])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("case", range(len(CASES)))
-def test_prefill_against_the_oracle(case, causal):
+def test_prefill_against_the_oracle(case, causal, max_q):
     q_lens, k_lens, heads = CASES[case]
     q, kv, pe = _problem(700 + case, q_lens, k_lens, heads)
-    bits, lse = _run(q, kv, pe, q_lens, k_lens, causal, spare=5)
+    bits, lse = _run(q, kv, pe, q_lens, k_lens, causal, spare=5, max_q=max_q)
     _check(bits, lse, q, kv, pe, q_lens, k_lens, causal)
 
 
+@pytest.mark.parametrize("max_q", [1, 1000])
 @pytest.mark.parametrize("splits", [1, 2, 3, 7, 64])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("case", [2, 5, 8, 9, 12, 14])
-def test_prefill_with_split_keys(case, causal, splits):
+def test_prefill_with_split_keys(case, causal, splits, max_q):
     q_lens, k_lens, heads = CASES[case]
     q, kv, pe = _problem(800 + case, q_lens, k_lens, heads, q_scale=2.0)
-    bits, lse = _run(q, kv, pe, q_lens, k_lens, causal, splits=splits, spare=3)
+    bits, lse = _run(q, kv, pe, q_lens, k_lens, causal, splits=splits, spare=3, max_q=max_q)
     _check(bits, lse, q, kv, pe, q_lens, k_lens, causal)
 
 
+@pytest.mark.parametrize("max_q", [1, 1000])
 @pytest.mark.parametrize("splits", [1, 3])
 @pytest.mark.parametrize("order", ["rising", "falling", "far below"])
-def test_prefill_as_the_reference_maximum_moves(order, splits):
+def test_prefill_as_the_reference_maximum_moves(order, splits, max_q):
     """Scores that climb by far more than the rescale threshold step after
     step, that only fall, and that are all far below zero."""
     rng = np.random.default_rng(31)
@@ -148,24 +155,25 @@ def test_prefill_as_the_reference_maximum_moves(order, splits):
     kv[..., :128] = 0.1 * kv[..., :128] + height[:, None, None] * direction[None, :, :128]
     q = np.repeat(direction[None], 200, 0) * rng.uniform(10, 20, (200, 1, 1))
     q, kv, pe = (f32_to_bf16_bits(x.astype(np.float32)) for x in (q, kv, pe))
-    bits, lse = _run(q, kv, pe, [200], [n], True, splits=splits)
+    bits, lse = _run(q, kv, pe, [200], [n], True, splits=splits, max_q=max_q)
     _check(bits, lse, q, kv, pe, [200], [n], True)
 
 
+@pytest.mark.parametrize("max_q", [1, 1000])
 @pytest.mark.parametrize("splits", [1, 2])
 @pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
-def test_what_a_query_does_not_see_does_not_reach_it(value, splits):
+def test_what_a_query_does_not_see_does_not_reach_it(value, splits, max_q):
     """Non-finite keys and values at positions from `at` on: queries before
     `at` keep their results bit for bit, later ones see them."""
     q_lens, k_lens, heads = [300, 200], [420, 200], 2
     q, kv, pe = _problem(41, q_lens, k_lens, heads)
-    clean, clean_lse = _run(q, kv, pe, q_lens, k_lens, True, splits=splits)
+    clean, clean_lse = _run(q, kv, pe, q_lens, k_lens, True, splits=splits, max_q=max_q)
     bad = f32_to_bf16_bits(np.array([value], dtype=np.float32))[0]
     starts_q, starts_k = _starts(q_lens), _starts(k_lens)
     for seq, at, col in [(0, 419, 130), (0, 300, 255), (1, 0, 128), (1, 77, 200), (0, 130, 180)]:
         x = kv.copy()
         x[starts_k[seq] + at, 1, col] = bad
-        got, lse = _run(q, x, pe, q_lens, k_lens, True, splits=splits)
+        got, lse = _run(q, x, pe, q_lens, k_lens, True, splits=splits, max_q=max_q)
         want = bf16_bits_to_f64(clean).copy()
         rows = starts_q[seq] + max(0, at - (k_lens[seq] - q_lens[seq]))
         want[rows:starts_q[seq + 1], 1, col - 128] = value
@@ -175,7 +183,7 @@ def test_what_a_query_does_not_see_does_not_reach_it(value, splits):
     x, y = kv.copy(), pe.copy()
     x[starts_k[0] + 400, 0, 5] = 0x7FC0
     y[starts_k[1] + 190, 3] = 0x7FC0
-    got, lse = _run(q, x, y, q_lens, k_lens, True, splits=splits)
+    got, lse = _run(q, x, y, q_lens, k_lens, True, splits=splits, max_q=max_q)
     keep = np.ones((500, 2), dtype=bool)
     keep[280:300, 0] = False
     keep[490:500, :] = False
@@ -184,28 +192,30 @@ def test_what_a_query_does_not_see_does_not_reach_it(value, splits):
     # queries: their own rows only
     x = q.copy()
     x[100, 1, 7] = 0x7FC0
-    got, lse = _run(x, kv, pe, q_lens, k_lens, True, splits=splits)
+    got, lse = _run(x, kv, pe, q_lens, k_lens, True, splits=splits, max_q=max_q)
     keep = np.ones((500, 2), dtype=bool)
     keep[100, 1] = False
     assert np.array_equal(got[keep], clean[keep])
     assert np.isnan(bf16_bits_to_f64(got)[100, 1]).all()
 
 
-def test_both_infinities_seen_give_nan():
+@pytest.mark.parametrize("max_q", [1, 1000])
+def test_both_infinities_seen_give_nan(max_q):
     q, kv, pe = _problem(42, [10], [140], 1)
     kv[135, 0, 128 + 9], kv[138, 0, 128 + 9] = 0x7F80, 0xFF80
-    bits, _ = _run(q, kv, pe, [10], [140], True)
+    bits, _ = _run(q, kv, pe, [10], [140], True, max_q=max_q)
     col = bf16_bits_to_f64(bits)[:, 0, 9]
     assert np.isfinite(col[:5]).all() and (col[5:8] == np.inf).all() and np.isnan(col[8:]).all()
 
 
-def test_scores_of_the_lowest_value():
+@pytest.mark.parametrize("max_q", [1, 1000])
+def test_scores_of_the_lowest_value(max_q):
     """A key of the type's lowest value gives scores of -inf or near it: its
     weight is 0; a row that sees nothing else has no sum."""
     q, kv, pe = _problem(43, [4], [4], 1)
     q[:, 0, 0] = 0x7F7F                    # the largest finite bf16
     kv[:2, 0, 0] = 0xFF7F
-    bits, lse = _run(q, kv, pe, [4], [4], True)
+    bits, lse = _run(q, kv, pe, [4], [4], True, max_q=max_q)
     assert np.isneginf(lse[:2, 0]).all() and (bits[:2] == 0).all()
     assert not np.isneginf(lse[2:, 0]).any()
 
@@ -215,8 +225,8 @@ def test_prefill_is_deterministic_and_replays_in_a_graph():
     q_lens, k_lens, heads = [300, 77, 1], [300, 500, 900], 4
     q, kv, pe = _problem(51, q_lens, k_lens, heads)
     args = (_dev(q), _dev(kv), _dev(pe), _int(_starts(q_lens)), _int(_starts(k_lens)))
-    for splits in (1, 4):
-        plan = binding.make_prefill_plan(3, heads, sum(q_lens), 300, 900, num_kv_splits=splits)
+    for splits, max_q in ((1, 300), (4, 300), (1, 1), (4, 1)):
+        plan = binding.make_prefill_plan(3, heads, sum(q_lens), max_q, 900, num_kv_splits=splits)
         ws = binding.new_workspace(plan)
         out, lse = binding.mla_prefill(*args, SCALE, plan=plan, workspace=ws)
         torch.cuda.synchronize()

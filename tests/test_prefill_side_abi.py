@@ -179,8 +179,15 @@ def test_prefill_plan_layout_and_splits(lib):
     assert p.workspace_bytes >= p.lse_partial_offset + rows * 4 and p.workspace_bytes % 256 == 0
     # split only while SMs would idle, and only keys that are long enough
     assert _plan(lib, batch=1, heads=16, total_q=1, max_q=1, max_k=8192)[1].num_kv_splits > 1
-    assert _plan(lib, batch=1, heads=16, total_q=1, max_q=1, max_k=300)[1].num_kv_splits == 1
+    assert _plan(lib, batch=1, heads=16, total_q=200, max_q=200, max_k=300)[1].num_kv_splits == 1
     assert _plan(lib, batch=8, heads=128, total_q=8, max_q=1, max_k=8192)[1].num_kv_splits == 1
+    assert _plan(lib, batch=1, heads=16, total_q=200, max_q=200, max_k=8192)[1].num_kv_splits > 1
+    # the kernel follows from the longest query length
+    for splits, got in [(1, 1), (3, 2), (7, 4), (64, 8)]:
+        rc, p = _plan(lib, max_q=1, splits=splits)
+        assert rc == 0 and p.num_kv_splits == got and p.workspace_bytes == binding.STATUS_BYTES
+    for max_q, rows in [(0, 1), (1, 1), (2, 0), (4096, 0)]:
+        assert _plan(lib, total_q=5000, max_q=max_q)[1].single_rows == rows
 
 
 def test_prefill_plan_struct_matches_the_header(tmp_path):
@@ -236,7 +243,8 @@ def test_prefill_refusals(lib, kw, code):
 @pytest.mark.parametrize("field,value", [("workspace_bytes", 8192), ("partial_offset", 0),
                                          ("lse_partial_offset", 8192), ("num_kv_splits", 0),
                                          ("num_kv_splits", 2), ("num_heads", 200), ("batch", -1),
-                                         ("total_q", -5), ("num_sms", 0)])
+                                         ("total_q", -5), ("num_sms", 0),
+                                         ("single_rows", 2), ("single_rows", -1)])
 def test_prefill_refuses_an_edited_plan(lib, field, value):
     plan = _plan(lib, splits=3)[1]
     setattr(plan, field, value)
