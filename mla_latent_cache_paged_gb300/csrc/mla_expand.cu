@@ -503,8 +503,8 @@ int launch_expand(const ExpandParams& p, const void* w_uk_t, const void* w_uv, i
         !encode_2d(&uv, w_uv, kHalf, uint64_t(p.heads) * kLkv, kChunk))
         return int(cudaErrorInvalidValue);
     auto kernel = mla_expand_kernel<kEntryBytes>;
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_shared_memory(kernel, kSmemBytes, &allowed);
     if (e != cudaSuccess) return int(e);
     const unsigned grid = unsigned(p.items < num_sms ? p.items : num_sms);
     kernel<<<grid, kThreads, kSmemBytes, st>>>(p, uk, uv);

@@ -330,8 +330,7 @@ struct ItemReader {
 
 __global__ void __launch_bounds__(kThreads, 1)
 mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap map_q,
-                   const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ CUtensorMap map_kv,
                    const __grid_constant__ CUtensorMap map_pe) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = ptx::smem_addr(smem);
@@ -402,13 +401,17 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                         const int row = it.k_row + j * kStep;
                         const uint32_t bar = MLA_BAR(k_full) + 8 * (step & 1);
                         ptx::mbar_arrive_expect_tx(bar, 3 * kBlock);
-                        ptx::tma_load_2d(addr(5 * step), &map_k, it.head * kKvHead, row, bar);
+                        // (boxes of 64 rows; a block of keys takes two)
+                        auto load_keys = [&](uint32_t dst, int x) {
+                            ptx::tma_load_2d(dst, &map_kv, x, row, bar);
+                            ptx::tma_load_2d(dst + kBlock / 2, &map_kv, x, row + kStep / 2, bar);
+                        };
+                        load_keys(addr(5 * step), it.head * kKvHead);
                         if (step >= 2)
                             ok = wait(MLA_BAR(v_empty), step & 1, bars, p.status, kSiteRingFree);
                         // (after an abort the phase's other bytes still come, so
                         // that the drain below ends)
-                        ptx::tma_load_2d(addr(5 * step + (ok ? 1 : 0)), &map_k,
-                                         it.head * kKvHead + 64, row, bar);
+                        load_keys(addr(5 * step + (ok ? 1 : 0)), it.head * kKvHead + 64);
                         ptx::tma_load_2d(addr(5 * step + (ok ? 2 : 0)), &map_pe, 0, row, bar);
                         if (j == it.step_lo) {
 #pragma unroll
@@ -445,8 +448,8 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                         for (int c = 0; c < 2; ++c) {
                             const int x = it.head * kKvHead + 128, y = row + 64 * c;
                             const uint32_t dst = addr(5 * step + 3 + c);
-                            ptx::tma_load_2d(dst, &map_v, x, y, v_bar);
-                            ptx::tma_load_2d(dst + 8192, &map_v, x + 64, y, v_bar);
+                            ptx::tma_load_2d(dst, &map_kv, x, y, v_bar);
+                            ptx::tma_load_2d(dst + 8192, &map_kv, x + 64, y, v_bar);
                         }
                     }
                     items.release();
@@ -914,22 +917,21 @@ int launch_prefill_tiles(PrefillParams p, int num_sms, cudaStream_t st) {
     p.group = group < 1 ? 1 : group > p.heads ? p.heads : int(group);
     // (Without keys the maps over them are never read through; the queries
     // stand in.)
-    CUtensorMap mq, mk, mv, mpe;
+    CUtensorMap mq, mkv, mpe;
     const void* kv_base = p.total_k > 0 ? p.kv : p.q;
     const void* pe_base = p.total_k > 0 ? p.k_pe : p.q;
     const uint64_t k_rows = p.total_k > 0 ? uint64_t(p.total_k) : 1;
     const uint64_t kv_cols = p.total_k > 0 ? uint64_t(p.heads) * kKvHead : 64;
     if (!encode_2d(&mq, p.q, uint64_t(p.heads) * kQk, uint64_t(p.total_q), kTileRows) ||
-        !encode_2d(&mk, kv_base, kv_cols, k_rows, kStep) ||
-        !encode_2d(&mv, kv_base, kv_cols, k_rows, kStep / 2) ||
+        !encode_2d(&mkv, kv_base, kv_cols, k_rows, kStep / 2) ||
         !encode_2d(&mpe, pe_base, kRope, k_rows, kStep))
         return int(cudaErrorInvalidValue);
-    const cudaError_t e = cudaFuncSetAttribute(
-        mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_shared_memory(mla_prefill_kernel, kSmemBytes, &allowed);
     if (e != cudaSuccess) return int(e);
     const int64_t most = (int64_t(p.total_q) / kItemRows + p.batch) * p.heads * p.splits;
     const unsigned grid = unsigned(most < num_sms ? most : num_sms);
-    mla_prefill_kernel<<<grid, kThreads, kSmemBytes, st>>>(p, mq, mk, mv, mpe);
+    mla_prefill_kernel<<<grid, kThreads, kSmemBytes, st>>>(p, mq, mkv, mpe);
     return int(cudaGetLastError());
 }
 

@@ -6,9 +6,24 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdint>
 
 namespace mla {
+
+// Let `kernel` use `bytes` of dynamic shared memory on the current device; a
+// call sets it the first time it is made there. `done` has a bit per device.
+template <typename Kernel>
+cudaError_t allow_shared_memory(Kernel kernel, int bytes, std::atomic<uint64_t>* done) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if ((done->load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // The driver's encoder, looked up once (null if there is none).
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
