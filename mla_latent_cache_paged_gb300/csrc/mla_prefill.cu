@@ -92,10 +92,11 @@ struct Item {
 };
 
 struct Bars {
-    // Steps alternate between the two of a pair; the single ones complete
-    // once per step (nobody can be two steps behind them).
+    // Steps alternate between the two of a pair: a waiter tells a phase from
+    // its predecessor only, and the loads may be two releases behind the MMAs
+    // (they wait for an item between two steps), but never a whole pair.
     uint64_t k_full[2], v_full[2];
-    uint64_t k_empty, v_empty;
+    uint64_t k_empty[2], v_empty[2];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];       // scores of the step complete
     uint64_t p_ready[2];      // 128 arrivals: weights in TMEM, O rescaled
@@ -345,11 +346,11 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
         return;
     }
     if (threadIdx.x == 0) {
-        ptx::mbar_init(MLA_BAR(k_empty), 1);
-        ptx::mbar_init(MLA_BAR(v_empty), 1);
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(MLA_BAR(k_full) + 8 * t, 1);
             ptx::mbar_init(MLA_BAR(v_full) + 8 * t, 1);
+            ptx::mbar_init(MLA_BAR(k_empty) + 8 * t, 1);
+            ptx::mbar_init(MLA_BAR(v_empty) + 8 * t, 1);
             ptx::mbar_init(MLA_BAR(raw_full) + 8 * t, 1);
             ptx::mbar_init(MLA_BAR(q_full) + 8 * t, 1);
             ptx::mbar_init(MLA_BAR(q_empty) + 8 * t, 1);
@@ -408,7 +409,8 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                         };
                         load_keys(addr(5 * step), it.head * kKvHead);
                         if (step >= 2)
-                            ok = wait(MLA_BAR(v_empty), step & 1, bars, p.status, kSiteRingFree);
+                            ok = wait(MLA_BAR(v_empty) + 8 * (step & 1), ((step - 2) >> 1) & 1,
+                                      bars, p.status, kSiteRingFree);
                         // (after an abort the phase's other bytes still come, so
                         // that the drain below ends)
                         load_keys(addr(5 * step + (ok ? 1 : 0)), it.head * kKvHead + 64);
@@ -431,8 +433,8 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                             }
                         }
                         if (step >= 1)
-                            ok = ok && wait(MLA_BAR(k_empty), (step - 1) & 1, bars, p.status,
-                                            kSiteRingFree);
+                            ok = ok && wait(MLA_BAR(k_empty) + 8 * ((step - 1) & 1),
+                                            ((step - 1) >> 1) & 1, bars, p.status, kSiteRingFree);
                         if (!ok) {
                             ++step;
                             raw_last[(step - 1) & 1] = true;   // no values were asked for
@@ -533,7 +535,7 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                             if (it.step_hi[t] == it.step_lo + 1)
                                 ptx::mma_commit(MLA_BAR(q_empty) + 8 * t);
                         }
-                        if (ok) ptx::mma_commit(MLA_BAR(k_empty));
+                        if (ok) ptx::mma_commit(MLA_BAR(k_empty) + 8 * (step & 1));
                     }
                     // Per step: P.V of the step and the scores of the next,
                     // tile after tile.
@@ -554,7 +556,7 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                                 ptx::tc_fence_after();
                                 values(t, step, j == it.step_lo);
                             }
-                            if (t == 1) ptx::mma_commit(MLA_BAR(v_empty));
+                            if (t == 1) ptx::mma_commit(MLA_BAR(v_empty) + 8 * (step & 1));
                             if (j + 1 < it.step_hi[t]) {
                                 if (!have_k)
                                     ok = wait(MLA_BAR(k_full) + 8 * ((step + 1) & 1),
@@ -567,7 +569,8 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                                     ptx::mma_commit(MLA_BAR(q_empty) + 8 * t);
                             }
                         }
-                        if (ok && j + 1 < steps) ptx::mma_commit(MLA_BAR(k_empty));
+                        if (ok && j + 1 < steps)
+                            ptx::mma_commit(MLA_BAR(k_empty) + 8 * ((step + 1) & 1));
                     }
                     items.release();
                 }

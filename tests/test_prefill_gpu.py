@@ -266,6 +266,38 @@ def test_prefill_on_two_streams_at_once():
         assert torch.equal(out, results[i % 2][0])
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("splits", [1, 2, 3, 8])
+def test_many_items_of_few_steps(splits, causal):
+    """Several items per SM, many without steps of their own: the loads wait
+    for an item between two steps, and every split gives the same result."""
+    import torch
+    rng = np.random.default_rng(5)
+    q_lens = [int(x) for x in rng.integers(2, 700, 24)]
+    k_lens = [n + (0 if b % 3 else int(rng.integers(0, 900))) for b, n in enumerate(q_lens)]
+    heads = 16
+    q, kv, pe = _problem(55, q_lens, k_lens, heads)
+    args = (_dev(q), _dev(kv), _dev(pe), _int(_starts(q_lens)), _int(_starts(k_lens)))
+    ref, ref_lse = None, None
+    plan = binding.make_prefill_plan(24, heads, sum(q_lens), max(q_lens), max(k_lens),
+                                     num_kv_splits=splits)
+    ws = binding.new_workspace(plan)
+    for _ in range(30):
+        out, lse = binding.mla_prefill(*args, SCALE, causal=causal, plan=plan, workspace=ws)
+        torch.cuda.synchronize()
+        assert binding.read_error(ws) == 0
+        if ref is None:
+            ref, ref_lse = out, lse
+        assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    # three of the sequences and two heads against the definition
+    bits, z = bf16_tensor_bits(ref), ref_lse.cpu().numpy().astype(np.float64)
+    starts_q, starts_k = _starts(q_lens), _starts(k_lens)
+    for b in (0, 9, 23):
+        rq, rk = slice(starts_q[b], starts_q[b + 1]), slice(starts_k[b], starts_k[b + 1])
+        _check(bits[rq, 3:5], z[rq, 3:5], q[rq, 3:5], kv[rk, 3:5], pe[rk], [q_lens[b]],
+               [k_lens[b]], causal)
+
+
 def test_prefill_without_lse_plan_and_workspace():
     q, kv, pe = _problem(71, [50], [60], 2)
     out, lse = binding.mla_prefill(_dev(q), _dev(kv), _dev(pe), _int([0, 50]), _int([0, 60]), SCALE,
