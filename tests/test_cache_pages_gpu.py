@@ -384,3 +384,70 @@ def test_pages_calls_replay_in_a_graph():
         assert np.array_equal(_host(out), want[0]) and np.array_equal(_host(out2), ref)
         assert int(freed) == sum(-(-n // 64) for n in [400, 64, 300, 10, 1, 640]) - \
             sum(s // 64 for s in [389, 64, 100, 0, 1, 389])
+
+
+def test_page_operations_on_two_streams_at_once():
+    """Two pools, two streams, nothing between the calls: every result is the
+    one that a stream of its own gives."""
+    import torch
+    rng = np.random.default_rng(21)
+    pools = []
+    for blocks in (900, 1500):
+        table, ref = _state(rng, blocks, [64 * 7 + 9] * 30, max_blocks=12)
+        bits, cache = _cache(rng, (3, blocks, 64, 576), False)
+        kids = [(int(rng.integers(0, 30)), int(rng.integers(0, 458)), 500) for _ in range(40)]
+        want = cache_fork(ref, table, *zip(*kids))
+        pools.append(dict(cache=cache, refs=_dev(ref), table=_dev(table), want=want, bits=bits,
+                          kids=[_dev(x) for x in zip(*kids)], out=_dev(np.zeros(blocks)),
+                          back=_dev(np.zeros(blocks)), child=_dev(np.full((40, 12), -1)),
+                          rows=_dev(np.arange(40)), lens=_dev([500] * 40), freed=_dev([0]),
+                          ref=ref, ws=binding.new_cache_workspace(blocks, 40),
+                          stream=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p in pools:
+            binding.mla_cache_fork(p["cache"], p["refs"], p["table"], *p["kids"], workspace=p["ws"],
+                                   child_table=p["child"], ref_counts_out=p["out"],
+                                   stream=p["stream"])
+            binding.mla_cache_free(p["out"], p["child"], p["lens"], p["rows"], workspace=p["ws"],
+                                   ref_counts_out=p["back"], num_freed=p["freed"],
+                                   stream=p["stream"])
+    torch.cuda.synchronize()
+    for p in pools:
+        assert binding.read_error(p["ws"]) == 0
+        assert np.array_equal(_host(p["out"]), p["want"][0])
+        assert np.array_equal(_host(p["back"]), p["ref"])
+        for src, dst, rows in p["want"][2]:
+            p["bits"][:, dst, :rows] = p["bits"][:, src, :rows]
+        assert np.array_equal(_host(p["cache"]), p["bits"])
+
+
+def test_a_pool_of_many_chunks_and_a_cache_past_2_31_bytes():
+    """700,000 pages' counts (more chunks than a grid has CTAs), and pages
+    behind the first 2^31 bytes of a layer."""
+    import torch
+    rng = np.random.default_rng(22)
+    blocks = 700_000
+    ref = (rng.random(blocks) < 0.5).astype(np.int32)
+    live = np.flatnonzero(ref)
+    table = live[-64:].reshape(1, -1).astype(np.int32)
+    ws = binding.new_status_workspace()
+    got, freed = binding.mla_cache_free(_dev(ref), _dev(table), _dev([64 * 64]), _dev([0]),
+                                        workspace=ws, ref_counts_out=_dev(np.zeros(blocks)))
+    assert binding.read_error(ws) == 0 and int(freed) == 64
+    assert np.array_equal(_host(got), np.where(np.isin(np.arange(blocks), table), 0, ref))
+    blocks = 70_000
+    ref = np.zeros(blocks, dtype=np.int32)
+    ref[-3000:] = 1
+    cache = torch.zeros((blocks, 64, 576), dtype=torch.uint8, device="cuda")
+    cache[-3000:] = torch.arange(3000, device="cuda").remainder(251).to(torch.uint8)[:, None, None]
+    ws = binding.new_cache_workspace(blocks)
+    refs = _dev(ref)
+    table = _dev(np.arange(blocks - 3000, blocks).reshape(3, 1000))
+    table, _, page_map, live = binding.mla_cache_compact(cache, refs, table, _dev([64000] * 3),
+                                                         workspace=ws)
+    assert binding.read_error(ws) == 0 and int(live) == 3000
+    assert np.array_equal(_host(table).reshape(-1), np.arange(3000))
+    assert torch.equal(cache[:3000, 0, 0].long(),
+                       torch.arange(3000, device="cuda").remainder(251))
+    assert bool((cache[:3000] == cache[:3000, :1, :1]).all())

@@ -153,6 +153,50 @@ def test_expand_of_bad_pages_gives_zeros_and_an_error(what):
         assert (err <= 2.0 ** -8 * np.abs(ref[~bad]) + 512 * 2.0 ** -23 * 512).all()
 
 
+def test_expand_from_and_to_offsets_past_2_31_elements():
+    """Pages at the end of a cache of 60,000 (2.2 G elements), into the rows at
+    the end of 70,000 x 128 x 256 (2.3 G elements)."""
+    import torch
+    rng = np.random.default_rng(13)
+    lens, heads, blocks, rows = [150], 128, 60000, 70000
+    cache, table, w_uk, w_uv = _problem(rng, lens, [0], heads, False)
+    big = torch.zeros((blocks, 64, 576), dtype=torch.bfloat16, device="cuda")
+    big[blocks - len(cache):] = _dev(cache)
+    kv = torch.zeros((rows, heads, 256), dtype=torch.bfloat16, device="cuda")
+    pe = torch.zeros((rows, 64), dtype=torch.bfloat16, device="cuda")
+    ws = binding.new_status_workspace()
+    binding.mla_expand_kv(big, _int(table[:, :3] + blocks - len(cache)),
+                          _int([rows - 150, rows]), _dev(w_uk), _dev(w_uv), total_k=rows,
+                          workspace=ws, kv=kv, k_pe=pe)
+    torch.cuda.synchronize()
+    assert binding.read_error(ws) == 0
+    _check(bf16_bits_to_f64(bf16_tensor_bits(kv[-150:])),
+           bf16_bits_to_f64(bf16_tensor_bits(pe[-150:])), cache, 1.0, table, [0], lens, w_uk, w_uv,
+           False)
+    assert not kv[:-150].any() and not pe[:-150].any()
+
+
+def test_expand_replays_in_a_graph():
+    import torch
+    rng = np.random.default_rng(14)
+    lens, first = [300, 70], [5, 64]
+    cache, table, w_uk, w_uv = _problem(rng, lens, first, 3, False)
+    args = (_dev(cache), _int(table), _int([0, 300, 370]), _dev(w_uk), _dev(w_uv))
+    ws, start = binding.new_status_workspace(), _int(first)
+    want = binding.mla_expand_kv(*args, total_k=370, workspace=ws, first_token=start)
+    kv, pe = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    torch.cuda.synchronize()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        binding.mla_expand_kv(*args, total_k=370, workspace=ws, first_token=start, kv=kv, k_pe=pe,
+                              stream=stream)
+    for _ in range(2):
+        kv.zero_(), pe.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kv, want[0]) and torch.equal(pe, want[1])
+
+
 def test_expand_with_starts_that_make_no_sense_stays_in_bounds():
     """Decreasing or oversized starts: what is written lies in the outputs."""
     import torch

@@ -114,6 +114,7 @@ CASES = [
     ([17], [2000], 5),
     ([33, 90], [128, 384], 16),
     ([3], [260], 128),
+    ([3, 2], [0, 0], 2),                 # no keys at all
 ]
 
 
@@ -296,6 +297,36 @@ def test_many_items_of_few_steps(splits, causal):
         rq, rk = slice(starts_q[b], starts_q[b + 1]), slice(starts_k[b], starts_k[b + 1])
         _check(bits[rq, 3:5], z[rq, 3:5], q[rq, 3:5], kv[rk, 3:5], pe[rk], [q_lens[b]],
                [k_lens[b]], causal)
+
+
+@pytest.mark.parametrize("max_q", [1, 1000])
+def test_prefill_of_many_short_sequences(max_q):
+    rng = np.random.default_rng(6)
+    q_lens = [int(x) for x in rng.integers(0, 4, 700)]
+    k_lens = [int(x) for x in rng.integers(0, 40, 700)]
+    q, kv, pe = _problem(56, q_lens, k_lens, 2)
+    bits, lse = _run(q, kv, pe, q_lens, k_lens, True, max_q=max_q, spare=2)
+    _check(bits, lse, q, kv, pe, q_lens, k_lens, True)
+
+
+@pytest.mark.parametrize("max_q", [1, 1000])
+def test_prefill_behind_the_first_2_31_elements(max_q):
+    """kv of 70,000 tokens x 128 heads x 256: the last sequence lies past 2^31
+    elements; the first takes the rest as keys that are not looked at here."""
+    import torch
+    heads, lk, lq = 128, 70000, 3
+    kv = torch.zeros((lk, heads, 256), dtype=torch.bfloat16, device="cuda")
+    pe = torch.zeros((lk, 64), dtype=torch.bfloat16, device="cuda")
+    q, kv_end, pe_end = _problem(57, [lq], [200], heads)
+    kv[-200:], pe[-200:] = _dev(kv_end), _dev(pe_end)
+    plan = binding.make_prefill_plan(2, heads, lq, max_q, 200)
+    ws = binding.new_workspace(plan)
+    out, lse = binding.mla_prefill(_dev(q), kv, pe, _int([0, 0, lq]), _int([0, lk - 200, lk]),
+                                   SCALE, plan=plan, workspace=ws)
+    torch.cuda.synchronize()
+    assert binding.read_error(ws) == 0
+    _check(bf16_tensor_bits(out), lse.cpu().numpy().astype(np.float64), q, kv_end, pe_end, [lq],
+           [200], True)
 
 
 def test_prefill_without_lse_plan_and_workspace():
