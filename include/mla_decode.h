@@ -489,18 +489,15 @@ int mla_decode_v_up_proj(const mla_decode_plan_t* plan, const void* q, const voi
 
 /*
  * Expansion of cached latent rows into per-head keys and values, for the
- * attention in its expanded form (vLLM mla_attention API docs,
- * "Compute Friendly Approach (i.e. forward_mha)" and
- * _compute_prefill_context: gather_cache, then the kv_b projection). Packed
- * row t of request b, t in [cu_seqlens_k[b], cu_seqlens_k[b + 1]), is its
+ * attention in its expanded (compute-friendly) form. Packed row t of request b, t in [cu_seqlens_k[b], cu_seqlens_k[b + 1]), is its
  * cached token first_token[b] + t - cu_seqlens_k[b]; with the 576-wide entry
  * e of that token, read through the block table,
  *     kv[t, n, 0:128]   = sum_l e[l] * w_uk_t[n, 0:128, l]   (l < 512)
  *     kv[t, n, 128:256] = sum_l e[l] * w_uv[n, l, 0:128]
  *     k_pe[t, 0:64]     = e[512:576]
  * Accumulation in fp32, one rounding to bf16 (nearest even). k_pe is one row
- * for all heads; kv is the layout of a kv_b projection's output, so new
- * tokens' keys and values may come from such a product too.
+ * for all heads; kv is also what one product of the new tokens' latent rows
+ * with both weights gives, so they may come from there.
  *
  *   latent_cache   device, bf16 [num_blocks, 64, 576] (mla_expand_kv), or
  *                  E4M3 codes with entry = k_scale * e4m3(code), k_scale
@@ -535,10 +532,9 @@ int mla_expand_kv_fp8(const void* latent_cache_fp8, float k_scale, int64_t num_b
                       void* k_pe, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * mla_prefill -- attention of many query tokens in the expanded form
- * ("forward_mha" of the vLLM mla_attention API docs: flash attention of
+ * mla_prefill -- attention of many query tokens in the expanded form:
  * q [T, N, 192] over k = cat[k_nope, k_pe] and v, ragged batches by
- * cu_seqlens, returning the LSE so that context chunks can be merged).
+ * cu_seqlens, with the LSE, so that context chunks can be merged.
  *
  * Sequence b has queries [cu_seqlens_q[b], cu_seqlens_q[b+1]) and keys
  * [cu_seqlens_k[b], cu_seqlens_k[b+1]), Lq and Lk of them. Query i sees key j
