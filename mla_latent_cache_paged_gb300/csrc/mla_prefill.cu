@@ -146,6 +146,11 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
     }
 }
 
+// sum += 0 * x for a pair of bf16 values.
+__device__ __forceinline__ void add_zero_times(uint32_t x, uint32_t* sum) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(*sum) : "r"(x), "r"(0));
+}
+
 // Pairs of floats: one instruction for two (round to nearest, as the single ones).
 __device__ __forceinline__ uint64_t pack_f32(float a, float b) {
     uint64_t d;
@@ -594,7 +599,8 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                                          p.status, kSiteRaw));
                     if (!ok) break;
                     const int end = it.lk - j * kStep;      // rows of the step that exist
-                    uint32_t top = 0;                       // largest magnitudes, two at a time
+                    // 0 x + sum: NaN as soon as one x is a NaN or an infinity.
+                    uint32_t sum[4] = {0, 0, 0, 0};
                     for (int c = 0; c < 2; ++c) {
                         // Two 64 x 64 boxes of 128-byte rows; a row is 8 pieces of 16 bytes.
                         uint4* v = reinterpret_cast<uint4*>(
@@ -612,14 +618,17 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                                         v[k0 + 32 * i] = x[i] = make_uint4(0, 0, 0, 0);
                             }
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu,
-                                                                      x[i].y & 0x7fff7fffu),
-                                                             __vmaxu2(x[i].z & 0x7fff7fffu,
-                                                                      x[i].w & 0x7fff7fffu)));
+                            for (int i = 0; i < 8; ++i) {
+                                add_zero_times(x[i].x, &sum[0]);
+                                add_zero_times(x[i].y, &sum[1]);
+                                add_zero_times(x[i].z, &sum[2]);
+                                add_zero_times(x[i].w, &sum[3]);
+                            }
                         }
                     }
-                    const bool bad = (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u;
+                    // (the sums are +-0 or NaN)
+                    const uint32_t any = (sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu;
+                    const bool bad = any != 0;
                     if (__any_sync(0xffffffffu, bad)) {
                         for (int c = 0; c < 2; ++c) {
                             uint32_t* v = reinterpret_cast<uint32_t*>(
