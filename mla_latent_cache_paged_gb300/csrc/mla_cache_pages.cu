@@ -105,6 +105,11 @@ struct PageScratch {
     int32_t* moved_ref;     // compact: [moves] count of src[k]; fork: [children] rows to copy
 };
 
+// Pages of L >= 0 tokens, up to the largest int.
+__device__ __forceinline__ int pages_in(int L) {
+    return int((uint32_t(L) + kPageSize - 1) / kPageSize);
+}
+
 __device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -213,7 +218,7 @@ __device__ __forceinline__ void check_child(const ForkParams& p, int c) {
     } else {
         // Every page that the child shares or copies from is in use.
         const int32_t* row = p.table + int64_t(parent) * p.max_blocks;
-        for (int j = lane; j < pages_of(S); j += 32) {
+        for (int j = lane; j < pages_in(S); j += 32) {
             const int page = row[j];
             if (page < 0 || int64_t(page) >= p.num_blocks) {
                 bad = MLA_ERR_BAD_BLOCK_ID;
@@ -231,7 +236,7 @@ __device__ __forceinline__ void check_child(const ForkParams& p, int c) {
     const bool any = __any_sync(0xffffffffu, bad != MLA_OK);
     from = int(__reduce_add_sync(0xffffffffu, uint32_t(from)));
     if (lane == 0) {
-        p.ws.need[c] = any ? -1 : pages_of(L) - S / kPageSize;
+        p.ws.need[c] = any ? -1 : pages_in(L) - S / kPageSize;
         p.ws.src[c] = from;
         p.ws.moved_ref[c] = S % kPageSize;
     }
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kPageThreads, kCtasPerSm) free_kernel(const Fr
             if (j0 == 0 && threadIdx.x == 0) record_error(p.status, MLA_ERR_BAD_SEQ_LEN, L);
             continue;
         }
-        const int n = pages_of(L);
+        const int n = pages_in(L);
         if (j0 >= n) continue;
         const int j = j0 + threadIdx.x;
         int page = j < n ? p.table[int64_t(row) * p.max_blocks + j] : -1;
@@ -549,7 +554,7 @@ __global__ void __launch_bounds__(kPageThreads, kCtasPerSm) compact_kernel(const
             if (j == 0) record_error(p.ws.status, MLA_ERR_BAD_SEQ_LEN, L);
             continue;
         }
-        if (j >= pages_of(L)) continue;
+        if (j >= pages_in(L)) continue;
         int page = p.table[e];
         if (page < 0 || int64_t(page) >= p.num_blocks) {
             record_error(p.ws.status, MLA_ERR_BAD_BLOCK_ID, page);

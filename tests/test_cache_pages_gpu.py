@@ -451,3 +451,28 @@ def test_a_pool_of_many_chunks_and_a_cache_past_2_31_bytes():
     assert torch.equal(cache[:3000, 0, 0].long(),
                        torch.arange(3000, device="cuda").remainder(251))
     assert bool((cache[:3000] == cache[:3000, :1, :1]).all())
+
+
+def test_lengths_near_the_largest_int_are_counted_right():
+    """A row of 2^25 entries may be 2^31 - 1 tokens long: its pages are 2^25,
+    not a negative number that is passed over."""
+    import torch
+    width, blocks, longest = 1 << 25, 4, 2 ** 31 - 1
+    ws = binding.new_cache_workspace(blocks, 1)
+    table = torch.full((1, width), -3, dtype=torch.int32, device="cuda")
+    table[0, 0] = 2
+    ref = _dev([0, 0, 1, 0])
+    cache = torch.zeros((blocks, 64, 576), dtype=torch.uint8, device="cuda")
+    child = torch.full((1, width), -5, dtype=torch.int32, device="cuda")
+    binding.mla_cache_fork(cache, ref, table, _dev([0]), _dev([64]), _dev([longest]), workspace=ws,
+                           child_table=child)
+    assert binding.read_error(ws) == binding.MLA_ERR_NO_PAGES
+    assert ref.tolist() == [0, 0, 1, 0] and bool((child == -5).all())
+    # The one good entry is counted down, the others are reported.
+    _, freed = binding.mla_cache_free(ref, table, _dev([longest]), _dev([0]), workspace=ws)
+    assert binding.read_error(ws) == binding.MLA_ERR_BAD_BLOCK_ID
+    assert ref.tolist() == [0, 0, 0, 0] and int(freed) == 1
+    ref = _dev([0, 0, 1, 0])
+    table, _, _, live = binding.mla_cache_compact(cache, ref, table, _dev([longest]), workspace=ws)
+    assert binding.read_error(ws) == binding.MLA_ERR_BAD_BLOCK_ID
+    assert int(live) == 1 and int(table[0, 0]) == 0 and bool((table[0, 1:] == -3).all())
