@@ -489,9 +489,10 @@ int mla_decode_v_up_proj(const mla_decode_plan_t* plan, const void* q, const voi
 
 /*
  * Expansion of cached latent rows into per-head keys and values, for the
- * attention in its expanded (compute-friendly) form. Packed row t of request b, t in [cu_seqlens_k[b], cu_seqlens_k[b + 1]), is its
- * cached token first_token[b] + t - cu_seqlens_k[b]; with the 576-wide entry
- * e of that token, read through the block table,
+ * attention in its expanded (compute-friendly) form. Packed row t of request
+ * b, t in [cu_seqlens_k[b], cu_seqlens_k[b + 1]), is its cached token
+ * first_token[b] + t - cu_seqlens_k[b]; with the 576-wide entry e of that
+ * token, read through the block table,
  *     kv[t, n, 0:128]   = sum_l e[l] * w_uk_t[n, 0:128, l]   (l < 512)
  *     kv[t, n, 128:256] = sum_l e[l] * w_uv[n, l, 0:128]
  *     k_pe[t, 0:64]     = e[512:576]
@@ -509,7 +510,9 @@ int mla_decode_v_up_proj(const mla_decode_plan_t* plan, const void* q, const voi
  *                  kv and k_pe at cu_seqlens_k[batch] and after are left as
  *                  they were.
  *   total_k        rows of kv and k_pe; work is sized by it, so it should be
- *                  cu_seqlens_k[batch] or little more.
+ *                  cu_seqlens_k[batch] or little more. (If it is less, the rows
+ *                  that there is room for are written, and MLA_ERR_BAD_SEQ_LEN
+ *                  is recorded.)
  *   w_uk_t, w_uv   device, bf16 [N, 128, 512] and [N, 512, 128], 16-byte
  *                  aligned: the weights of mla_q_absorb_concat_cache and
  *                  mla_v_up_proj.
@@ -596,8 +599,9 @@ int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q_len, int m
  *                  initialised once with mla_workspace_init; calls that
  *                  share one must not overlap on the device.
  * The softmax weights are rounded to bf16 for the tensor cores (with
- * single_rows they stay fp32); scores, sums and accumulators are fp32. Results do not depend on timing. One launch (two
- * with S > 1 and single_rows = 0) on `stream`, no synchronisation.
+ * single_rows they stay fp32); scores, sums and accumulators are fp32. Results
+ * do not depend on timing. One launch (two with S > 1 and single_rows = 0) on
+ * `stream`, no synchronisation.
  */
 int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const void* kv, const void* k_pe,
                 int total_k, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int causal,

@@ -126,6 +126,9 @@ template <int kEntryBytes>
 __device__ __forceinline__ RowSource find_row(const ExpandParams& p, int t) {
     RowSource r{nullptr, false};
     if (t >= p.total) return r;
+    // (the last row speaks for the sequences that the rows have no room for)
+    if (t == p.total - 1 && p.cu[p.batch] > p.total)
+        record_error(p.status, MLA_ERR_BAD_SEQ_LEN, p.cu[p.batch]);
     int lo = 0, hi = p.batch;       // the last b with cu[b] <= t
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;

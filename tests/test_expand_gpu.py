@@ -209,3 +209,20 @@ def test_expand_with_starts_that_make_no_sense_stays_in_bounds():
         torch.cuda.synchronize()
         binding.read_error(ws)
         assert kv.shape == (120, 2, 256)
+
+
+@pytest.mark.parametrize("cu,total", [([0, 100, 200], 150), ([0, 100, 200], 100), ([0, 0, 200], 1)])
+def test_expand_into_too_few_rows_is_reported(cu, total):
+    """Rows that there is room for are those of the whole call; the error says
+    that there were more, whether a sequence is cut or left out."""
+    import torch
+    rng = np.random.default_rng(13)
+    cache, table, w_uk, w_uv = _problem(rng, [200, 200], [0, 0], 2, False)
+    args = (_dev(cache), _int(table), _int(cu), _dev(w_uk), _dev(w_uv))
+    ws = binding.new_status_workspace()
+    want = binding.mla_expand_kv(*args, total_k=cu[-1], workspace=ws)
+    assert binding.read_error(ws) == 0
+    got = binding.mla_expand_kv(*args, total_k=total, workspace=ws)
+    assert binding.read_error(ws) == binding.MLA_ERR_BAD_SEQ_LEN
+    assert all(torch.equal(g.view(torch.int16), w[:total].view(torch.int16))
+               for g, w in zip(got, want))
