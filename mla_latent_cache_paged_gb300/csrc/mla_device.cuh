@@ -17,6 +17,13 @@ __device__ __forceinline__ uint16_t f32_to_bf16_bits_rn(float f) {
     return *reinterpret_cast<uint16_t*>(&h);
 }
 
+// Two floats as a pair of bf16, `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 // Tokens row h must not see at the end of its request (multi-token rows).
 __device__ __forceinline__ int row_shift(const DecodeParams& p, int h) {
     if (p.q_len <= 1 || !p.causal) return 0;

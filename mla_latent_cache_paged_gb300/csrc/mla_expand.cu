@@ -12,29 +12,31 @@
 //
 // A matrix product with T rows, N * 256 columns and K = 512. Its bound at
 // N = 128 is the tensor pipe (2 * 512 flops per output element against 2
-// bytes written). A CTA works on 256 tokens and walks the (head, half) column
-// tiles of 128: a weight tile streamed from L2 then serves 256 rows, 32 bytes
-// per clock per SM at the tensor pipe's full rate (with 128 rows it would be
-// 64). Both halves of the 256 x 512 latent tile stay on chip for all of a
-// CTA's columns: rows 0..127 as the A operand in TMEM (256 columns of bf16
-// pairs), rows 128..255 in shared memory (128 KB), which leaves 96 KB for the
-// ring of weight chunks (6 x 128 columns x 64 k) and 2 x 128 TMEM columns for
-// the two accumulators. The accumulators are single; the second half's MMAs
-// run kSkew chunks behind the first's, so one accumulator is read out while
-// the tensor pipe works on the other.
+// bytes written). A pair of CTAs works on 256 tokens and walks the (head,
+// half) column tiles of 128 with M = 256 MMAs (cta_group::2): each CTA holds
+// 128 of the rows, as the A operand in TMEM (256 columns of bf16 pairs) for all
+// of the pair's columns, and half of each weight chunk in shared memory, 32
+// bytes per clock per SM from L2 at the tensor pipe's full rate. The other 2 x
+// 128 TMEM columns are two accumulators: one is read out while the tensor pipe
+// fills the other. (One CTA on 256 rows, half of them in shared memory, was
+// bound by that pipe: 205 us where this takes 153-157.)
 //
-// What bounds it now: the shared-memory pipe. Per weight chunk and 256 rows the
-// MMAs read 48 KB (the chunk twice, the second half's rows once) and the loads
-// write 16 KB, 512 clocks at 128 bytes a clock and as many as the MMAs take;
-// the result's stores pass through the same pipe. 7,865 tokens, N = 128: 204 us
-// (1,290 TFLOP/s, 2.5 TB/s written), 165 us with the stores left out; 500
-// tokens, N = 16: 14 us (bf16 cache), 15 us (fp8).
+// 7,865 tokens, N = 128: 153-157 us (1,670-1,725 TFLOP/s, 3.3 TB/s written);
+// with the stores left out 137 us (1,920 TFLOP/s). What is between is the
+// weights' way from L2 under the result's writes: a ring of 6 chunks instead
+// of 8 costs 11 us, and 9 and 10 (which leave less of the SM's memory to L1)
+// 4 to 7. 7,865 tokens, N = 16: 30 us; 500 tokens, N = 16: 9.5 us (bf16 cache)
+// and 8.7 us (fp8). Arrivals on the other CTA's barriers carry no writes of
+// memory (what they announce lies in TMEM, ordered by the tcgen05 fences), so
+// they release at CTA scope: at cluster scope each waited for the thread's
+// earlier stores (183 us).
 //
 // Work: the (token tile, head, half) items in that order, cut into one
-// contiguous range per CTA, so each CTA gathers one or two token tiles.
-// Warps: 0 = weight loads (TMA), 1 = MMAs, 2-5 and 6-9 = gather and epilogue
-// of the first and second 128 rows (thread = row = TMEM lane). Every wait is
-// bounded (MLA_ERR_TIMEOUT).
+// contiguous range per pair, so each pair gathers one or two token tiles.
+// Warps: 0 = weight loads (TMA; each CTA its half), 1 = MMAs (the first CTA's),
+// 2-5 and 6-9 = gather and epilogue (thread = row = TMEM lane), each of the
+// two groups half of a row's columns, then every other column tile. Every wait
+// is bounded (MLA_ERR_TIMEOUT).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -50,37 +52,44 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kRows = 256;                    // tokens per CTA tile
-constexpr int kChunk = 64;                    // K per ring stage
-constexpr int kChunks = kLkv / kChunk;        // 8 per column tile
-constexpr int kStages = 6;
-constexpr int kSkew = 2;                      // chunks the second half runs behind
-constexpr int kStageBytes = 128 * kChunk * 2; // 16 KB
+constexpr int kRows = 256;                    // tokens per tile of a CTA pair
+constexpr int kCtaRows = 128;                 // of which a CTA holds half
+constexpr int kChunk = 128;                   // K per ring stage
+constexpr int kChunks = kLkv / kChunk;        // 4 per column tile
+constexpr int kStages = 8;
 constexpr int kHalf = 128;                    // columns of a tile: k_nope or v of one head
-constexpr int kOffA = 0;                      // second half's rows: 8 x [128 x 64] bf16, SW128
-constexpr int kOffRing = kChunks * 16384;
-constexpr int kOffBar = kOffRing + kStages * kStageBytes;
-constexpr int kSmemBytes = kOffBar + 256;     // base is 1 KB aligned
+constexpr int kCtaCols = kHalf / 2;           // of whose weights a CTA holds half
+constexpr int kStageBytes = kCtaCols * kChunk * 2;   // 16 KB
+constexpr int kWarpOut = 32 * kHalf * 2;      // a warp's part of a column tile: 2 boxes of 32 x 64
+constexpr int kOffOut = kStages * kStageBytes;
+constexpr int kOffBar = kOffOut + 8 * kWarpOut;
+constexpr int kSmemBytes = kOffBar + 512;     // base is 1 KB aligned
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-constexpr uint32_t kTmemA = 0;                // 256 columns: first half's rows, bf16 pairs
+// (Two pairs on the same SMs could each hold one SM's TMEM and wait for the other's.)
+static_assert(2 * kSmemBytes > 233472, "one CTA per SM");
+constexpr uint32_t kTmemA = 0;                // 256 columns: the CTA's rows, bf16 pairs
 constexpr uint32_t kTmemAcc = 256;            // 2 x 128 fp32 columns
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr uint32_t kSuspendNs = 20000;
+constexpr uint16_t kBoth = 3;                 // the pair's CTAs
 
-enum ExpandSite : int32_t { kSiteEmpty = 50, kSiteFull, kSiteA, kSiteAccEmpty, kSiteAccFull,
-                            kSiteDrain };
+enum ExpandSite : int32_t { kSiteEmpty = 50, kSiteFull, kSiteA, kSiteAFree, kSiteAccEmpty,
+                            kSiteAccFull, kSiteDrain };
 
+// In both CTAs; those marked L are used in the pair's first CTA only, the one
+// that issues the MMAs.
 struct Bars {
-    uint64_t full[kStages];
+    uint64_t full[kStages];   // L: both CTAs' halves of the weight chunk
     uint64_t empty[kStages];
-    uint64_t a_ready[2];      // 128 arrivals: this half's rows are staged
+    uint64_t a_ready;         // L: 2 x 8 warps: the rows of a token tile are staged
+    uint64_t a_free;          // the MMAs that read them are done
     uint64_t acc_full[2];
-    uint64_t acc_empty[2];    // 4 warps: accumulator read out
-    uint64_t drain;
+    uint64_t acc_empty[2];    // L: 2 x 4 warps: accumulator read out
+    uint64_t drain;           // L
     uint32_t tmem_base;
     int32_t abort;
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= 512, "barrier block");
 
 struct ExpandParams {
     const void* cache;              // bf16 or E4M3 [num_blocks, 64, 576]
@@ -156,14 +165,9 @@ __device__ __forceinline__ RowSource find_row(const ExpandParams& p, int t) {
 __device__ __forceinline__ uint32_t widen2(uint32_t codes16) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(codes16), __NV_E4M3);
     const float2 f = __half22float2(__half2(h));
-    return uint32_t(f32_to_bf16_bits_rn(f.x)) | (uint32_t(f32_to_bf16_bits_rn(f.y)) << 16);
+    return pack_bf16(f.x, f.y);
 }
 
-__device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* w) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3])
-                 : "memory");
-}
 // 32 bytes (32-byte aligned).
 __device__ __forceinline__ void load32(const char* p, uint32_t* r) {
     asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -172,11 +176,9 @@ __device__ __forceinline__ void load32(const char* p, uint32_t* r) {
                  : "l"(p));
 }
 
-// 64 entries (32 words of bf16 pairs) from column 64 g of a row; zeros
-// without one.
+// 64 entries from column 64 g of a row, as they lie; zeros without one.
 template <int kEntryBytes>
-__device__ __forceinline__ void load64(const char* entry, int g, uint32_t* w) {
-    uint32_t c[16 * kEntryBytes];
+__device__ __forceinline__ void load64(const char* entry, int g, uint32_t (&c)[16 * kEntryBytes]) {
 #pragma unroll
     for (int k = 0; k < 16 * kEntryBytes; ++k) c[k] = 0;
     if (entry != nullptr) {
@@ -184,6 +186,10 @@ __device__ __forceinline__ void load64(const char* entry, int g, uint32_t* w) {
         for (int k = 0; k < 2 * kEntryBytes; ++k)
             load32(entry + g * 64 * kEntryBytes + k * 32, c + 8 * k);
     }
+}
+// The same as bf16 pairs.
+template <int kEntryBytes>
+__device__ __forceinline__ void widen64(const uint32_t (&c)[16 * kEntryBytes], uint32_t (&w)[32]) {
     if constexpr (kEntryBytes == 2) {
 #pragma unroll
         for (int k = 0; k < 32; ++k) w[k] = c[k];
@@ -196,27 +202,31 @@ __device__ __forceinline__ void load64(const char* entry, int g, uint32_t* w) {
     }
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    return uint32_t(f32_to_bf16_bits_rn(a)) | (uint32_t(f32_to_bf16_bits_rn(b)) << 16);
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
 }
-
 template <int kEntryBytes>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_uk,
-                  const __grid_constant__ CUtensorMap map_uv) {
+                  const __grid_constant__ CUtensorMap map_uv,
+                  const __grid_constant__ CUtensorMap map_kv) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = ptx::smem_addr(smem);
     Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
     const uint32_t b0 = sbase + kOffBar;
     auto full = [&](int s) { return b0 + uint32_t(offsetof(Bars, full)) + 8 * s; };
     auto empty = [&](int s) { return b0 + uint32_t(offsetof(Bars, empty)) + 8 * s; };
-    auto a_ready = [&](int h) { return b0 + uint32_t(offsetof(Bars, a_ready)) + 8 * h; };
-    auto acc_full = [&](int h) { return b0 + uint32_t(offsetof(Bars, acc_full)) + 8 * h; };
-    auto acc_empty = [&](int h) { return b0 + uint32_t(offsetof(Bars, acc_empty)) + 8 * h; };
+    auto acc_full = [&](int a) { return b0 + uint32_t(offsetof(Bars, acc_full)) + 8 * a; };
+    auto acc_empty = [&](int a) { return b0 + uint32_t(offsetof(Bars, acc_empty)) + 8 * a; };
+    const uint32_t a_ready = b0 + uint32_t(offsetof(Bars, a_ready));
+    const uint32_t a_free = b0 + uint32_t(offsetof(Bars, a_free));
     const uint32_t drain = b0 + uint32_t(offsetof(Bars, drain));
     const int warp = threadIdx.x >> 5;
+    const int rank = int(ptx::cluster_ctarank());
 
-    if ((sbase & 1023u) != 0) {   // the swizzled tiles need it
+    if ((sbase & 1023u) != 0) {   // the swizzled tiles need it (the same in both CTAs)
         if (threadIdx.x == 0) record_error(p.status, MLA_ERR_UNSUPPORTED, 0);
         return;
     }
@@ -225,37 +235,41 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
             ptx::mbar_init(full(s), 1);
             ptx::mbar_init(empty(s), 1);
         }
-        for (int h = 0; h < 2; ++h) {
-            ptx::mbar_init(a_ready(h), 128);
-            ptx::mbar_init(acc_full(h), 1);
-            ptx::mbar_init(acc_empty(h), 4);
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(acc_full(a), 1);
+            ptx::mbar_init(acc_empty(a), 2 * 4);
         }
+        ptx::mbar_init(a_ready, 2 * 8);
+        ptx::mbar_init(a_free, 1);
         ptx::mbar_init(drain, 1);
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_addr(&bars->tmem_base), 512);
-        ptx::tmem_relinquish();
+        ptx::tmem_alloc_pair(ptx::smem_addr(&bars->tmem_base), 512);
+        ptx::tmem_relinquish_pair();
     }
     ptx::tc_fence_before();
     __syncthreads();
+    ptx::cluster_sync();          // (the pair's barriers exist before either uses the other's)
     ptx::tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
 
-    // This CTA's items, and their token tiles. A token tile's rows past
-    // `total` are zeros; a second half without rows does not run.
+    // The pair's items, and their token tiles. A token tile's rows past
+    // `total` are zeros.
     const int per_tile = p.heads * 2;
-    const int64_t begin = int64_t(blockIdx.x) * p.items / gridDim.x;
-    const int64_t end = int64_t(blockIdx.x + 1) * p.items / gridDim.x;
+    const int64_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int64_t begin = pair * p.items / pairs;
+    const int64_t end = (pair + 1) * p.items / pairs;
     auto tile_end = [&](int64_t it) {
         const int64_t e = (it / per_tile + 1) * per_tile;
         return e < end ? e : end;
     };
-    auto two_halves = [&](int64_t it) { return int64_t(p.total) - (it / per_tile) * kRows > 128; };
 
     if (warp == 0) {
         if (ptx::elect_one()) {
+            // This CTA's half of each weight chunk; the first CTA's barrier
+            // counts the bytes of both.
             uint32_t chunk = 0;
             const uint32_t chunks = uint32_t(end - begin) * kChunks;
             int item = int(begin % per_tile);
@@ -266,203 +280,150 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
                 const int n = item >> 1, c = int(chunk % kChunks);
                 const bool is_k = (item & 1) == 0;
                 if (c == kChunks - 1 && ++item == per_tile) item = 0;
-                const uint32_t st = sbase + uint32_t(kOffRing + s * kStageBytes);
-                ptx::mbar_arrive_expect_tx(full(s), kStageBytes);
+                const uint32_t st = sbase + uint32_t(s * kStageBytes);
+                const uint32_t bar = ptx::map_to_rank(full(s), 0);
+                if (rank == 0) ptx::mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
                 if (is_k) {
-                    ptx::tma_load_2d(st, &map_uk, c * kChunk, n * kHalf, full(s));
+                    const int y = n * kHalf + rank * kCtaCols;
+                    ptx::tma_load_2d_pair(st, &map_uk, c * kChunk, y, bar);
+                    ptx::tma_load_2d_pair(st + kStageBytes / 2, &map_uk, c * kChunk + 64, y, bar);
                 } else {
-                    ptx::tma_load_2d(st, &map_uv, 0, n * kLkv + c * kChunk, full(s));
-                    ptx::tma_load_2d(st + 8192, &map_uv, 64, n * kLkv + c * kChunk, full(s));
+                    ptx::tma_load_2d_pair(st, &map_uv, rank * kCtaCols, n * kLkv + c * kChunk, bar);
                 }
             }
-            // Loads still in flight (after an abort) land before the CTA exits.
-            for (uint32_t i = chunk > kStages ? chunk - kStages : 0; i < chunk; ++i)
-                wait(full(int(i % kStages)), (i / kStages) & 1, bars, p.status, kSiteDrain,
-                     true);
+            // Loads still in flight (after an abort) land before the CTA
+            // exits; the second CTA exits after the first.
+            if (rank == 0)
+                for (uint32_t i = chunk > kStages ? chunk - kStages : 0; i < chunk; ++i)
+                    wait(full(int(i % kStages)), (i / kStages) & 1, bars, p.status, kSiteDrain,
+                         true);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (ptx::elect_one()) {
-            constexpr uint32_t idesc_k = ptx::idesc_bf16_f32(kHalf, false);
-            constexpr uint32_t idesc_v = ptx::idesc_bf16_f32(kHalf, true);
+        if (rank == 0 && ptx::elect_one()) {
+            constexpr uint32_t idesc_k = ptx::idesc_bf16_f32_pair(kHalf, false);
+            constexpr uint32_t idesc_v = ptx::idesc_bf16_f32_pair(kHalf, true);
             // (The thread that issues MMAs waits for the tensor pipe to take
             // each; what it does in between should be little. A descriptor is
-            // the layout's constant bits plus the address, and only the first
-            // half waits for a weight chunk.)
-            const uint64_t desc_k = ptx::desc_sw128(0, 16, 1024);
-            const uint64_t desc_v = ptx::desc_sw128(0, 8192, 1024);
-            const uint32_t ring = (sbase + uint32_t(kOffRing)) >> 4;
-            const uint64_t a_base = desc_k + ((sbase + uint32_t(kOffA)) >> 4);
+            // the layout's constant bits plus the address.)
+            const uint64_t desc_k = ptx::desc_sw128(0, 16, 1024) + (sbase >> 4);
+            const uint64_t desc_v = ptx::desc_sw128(0, 8192, 1024) + (sbase >> 4);
             bool ok = true;
-            uint32_t slot0 = 0, slot1 = 0, turn = 0;   // ring slot per half, parity of the first's
-            uint32_t tiles[2] = {0, 0};                // column tiles begun per half
-            uint32_t seg[2] = {0, 0};                  // token tiles begun per half
-            for (int64_t it = begin; it < end && ok;) {
+            uint32_t slot = 0, turn = 0;               // ring slot and its parity
+            uint32_t n = 0, seg = 0;                   // column and token tiles begun
+            for (int64_t it = begin; it < end && ok; ++seg) {
                 const int64_t e = tile_end(it);
-                const bool two = two_halves(it);
-                ok = wait(a_ready(0), seg[0]++ & 1, bars, p.status, kSiteA);
-                if (two) ok = ok && wait(a_ready(1), seg[1]++ & 1, bars, p.status, kSiteA);
-                for (; it < e && ok; ++it) {
-                    // W_UK_T: 16 k = 32 bytes per step; W_UV: 16 k-rows = 2 KB
-                    // per step, its two 64-column blocks 8 KB apart.
+                ok = wait(a_ready, seg & 1, bars, p.status, kSiteA);
+                for (; it < e && ok; ++it, ++n) {
+                    // W_UK_T: 16 k = 32 bytes per step, 64 k = 8 KB; W_UV: 16
+                    // k-rows = 2 KB per step.
                     const bool is_v = (it & 1) != 0;
-                    const uint64_t w_base = (is_v ? desc_v : desc_k) + ring;
+                    const uint64_t desc = is_v ? desc_v : desc_k;
                     const uint32_t st = is_v ? 128 : 2;
                     const uint32_t idesc = is_v ? idesc_v : idesc_k;
-                    // First half's chunk k, second half's chunk k - kSkew; the
-                    // tile's last chunks of the second half go out before the
-                    // next tile's first of the first half, so that three
-                    // chunks' MMAs cover the readout of each accumulator.
+                    const uint32_t acc = tmem + kTmemAcc + (n & 1) * kHalf;
+                    if (n >= 2)
+                        ok = wait(acc_empty(n & 1), ((n >> 1) - 1) & 1, bars, p.status,
+                                  kSiteAccEmpty);
 #pragma unroll
-                    for (int k = 0; k < kChunks + kSkew; ++k) {
-                        if (k < kChunks) {
-                            if (k == 0 && tiles[0]++ > 0)
-                                ok = wait(acc_empty(0), tiles[0] & 1, bars, p.status,
-                                          kSiteAccEmpty);
-                            ok = ok && wait(full(slot0), turn, bars, p.status, kSiteFull);
-                            if (!ok) break;
-                            ptx::tc_fence_after();
-                            const uint64_t w = w_base + slot0 * (kStageBytes / 16);
-                            const uint32_t a = tmem + kTmemA + uint32_t(k * 32);
-                            ptx::mma4_ts(tmem + kTmemAcc, a, a + 8, a + 16, a + 24, w, w + st,
-                                         w + 2 * st, w + 3 * st, idesc, k > 0 ? 1u : 0u);
-                            if (!two) ptx::mma_commit(empty(slot0));
-                            if (k == kChunks - 1) ptx::mma_commit(acc_full(0));
-                            if (++slot0 == kStages) {
-                                slot0 = 0;
-                                turn ^= 1;
-                            }
+                    for (int c = 0; c < kChunks; ++c) {
+                        ok = ok && wait(full(slot), turn, bars, p.status, kSiteFull);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint64_t w = desc + slot * (kStageBytes / 16);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t a = tmem + kTmemA + uint32_t(c * 64 + h * 32);
+                            const uint64_t b = w + uint32_t(h * 512);
+                            ptx::mma4_ts_pair(acc, a, a + 8, a + 16, a + 24, b, b + st, b + 2 * st,
+                                              b + 3 * st, idesc, c + h > 0 ? 1u : 0u);
                         }
-                        if (two && k >= kSkew) {
-                            if (k == kSkew && tiles[1]++ > 0) {
-                                ok = wait(acc_empty(1), tiles[1] & 1, bars, p.status,
-                                          kSiteAccEmpty);
-                                if (!ok) break;
-                                ptx::tc_fence_after();
-                            }
-                            const uint64_t w = w_base + slot1 * (kStageBytes / 16);
-                            const uint64_t a = a_base + uint32_t((k - kSkew) * 1024);
-                            ptx::mma4_ss(tmem + kTmemAcc + uint32_t(kHalf), a, a + 2, a + 4, a + 6,
-                                         w, w + st, w + 2 * st, w + 3 * st, idesc,
-                                         k > kSkew ? 1u : 0u);
-                            ptx::mma_commit(empty(slot1));
-                            if (k == kChunks + kSkew - 1) ptx::mma_commit(acc_full(1));
-                            if (++slot1 == kStages) slot1 = 0;
+                        ptx::mma_commit_pair(empty(slot), kBoth);
+                        if (++slot == kStages) {
+                            slot = 0;
+                            turn ^= 1;
                         }
                     }
+                    if (ok) ptx::mma_commit_pair(acc_full(n & 1), kBoth);
                 }
-                if (!two) slot1 = slot0;
+                if (ok) ptx::mma_commit_pair(a_free, kBoth);
             }
             // Every MMA issued above has completed before TMEM is freed.
-            ptx::mma_commit(drain);
+            ptx::mma_commit_pair(drain, 1);
             wait(drain, 0, bars, p.status, kSiteDrain, true);
         }
         __syncwarp();
     } else {
-        const int h = warp >= 6 ? 1 : 0;
+        // Gather and epilogue. Group g takes columns 256 g.. of the latent
+        // rows into TMEM, and every other column tile out of it.
+        const int g = warp >= 6 ? 1 : 0;
         const int lanes = (warp & 3) * 32;                 // TMEM lanes this warp reads
         const int lane = threadIdx.x & 31;
-        const int r = lanes + lane;                        // row of the half
+        const int r = lanes + lane;                        // row of the CTA
         const uint32_t lane_addr = uint32_t(lanes) << 16;
+        const uint32_t acc = tmem + kTmemAcc + lane_addr + uint32_t(g * kHalf);
+        const uint32_t to_ready = ptx::map_to_rank(a_ready, 0);
+        const uint32_t to_empty = ptx::map_to_rank(acc_empty(g), 0);
+        const uint32_t out = sbase + uint32_t(kOffOut + (warp - 2) * kWarpOut);
         bool ok = true;
-        uint32_t done = 0;
-        for (int64_t it = begin; it < end && ok;) {
+        uint32_t n = 0, seg = 0;
+        for (int64_t it = begin; it < end && ok; ++seg) {
             const int64_t e = tile_end(it);
-            const int64_t t = (it / per_tile) * kRows + h * 128 + r;
-            if (h == 1 && !two_halves(it)) { it = e; continue; }
-            // Gather: this thread's row of the latent tile. Every MMA that
-            // read the half's previous rows is done: its last accumulator was
-            // waited for below.
+            const int64_t t = (it / per_tile) * kRows + rank * kCtaRows + r;
             const RowSource src = find_row<kEntryBytes>(p, t < INT_MAX ? int(t) : INT_MAX);
             __syncwarp();
-            if (h == 0) {
-                // (TMEM takes a row per lane; whole 32-byte sectors at a time.)
-#pragma unroll 1
-                for (int g = 0; g < kLkv / 64; ++g) {
-                    uint32_t w[32];
-                    load64<kEntryBytes>(src.entry, g, w);
-                    __syncwarp();
-                    ptx::tmem_st32(tmem + kTmemA + lane_addr + uint32_t(g * 32), w);
-                }
-                ptx::tc_fence_before();
-            } else {
-                // A warp takes its 32 rows one after the other, eight in
-                // flight, each lane a piece of the row: a lane per row reads
-                // 32 lines a load (it took 20,000 clocks a token tile). Column
-                // 8 j is 16-byte piece j % 8 of chunk j / 8.
-                constexpr int kLoads = kEntryBytes;     // 16-byte loads per lane and row
-#pragma unroll 1
-                for (int i0 = 0; i0 < 32; i0 += 8) {
-                    uint4 v[8][kLoads];
+            const bool whole = __all_sync(0xffffffffu, src.exists);
+            // A row per lane, as TMEM takes it; whole 32-byte sectors at a time.
+            uint32_t c[4][16 * kEntryBytes];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint64_t entry = __shfl_sync(
-                            0xffffffffu, reinterpret_cast<uint64_t>(src.entry), i0 + i);
-#pragma unroll
-                        for (int k = 0; k < kLoads; ++k) {
-                            v[i][k] = make_uint4(0, 0, 0, 0);
-                            if (entry != 0)
-                                v[i][k] = __ldg(reinterpret_cast<const uint4*>(entry) + k * 32 + lane);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int q = lanes + i0 + i;
-                        const uint32_t row = sbase + uint32_t(kOffA + q * 128);
-                        auto put = [&](int j, const uint32_t* w) {
-                            st_shared16(row + uint32_t((j >> 3) * 16384 + (((j & 7) ^ (q & 7)) * 16)), w);
-                        };
-                        if constexpr (kEntryBytes == 2) {
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const uint32_t w[4] = {v[i][k].x, v[i][k].y, v[i][k].z, v[i][k].w};
-                                put(k * 32 + lane, w);
-                            }
-                        } else {
-                            const uint32_t c[4] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w};
-                            uint32_t w[8];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                w[2 * k] = widen2(c[k] & 0xffffu);
-                                w[2 * k + 1] = widen2(c[k] >> 16);
-                            }
-                            put(2 * lane, w);
-                            put(2 * lane + 1, w + 4);
-                        }
-                    }
-                }
-                ptx::fence_proxy_async_smem();
+            for (int k = 0; k < 4; ++k) load64<kEntryBytes>(src.entry, 4 * g + k, c[k]);
+            if (seg > 0) {
+                ok = __all_sync(0xffffffffu,
+                                wait(a_free, (seg - 1) & 1, bars, p.status, kSiteAFree));
+                if (!ok) break;
+                ptx::tc_fence_after();
             }
-            ptx::mbar_arrive(a_ready(h));
-            // The CTA with a token tile's first item writes its rows' k_pe.
-            if (it % per_tile == 0 && src.exists) {
-                uint4* dst = reinterpret_cast<uint4*>(p.k_pe + t * kRope);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
                 uint32_t w[32];
-                load64<kEntryBytes>(src.entry, kLkv / 64, w);
+                widen64<kEntryBytes>(c[k], w);
+                __syncwarp();
+                ptx::tmem_st32(tmem + kTmemA + lane_addr + uint32_t(g * 128 + k * 32), w);
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(to_ready);
+            // The pair with a token tile's first item writes its rows' k_pe.
+            if (g == 0 && it % per_tile == 0 && src.exists) {
+                uint4* dst = reinterpret_cast<uint4*>(p.k_pe + t * kRope);
+                uint32_t pe[16 * kEntryBytes], w[32];
+                load64<kEntryBytes>(src.entry, kLkv / 64, pe);
+                widen64<kEntryBytes>(pe, w);
                 if constexpr (kEntryBytes == 1) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)   // one rounding of scale * code
-                        w[i] = pack2(p.scale * bf16_bits_to_f32(w[i] & 0xffffu),
+                        w[i] = pack_bf16(p.scale * bf16_bits_to_f32(w[i] & 0xffffu),
                                      p.scale * bf16_bits_to_f32(w[i] >> 16));
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
             }
+            __syncwarp();
             int item = int(it % per_tile);
-            for (; it < e; ++it, ++item) {
-                ok = wait(acc_full(h), done & 1, bars, p.status, kSiteAccFull);
+            for (; it < e; ++it, ++item, ++n) {
+                if (int(n & 1) != g) continue;
+                ok = wait(acc_full(g), (n >> 1) & 1, bars, p.status, kSiteAccFull);
                 // (one answer for the warp: the TMEM loads are warp-wide)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                ++done;
                 ptx::tc_fence_after();
                 uint32_t lo[64], hi[64];
-                ptx::tmem_ld64(tmem + kTmemAcc + lane_addr + uint32_t(h * kHalf), lo);
-                ptx::tmem_ld64(tmem + kTmemAcc + lane_addr + uint32_t(h * kHalf + 64), hi);
+                ptx::tmem_ld64(acc, lo);
+                ptx::tmem_ld64(acc + 64, hi);
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(acc_empty(h));
+                if (lane == 0) ptx::mbar_arrive_cluster(to_empty);
                 uint32_t o[64];
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
@@ -472,13 +433,28 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
                         a *= p.scale;
                         b *= p.scale;
                     }
-                    o[i] = pack2(a, b);
+                    o[i] = pack_bf16(a, b);
                 }
-                // 32 bytes of a row per lane and store. (Swapping pieces between
-                // lanes so that a store fills whole 128-byte lines was 18%
-                // slower at N = 128: shuffles share the shared-memory pipe
-                // that feeds the MMAs, which is this kernel's bound.)
-                if (src.exists) {
+                if (whole) {
+                    // Through shared memory (16-byte piece k of a row of a box
+                    // at k ^ row % 8), so that whole lines are written: 153 us
+                    // against 159 by the stores below.
+                    if (lane == 0) ptx::bulk_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        st_shared16(out + uint32_t((i >> 3) * (kWarpOut / 2) + lane * 128 +
+                                                   (((i & 7) ^ (lane & 7)) * 16)), o + 4 * i);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int x = (item >> 1) * 256 + (item & 1) * kHalf;
+                        ptx::tma_store_2d(&map_kv, x, int(t), out);
+                        ptx::tma_store_2d(&map_kv, x + 64, int(t), out + kWarpOut / 2);
+                        ptx::bulk_commit();
+                    }
+                } else if (src.exists) {
+                    // 32 bytes of a row per lane and store.
                     uint16_t* dst = p.kv + (t * p.heads + (item >> 1)) * 256 + (item & 1) * kHalf;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -491,26 +467,32 @@ mla_expand_kernel(const ExpandParams p, const __grid_constant__ CUtensorMap map_
                 __syncwarp();
             }
         }
+        if (lane == 0) ptx::bulk_wait();
+        __syncwarp();
     }
+    // Neither CTA leaves while the other's MMAs, loads or arrivals may reach it.
     ptx::tc_fence_before();
     __syncthreads();
+    ptx::cluster_sync();
     ptx::tc_fence_after();
-    if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+    if (warp == 1) ptx::tmem_dealloc_pair(tmem, 512);
 }
 
 template <int kEntryBytes>
 int launch_expand(const ExpandParams& p, const void* w_uk_t, const void* w_uv, int num_sms,
                   cudaStream_t st) {
-    CUtensorMap uk, uv;
-    if (!encode_2d(&uk, w_uk_t, kLkv, uint64_t(p.heads) * kHalf, 128) ||
-        !encode_2d(&uv, w_uv, kHalf, uint64_t(p.heads) * kLkv, kChunk))
+    CUtensorMap uk, uv, kv;
+    if (!encode_2d(&uk, w_uk_t, kLkv, uint64_t(p.heads) * kHalf, kCtaCols) ||
+        !encode_2d(&uv, w_uv, kHalf, uint64_t(p.heads) * kLkv, kChunk) ||
+        !encode_2d(&kv, p.kv, uint64_t(p.heads) * 256, uint64_t(p.total), 32))
         return int(cudaErrorInvalidValue);
     auto kernel = mla_expand_kernel<kEntryBytes>;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_shared_memory(kernel, kSmemBytes, &allowed);
     if (e != cudaSuccess) return int(e);
-    const unsigned grid = unsigned(p.items < num_sms ? p.items : num_sms);
-    kernel<<<grid, kThreads, kSmemBytes, st>>>(p, uk, uv);
+    const int64_t most = num_sms / 2 > 1 ? num_sms / 2 : 1;
+    const unsigned pairs = unsigned(p.items < most ? p.items : most);
+    kernel<<<2 * pairs, kThreads, kSmemBytes, st>>>(p, uk, uv, kv);
     return int(cudaGetLastError());
 }
 

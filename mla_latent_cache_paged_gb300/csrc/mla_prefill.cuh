@@ -32,12 +32,6 @@ struct PrefillParams {
     uint32_t* done;               // CTAs that have finished
 };
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
 // Rows and keys of sequence b; one whose bounds make no sense has none.
 __device__ __forceinline__ void sequence(const PrefillParams& p, int b, int* q0, int* lq, int* k0,
                                          int* lk) {

@@ -117,6 +117,24 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int3
         : "memory");
 }
 
+// A tile from shared memory (written by threads: fence_proxy_async_smem
+// first) to global memory, in this thread's current bulk group.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int32_t x, int32_t y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until this thread's groups have read their sources / are complete.
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // 32-byte global store (the address must be 32-byte aligned).
 __device__ __forceinline__ void st_global_v8(void* dst, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
@@ -255,6 +273,80 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         : "memory");
 }
 
+// ------------------------------------------- pairs of CTAs (cta_group::2)
+
+// All threads of the cluster; earlier writes are seen behind it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+
+// The address of the same shared-memory variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    return a;
+}
+
+// Arrive on an mbarrier of any CTA of the cluster (address from map_to_rank).
+// Releases at CTA scope: it announces no writes of memory to another CTA.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+// tma_load_2d into this CTA's shared memory that counts on an mbarrier of
+// either CTA of the pair (address from map_to_rank).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int32_t x,
+                                                 int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Allocation and release by one warp of each CTA.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
+                 "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                 : "memory");
+}
+
+// mma4_ts for M = 256: each CTA's TMEM holds 128 rows of A and D, its shared
+// memory half of B's columns. Issued by the pair's first CTA.
+__device__ __forceinline__ void mma4_ts_pair(uint32_t d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint64_t b0, uint64_t b1, uint64_t b2,
+                                             uint64_t b3, uint32_t idesc, uint32_t acc0) {
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " setp.ne.b32 p, %9, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %5, %8, p;\n"
+        " setp.eq.b32 p, %9, %9;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%2], %6, %8, p;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%3], %7, %8, p;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%4], %10, %8, p;\n}\n"
+        ::"r"(d), "r"(a0), "r"(a1), "r"(a2), "r"(a3), "l"(b0), "l"(b1), "l"(b2), "r"(idesc),
+          "r"(acc0), "l"(b3)
+        : "memory");
+}
+
+// Arrive once on the mbarrier at this address in each CTA of `mask` when
+// every prior tcgen05 op of this thread completes.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar), "h"(mask)
+        : "memory");
+}
+
 // 32 lanes x 32 consecutive 32-bit columns; thread i of the warp gets lane
 // (base lane + i). Waits for the load before returning.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -334,6 +426,11 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int n, bool b_mn_major) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
            (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+}
+
+// The same for a pair of CTAs, M = 256 (`n` columns in all).
+__host__ __device__ constexpr uint32_t idesc_bf16_f32_pair(int n, bool b_mn_major) {
+    return idesc_bf16_f32(n, b_mn_major) + (uint32_t(128 >> 4) << 24);
 }
 
 // The same with f16 A and B (format field 0 for both operands).

@@ -226,3 +226,31 @@ def test_expand_into_too_few_rows_is_reported(cu, total):
     assert binding.read_error(ws) == binding.MLA_ERR_BAD_SEQ_LEN
     assert all(torch.equal(g.view(torch.int16), w[:total].view(torch.int16))
                for g, w in zip(got, want))
+
+
+def test_expansions_on_two_streams_at_once():
+    """Pairs of CTAs of two calls share the GPU: each call's result is the one
+    it has alone (ragged ends, so both ways out of the kernel are taken)."""
+    import torch
+    rng = np.random.default_rng(14)
+    calls = []
+    for lens, heads, fp8 in (([700, 31, 300], 32, False), ([257, 600], 17, True)):
+        first = [0] * len(lens)
+        cache, table, w_uk, w_uv = _problem(rng, lens, first, heads, fp8)
+        args = (torch.from_numpy(cache).cuda() if fp8 else _dev(cache), _int(table),
+                _int(np.concatenate([[0], np.cumsum(lens)])), _dev(w_uk), _dev(w_uv))
+        calls.append((binding.mla_expand_kv_fp8 if fp8 else binding.mla_expand_kv,
+                      args + ((0.25,) if fp8 else ()), sum(lens), binding.new_status_workspace(),
+                      torch.cuda.Stream()))
+    want = [fn(*args, total_k=total, workspace=ws) for fn, args, total, ws, _ in calls]
+    torch.cuda.synchronize()
+    got = [[] for _ in calls]
+    for _ in range(20):
+        for i, (fn, args, total, ws, stream) in enumerate(calls):
+            got[i].append(fn(*args, total_k=total, workspace=ws, stream=stream))
+    torch.cuda.synchronize()
+    for i, (_, _, _, ws, _) in enumerate(calls):
+        assert binding.read_error(ws) == 0
+        for kv, pe in got[i]:
+            assert torch.equal(kv.view(torch.int16), want[i][0].view(torch.int16))
+            assert torch.equal(pe.view(torch.int16), want[i][1].view(torch.int16))
