@@ -27,6 +27,12 @@
 // clocks of exponentials (32,768 of them) and 80 KB of loads (32 bytes per
 // clock per SM, from L2: the items of a group of heads run together, so that
 // their keys and values stay there).
+// Measured, 4,096 causal tokens x 128 heads (361 us at cuBLAS's rate): 465-475
+// us; 405 us with the softmax left out, 379 us with the key and value loads
+// left out too: the score MMAs take both operands from shared memory, 128 bytes
+// a clock, which is its rate, and the loads write there as well. 24 prompts of
+// 2 to 886 tokens x 16 heads 69.4 us; four chunks of ~480 rows over 3,589 to
+// 5,711 keys x 32 heads 148 us.
 //
 // Keys and values of a 128-key step that lie past the sequence's end belong to
 // the next sequence, and those past a row's causal limit are its own future:
