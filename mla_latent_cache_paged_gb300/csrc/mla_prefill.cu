@@ -27,11 +27,11 @@
 // clocks of exponentials (32,768 of them) and 80 KB of loads (32 bytes per
 // clock per SM, from L2: the items of a group of heads run together, so that
 // their keys and values stay there).
-// Measured, 4,096 causal tokens x 128 heads (361 us at cuBLAS's rate): 465-475
+// Measured, 4,096 causal tokens x 128 heads (361 us at cuBLAS's rate): 455-465
 // us; 405 us with the softmax left out, 379 us with the key and value loads
 // left out too: the score MMAs take both operands from shared memory, 128 bytes
 // a clock, which is its rate, and the loads write there as well. 24 prompts of
-// 2 to 886 tokens x 16 heads 69.4 us; four chunks of ~480 rows over 3,589 to
+// 2 to 886 tokens x 16 heads 66.7 us; four chunks of ~480 rows over 3,589 to
 // 5,711 keys x 32 heads 148 us.
 //
 // Keys and values of a 128-key step that lie past the sequence's end belong to
@@ -184,7 +184,9 @@ __device__ __forceinline__ int item_tiles(int lq) { return lq / kItemRows + (lq 
 // should also run together, so that its keys and values are read from HBM
 // once. So the row tiles are taken in four classes by the keys their last row
 // sees (more than 3/4, 1/2, 1/4 of the longest, the rest), in a class heads in
-// groups, in a group tile after tile, then heads, then splits.
+// groups, in a group tile after tile, then heads, then splits. In the lower two
+// classes all heads are one group: what comes last is short then (long prompt
+// 472 -> 464 us, 24 prompts 67.9 -> 66.5).
 // (4,096 causal tokens x 128 heads: within 1% of the mean load, against 29%
 // above it for a fixed deal by groups; four 480-row chunks over 3,589 to 5,711
 // keys x 32 heads: 168 -> 148 us against an order by position.)
@@ -256,10 +258,11 @@ __device__ __forceinline__ Item find_item(const PrefillParams& p, int64_t index,
             tiles = o.tiles[c];
         }
     }
-    const int64_t per_group = tiles * p.group * p.splits;
-    const int head0 = int(index / per_group) * p.group;
+    const int group = cls >= kClasses / 2 ? p.heads : p.group;
+    const int64_t per_group = tiles * group * p.splits;
+    const int head0 = int(index / per_group) * group;
     const int64_t rem = index % per_group;
-    const int per_tile = min(p.group, p.heads - head0) * p.splits;
+    const int per_tile = min(group, p.heads - head0) * p.splits;
     int64_t tile = rem / per_tile;
     const int rest = int(rem % per_tile);
     Item it;
@@ -668,8 +671,14 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
             for (int c = 0; c < kClasses; ++c) total += order.tiles[c] * p.heads * p.splits;
             uint32_t n = 0;
             while (true) {
-                // The next item of all CTAs. One CTA holds at most two: the
-                // one it works on and the one its loads run ahead to.
+                // The next item of all CTAs, drawn when the one before the last
+                // is done: a CTA holds two, the one it works on and the one its
+                // loads run ahead to. (One more, drawn early, left the ends of
+                // the CTAs 1.2-1.5% of the time further apart.)
+                const uint32_t s = n % kItemSlots, turn = n / kItemSlots;
+                const bool ok = turn == 0 || wait(MLA_BAR(item_empty) + 8 * s, (turn - 1) & 1, bars,
+                                                  p.status, kSiteItemFree);
+                if (!__all_sync(0xffffffffu, ok)) break;
                 unsigned long long drawn = 0;
                 if (lane == 0) drawn = atomicAdd(p.ticket, 1ull);
                 const int64_t index = int64_t(__shfl_sync(0xffffffffu, drawn, 0));
@@ -677,10 +686,6 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                 Item next;
                 next.head = -1;
                 if (more) next = find_item(p, index, order);
-                const uint32_t s = n % kItemSlots, turn = n / kItemSlots;
-                const bool ok = turn == 0 || wait(MLA_BAR(item_empty) + 8 * s, (turn - 1) & 1, bars,
-                                                  p.status, kSiteItemFree);
-                if (!__all_sync(0xffffffffu, ok)) break;
                 if (lane == 0) {
                     bars->items[s] = next;
                     ptx::mbar_arrive(MLA_BAR(item_full) + 8 * s);
