@@ -674,14 +674,18 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                 // The next item of all CTAs, drawn when the one before the last
                 // is done: a CTA holds two, the one it works on and the one its
                 // loads run ahead to. (One more, drawn early, left the ends of
-                // the CTAs 1.2-1.5% of the time further apart.)
+                // the CTAs 1.2-1.5% of the time further apart.) The first ones
+                // need no ticket.
                 const uint32_t s = n % kItemSlots, turn = n / kItemSlots;
                 const bool ok = turn == 0 || wait(MLA_BAR(item_empty) + 8 * s, (turn - 1) & 1, bars,
                                                   p.status, kSiteItemFree);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                unsigned long long drawn = 0;
-                if (lane == 0) drawn = atomicAdd(p.ticket, 1ull);
-                const int64_t index = int64_t(__shfl_sync(0xffffffffu, drawn, 0));
+                unsigned long long drawn = blockIdx.x;
+                if (n > 0) {
+                    if (lane == 0) drawn = gridDim.x + atomicAdd(p.ticket, 1ull);
+                    drawn = __shfl_sync(0xffffffffu, drawn, 0);
+                }
+                const int64_t index = int64_t(drawn);
                 const bool more = index < total;
                 Item next;
                 next.head = -1;

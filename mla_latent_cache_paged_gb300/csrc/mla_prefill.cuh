@@ -28,7 +28,8 @@ struct PrefillParams {
     float* o_part;            // splits > 1: fp32 [total_q, N, S, 128]
     float* lse_part;          //             fp32 [total_q, N, S]
     int32_t* status;
-    unsigned long long* ticket;   // next item (in the status header; 0 between calls)
+    unsigned long long* ticket;   // items drawn after the first of each CTA (in the status
+                                  // header; 0 between calls)
     uint32_t* done;               // CTAs that have finished
 };
 
