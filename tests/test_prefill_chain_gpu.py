@@ -137,3 +137,64 @@ def test_fork_insert_expand_prefill_decode_free_compact():
     torch.cuda.synchronize()
     assert torch.equal(again, kv[lens[0]:]) and torch.equal(again_pe, pe[lens[0]:])
     assert torch.equal(out2, out[new:])
+
+
+def test_prefill_expand_decode_and_page_calls_on_streams_of_their_own():
+    """A server overlaps them: each call's result is the one it has alone. (The
+    first fork asks for 720 tokens in rows of 11 pages and is refused each time;
+    the second one fits.)"""
+    import torch
+    rng = np.random.default_rng(78)
+    heads, lens = 32, [700, 130, 1, 513]
+    pages = [-(-n // 64) for n in lens]
+    blocks = sum(pages)
+    table = np.full((len(lens), max(pages)), -1, np.int32)
+    ids, at = rng.permutation(blocks), 0
+    for b, n in enumerate(pages):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    cache, tab, cu = _dev(_bf16(rng, (blocks, 64, 576))), _int(table), _int(np.r_[0, np.cumsum(lens)])
+    uk, uv = _dev(_bf16(rng, (heads, 128, 512), 0.05)), _dev(_bf16(rng, (heads, 512, 128), 0.05))
+    q = _dev(_bf16(rng, (sum(lens), heads, 192)))
+    kv, pe = _dev(_bf16(rng, (sum(lens), heads, 256))), _dev(_bf16(rng, (sum(lens), 64)))
+    one, latent = _dev(_bf16(rng, (4, heads, 576))), _dev(_bf16(rng, (4, heads, 512)))
+    refs, kids = _int(np.bincount(ids, minlength=blocks + 40)), _int([0, 1, 3])
+    pplan = binding.make_prefill_plan(len(lens), heads, sum(lens), max(lens), max(lens))
+    dplan = binding.make_plan(len(lens), heads, table.shape[1], seq_lens_host=lens)
+    ews, pws, dws, uws, cws, fws = (
+        binding.new_status_workspace(), binding.new_workspace(pplan), binding.new_workspace(dplan),
+        binding.new_status_workspace(), binding.new_cache_workspace(blocks + 40, 3),
+        binding.new_cache_workspace(blocks + 40, 3))
+    big = torch.zeros((blocks + 40, 64, 576), dtype=torch.uint8, device="cuda")
+    shared, room, ref_out = _int([700, 100, 64]), _int([720, 300, 64]), torch.empty_like(refs)
+    fits, ref_fits = _int([704, 300, 64]), torch.empty_like(refs)
+    calls = [
+        lambda s: binding.mla_expand_kv(cache, tab, cu, uk, uv, total_k=sum(lens), workspace=ews,
+                                        stream=s),
+        lambda s: binding.mla_prefill(q, kv, pe, cu, cu, SCALE, plan=pplan, workspace=pws, stream=s),
+        lambda s: binding.mla_decode(one, cache, tab, _int_lens, SCALE, plan=dplan, workspace=dws,
+                                     stream=s),
+        lambda s: (binding.mla_v_up_proj(latent, uv, workspace=uws, stream=s),),
+        lambda s: binding.mla_cache_fork(big, refs, tab, kids, shared, room, workspace=cws,
+                                         ref_counts_out=ref_out, stream=s),
+        lambda s: binding.mla_cache_fork(big, refs, tab, kids, shared, fits, workspace=fws,
+                                         ref_counts_out=ref_fits, stream=s),
+    ]
+    _int_lens = _int(lens)
+    bits = lambda r: [x.view(torch.int16).clone() for x in r]   # noqa: E731
+    want = []
+    for call in calls:
+        want.append(bits(call(None)))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = []
+    for _ in range(12):
+        for i, (call, stream) in enumerate(zip(calls, streams)):
+            got.append((i, call(stream)))
+    torch.cuda.synchronize()
+    for i, result in got:
+        assert all(torch.equal(a, b) for a, b in zip(bits(result), want[i])), i
+    assert torch.equal(ref_out, refs) and int((ref_fits != refs).sum()) > 0
+    assert binding.read_error(cws) == binding.MLA_ERR_BAD_SEQ_LEN
+    for ws in (ews, pws, dws, uws, fws):
+        assert binding.read_error(ws) == 0
