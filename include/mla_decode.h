@@ -559,7 +559,7 @@ typedef struct mla_prefill_plan {
     int32_t  batch;               /* B */
     int32_t  num_heads;           /* N */
     int32_t  total_q;             /* rows of q, out and lse */
-    int32_t  num_kv_splits;       /* S >= 1: parts that each sequence's keys are cut into */
+    int32_t  num_kv_splits;       /* S >= 1: parts that keys are cut into */
     int32_t  num_sms;
     int32_t  single_rows;         /* 0: tensor-core kernel; 1: CUDA-core kernel, one query
                                      row at a time */
@@ -567,7 +567,10 @@ typedef struct mla_prefill_plan {
     uint64_t partial_offset;      /* byte offset of fp32 [total_q, N, S, 128] (S > 1,
                                      single_rows = 0) */
     uint64_t lse_partial_offset;  /* byte offset of fp32 [total_q, N, S] (likewise) */
-    uint32_t reserved[6];
+    int32_t  split_rest;          /* 1: only the work that would leave SMs idle at the end is
+                                     cut, into S parts at most (single_rows = 0; the caller may
+                                     set it on a plan with S > 1, or clear it) */
+    uint32_t reserved[5];
 } mla_prefill_plan_t;
 
 /*
@@ -577,8 +580,9 @@ typedef struct mla_prefill_plan {
  *                      (they steer the kernel and S alone: longer sequences are
  *                      computed too, more slowly).
  *   num_kv_splits      S in 1..64, or 0: the planner splits the keys when the
- *                      query rows alone leave SMs idle. (With single_rows
- *                      it becomes 1, 2, 4 or 8.)
+ *                      query rows alone leave SMs idle, all of them or
+ *                      (split_rest) those of the last rows to be worked on.
+ *                      (With single_rows it becomes 1, 2, 4 or 8.)
  *   num_sms            SMs of the target device, >= 1.
  */
 int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q_len, int max_k_len,

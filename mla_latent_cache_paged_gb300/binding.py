@@ -95,7 +95,8 @@ class MlaPrefillPlan(ctypes.Structure):
         ("workspace_bytes", ctypes.c_uint64),
         ("partial_offset", ctypes.c_uint64),
         ("lse_partial_offset", ctypes.c_uint64),
-        ("reserved", ctypes.c_uint32 * 6),
+        ("split_rest", ctypes.c_int32),
+        ("reserved", ctypes.c_uint32 * 5),
     ]
 
 

@@ -27,12 +27,12 @@
 // clocks of exponentials (32,768 of them) and 80 KB of loads (32 bytes per
 // clock per SM, from L2: the items of a group of heads run together, so that
 // their keys and values stay there).
-// Measured, 4,096 causal tokens x 128 heads (361 us at cuBLAS's rate): 455-465
+// Measured, 4,096 causal tokens x 128 heads (361 us at cuBLAS's rate): 457-469
 // us; 405 us with the softmax left out, 379 us with the key and value loads
 // left out too: the score MMAs take both operands from shared memory, 128 bytes
 // a clock, which is its rate, and the loads write there as well. 24 prompts of
-// 2 to 886 tokens x 16 heads 66.7 us; four chunks of ~480 rows over 3,589 to
-// 5,711 keys x 32 heads 148 us.
+// 2 to 886 tokens x 16 heads 67.5 us; four chunks of ~480 rows over 3,589 to
+// 5,711 keys x 32 heads 146 us.
 //
 // Keys and values of a 128-key step that lie past the sequence's end belong to
 // the next sequence, and those past a row's causal limit are its own future:
@@ -68,6 +68,12 @@ constexpr int kRing = 8;                      // blocks: K of a step takes 3, V 
 constexpr int kOffRing = 2 * kQBlocks * kBlock;
 constexpr int kOffBar = kOffRing + kRing * kBlock;
 constexpr int kItemSlots = 2;
+// The next item is drawn when the loads come to an item's last steps, so that
+// a CTA with a long item does not hold another that an idle one could take:
+// 2,048 causal tokens x 32 heads 48 -> 40 us, sequences of 700 and 300 rows over
+// 6,000 and 3,000 keys x 32 heads 130 -> 93 us. (The draw takes 3,000 clocks. With
+// 1 to 3 steps the long prompt takes 1-2% more, with 5 to 8 0.5%.)
+constexpr int kNearSteps = 5;
 constexpr int kSmemBytes = kOffBar + 1024;    // base is 1 KB aligned
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr uint32_t kTmemS = 0;                // 2 x 128 columns; P overwrites the first 64 of each
@@ -77,6 +83,9 @@ constexpr float kRescaleThreshold = 8.0f;     // log2 units
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr uint32_t kSuspendNs = 20000;
 constexpr int kMaxSplits = 64;
+// In place of a row's first partial LSE: the row was not split and is written.
+// (A NaN that no arithmetic gives: results of those are 0x7fffffff.)
+constexpr uint32_t kDoneMark = 0x7fc0600du;
 // Keys and values of the heads that run together (a third of the L2).
 constexpr int64_t kGroupBytes = int64_t(40) << 20;
 
@@ -94,7 +103,7 @@ struct Item {
     int32_t step_lo;      // steps of this split, per tile [step_lo, step_hi[t])
     int32_t step_hi[2];
     int32_t fix_from;     // first step whose values need the helper
-    int32_t pad;
+    int32_t splits;       // parts that the item's keys are cut into
 };
 
 struct Bars {
@@ -111,6 +120,7 @@ struct Bars {
     // helper completes v_full.
     uint64_t raw_full[2];
     uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+    uint64_t item_near;       // the loads have come to an item's last steps
     uint64_t drain;
     Item items[kItemSlots];
     int32_t bad_item[kItemSlots];   // sequence number of an item with replaced values
@@ -243,31 +253,60 @@ __device__ __forceinline__ Order count_tiles(const PrefillParams& p) {
     return o;
 }
 
-// Everything an item's roles need, from its place in the order. The whole
-// warp works on it.
-__device__ __forceinline__ Item find_item(const PrefillParams& p, int64_t index, const Order& o) {
+// Which items are split, and how often: all of them p.splits times, or
+// (split_rest) those of the last, partly filled wave, [whole, total), which
+// would leave SMs without work for its whole length. Of that wave each CTA gets
+// one part at most, so a wave that is more than half full is not split: a
+// part's fp32 rows and its share of the merge cost about as much as three steps.
+struct Units {
+    int64_t whole, total;      // items not split, items
+    int splits;
+    __device__ __forceinline__ Units(const PrefillParams& p, const Order& o) {
+        total = 0;
+#pragma unroll
+        for (int c = 0; c < kClasses; ++c) total += o.tiles[c] * p.heads;
+        whole = 0;
+        splits = p.splits;
+        if (p.split_rest) {
+            const int rest = int(total % gridDim.x);
+            if (rest > 0) splits = min(splits, int(gridDim.x) / rest);
+            whole = rest > 0 && splits > 1 ? total - rest : total;
+        }
+    }
+    __device__ __forceinline__ int64_t count() const { return whole + (total - whole) * splits; }
+};
+
+// Everything an item's roles need, from the unit's place in the order. The
+// whole warp works on it.
+__device__ __forceinline__ Item find_item(const PrefillParams& p, int64_t index, const Order& o,
+                                          const Units& units) {
     const int lane = threadIdx.x & 31;
-    const int per_row_tile = p.heads * p.splits;
+    Item it;
+    it.splits = 1;
+    it.split = 0;
+    if (index >= units.whole) {
+        const int64_t i = index - units.whole;
+        it.splits = units.splits;
+        it.split = int(i % units.splits);
+        index = units.whole + i / units.splits;
+    }
     int cls = 0;
     int64_t tiles = o.tiles[0];
 #pragma unroll
     for (int c = 1; c < kClasses; ++c) {
-        if (cls == c - 1 && index >= tiles * per_row_tile) {
-            index -= tiles * per_row_tile;
+        if (cls == c - 1 && index >= tiles * p.heads) {
+            index -= tiles * p.heads;
             cls = c;
             tiles = o.tiles[c];
         }
     }
     const int group = cls >= kClasses / 2 ? p.heads : p.group;
-    const int64_t per_group = tiles * group * p.splits;
+    const int64_t per_group = tiles * group;
     const int head0 = int(index / per_group) * group;
     const int64_t rem = index % per_group;
-    const int per_tile = min(group, p.heads - head0) * p.splits;
+    const int per_tile = min(group, p.heads - head0);
     int64_t tile = rem / per_tile;
-    const int rest = int(rem % per_tile);
-    Item it;
-    it.head = head0 + rest / p.splits;
-    it.split = rest % p.splits;
+    it.head = head0 + int(rem % per_tile);
     // The sequence that holds the class's tile of this number.
     int q0 = 0, lq = 0, k0 = 0, lk = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -315,7 +354,7 @@ __device__ __forceinline__ Item find_item(const PrefillParams& p, int64_t index,
         steps[t] = keys / kStep + (keys % kStep != 0);
     }
     const int most = max(steps[0], steps[1]);
-    const int chunk = (most + p.splits - 1) / p.splits;
+    const int chunk = (most + it.splits - 1) / it.splits;
     it.step_lo = min(most, it.split * chunk);
     const int hi = min(most, it.step_lo + chunk);
     it.step_hi[0] = max(it.step_lo, min(hi, steps[0]));
@@ -323,7 +362,6 @@ __device__ __forceinline__ Item find_item(const PrefillParams& p, int64_t index,
     // Steps before this one lie wholly within every row's limit.
     const int whole = p.causal ? max(0, min(it.limit0 + 1, lk)) : lk;
     it.fix_from = max(it.step_lo, whole / kStep);
-    it.pad = 0;
     return it;
 }
 
@@ -377,6 +415,7 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
             ptx::mbar_init(MLA_BAR(item_empty) + 8 * s, kItemConsumers);
             bars->bad_item[s] = -1;
         }
+        ptx::mbar_init(MLA_BAR(item_near), 1);
         ptx::mbar_init(MLA_BAR(drain), 1);
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -412,7 +451,10 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                 while (ok && items.next(bars, p.status, &it)) {
                     if (it.head < 0) break;
                     const int steps = max(it.step_hi[0], it.step_hi[1]);
+                    const int near = max(it.step_lo, steps - kNearSteps);
+                    if (near >= steps) ptx::mbar_arrive(MLA_BAR(item_near));
                     for (int j = it.step_lo; j < steps && ok; ++j, ++step) {
+                        if (j == near) ptx::mbar_arrive(MLA_BAR(item_near));
                         const int row = it.k_row + j * kStep;
                         const uint32_t bar = MLA_BAR(k_full) + 8 * (step & 1);
                         ptx::mbar_arrive_expect_tx(bar, 3 * kBlock);
@@ -666,19 +708,18 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
         } else {
             // --------------------------------------------------- scheduler
             const Order order = count_tiles(p);
-            int64_t total = 0;
-#pragma unroll
-            for (int c = 0; c < kClasses; ++c) total += order.tiles[c] * p.heads * p.splits;
+            const Units units(p, order);
+            const int64_t total = units.count();
             uint32_t n = 0;
             while (true) {
-                // The next item of all CTAs, drawn when the one before the last
-                // is done: a CTA holds two, the one it works on and the one its
-                // loads run ahead to. (One more, drawn early, left the ends of
-                // the CTAs 1.2-1.5% of the time further apart.) The first ones
-                // need no ticket.
+                // The next item of all CTAs. A CTA holds two at most, the one
+                // it works on and the one its loads run ahead to. The first
+                // ones need no ticket.
                 const uint32_t s = n % kItemSlots, turn = n / kItemSlots;
-                const bool ok = turn == 0 || wait(MLA_BAR(item_empty) + 8 * s, (turn - 1) & 1, bars,
-                                                  p.status, kSiteItemFree);
+                const bool ok = (n == 0 || wait(MLA_BAR(item_near), (n - 1) & 1, bars, p.status,
+                                                kSiteItemFree)) &&
+                                (turn == 0 || wait(MLA_BAR(item_empty) + 8 * s, (turn - 1) & 1,
+                                                   bars, p.status, kSiteItemFree));
                 if (!__all_sync(0xffffffffu, ok)) break;
                 unsigned long long drawn = blockIdx.x;
                 if (n > 0) {
@@ -689,7 +730,7 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                 const bool more = index < total;
                 Item next;
                 next.head = -1;
-                if (more) next = find_item(p, index, order);
+                if (more) next = find_item(p, index, order, units);
                 if (lane == 0) {
                     bars->items[s] = next;
                     ptx::mbar_arrive(MLA_BAR(item_full) + 8 * s);
@@ -837,8 +878,15 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
             if (mine) {
                 const float lse =
                     sum == 0.f ? -INFINITY : m * (p.scale_log2 * kLn2) + logf(sum);
-                if (p.splits > 1) p.lse_part[out_row * p.splits + it.split] = lse;
-                else if (p.lse != nullptr) p.lse[out_row] = lse;
+                if (it.splits > 1) {
+                    p.lse_part[out_row * p.splits + it.split] = lse;
+                    for (int i = it.splits + it.split; i < p.splits; i += it.splits)
+                        p.lse_part[out_row * p.splits + i] = -INFINITY;   // no such part
+                } else {
+                    if (p.lse != nullptr) p.lse[out_row] = lse;
+                    if (p.split_rest)
+                        p.lse_part[out_row * p.splits] = __uint_as_float(kDoneMark);
+                }
             }
             __syncwarp();
 #pragma unroll 1
@@ -879,7 +927,7 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                             }
                         }
                     }
-                    if (p.splits > 1) {
+                    if (it.splits > 1) {
                         float* dst = p.o_part + (out_row * p.splits + it.split) * kV + c;
 #pragma unroll
                         for (int i = 0; i < 32; i += 8) {
@@ -938,6 +986,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
     const int begin = p.cu_q[lo], end = p.cu_q[lo + 1];
     if (begin < 0 || q < begin || q >= end || end > p.total_q) return;
     const float* ls = p.lse_part + row * p.splits;
+    if (p.split_rest && __float_as_uint(ls[0]) == kDoneMark) return;
     float m = -INFINITY;
     for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ls[s]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -994,6 +1043,10 @@ uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
 // A split should have at least this many key steps: fewer cost more in items
 // and merging than the extra CTAs bring.
 constexpr int kMinSplitSteps = 4;
+// Parts of the items of a last, partly filled wave, and the waves up to which
+// that pays.
+constexpr int kRestSplits = 4;
+constexpr int kRestWaves = 4;
 // The single-row kernel: CTAs an SM that its splits aim at, and the fewest
 // keys of a split.
 constexpr int kRowCtasPerSm = 4;
@@ -1050,6 +1103,16 @@ extern "C" int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q
         if (s > most) s = most;
         if (s > kMaxSplits) s = kMaxSplits;
         p.num_kv_splits = s < 1 ? 1 : int(s);
+        // Few waves of long items, the last one not half full: it is split.
+        // (80 heads, 512 rows over 8,000 keys, 160 items: 222 -> 155 us; 90 heads
+        // over 3,000 keys 92 -> 76 us. Where shorter items fill the wave anyway
+        // it costs up to 5%, 92.7 -> 98 us for 160 items of 700 and 300 rows.)
+        const int64_t rest = items % slots;
+        if (!p.single_rows && items > slots && items < slots * kRestWaves &&
+            most >= kRestSplits && rest > 0 && rest * 2 <= slots) {
+            p.num_kv_splits = kRestSplits;
+            p.split_rest = 1;
+        }
     }
     if (p.single_rows) {
         // The splits are a cluster: 1, 2, 4 or 8.
@@ -1069,7 +1132,8 @@ extern "C" int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const 
     if (!plan) return MLA_ERR_INVALID_ARG;
     if (plan->batch < 0 || plan->num_heads < 1 || plan->num_heads > kMaxHeads ||
         plan->total_q < 0 || plan->num_kv_splits < 1 || plan->num_kv_splits > kMaxSplits ||
-        plan->num_sms < 1 || (plan->single_rows & ~1) != 0 || total_k < 0)
+        plan->num_sms < 1 || (plan->single_rows & ~1) != 0 || (plan->split_rest & ~1) != 0 ||
+        (plan->split_rest != 0 && plan->single_rows != 0) || total_k < 0)
         return MLA_ERR_INVALID_ARG;
     if (plan->single_rows &&
         (plan->num_kv_splits > kMaxRowSplits || (plan->num_kv_splits & (plan->num_kv_splits - 1))))
@@ -1103,6 +1167,7 @@ extern "C" int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const 
     p.total_k = total_k;
     p.causal = causal ? 1 : 0;
     p.splits = plan->num_kv_splits;
+    p.split_rest = plan->num_kv_splits > 1 ? plan->split_rest : 0;
     p.scale_log2 = scale_log2;
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;

@@ -21,6 +21,7 @@ struct PrefillParams {
     int batch, heads, total_q, total_k;
     int causal;
     int splits;
+    int split_rest;           // only the items of the last wave are split
     int group;                // heads that run together
     float scale_log2;
     uint16_t* out;            // bf16 [total_q, N, 128]

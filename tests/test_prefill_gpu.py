@@ -373,3 +373,72 @@ def test_prefill_refuses_tensors_that_do_not_fit():
                                           device="cuda")[8:].view(10, 2, 128)), binding.MlaError)]:
         with pytest.raises(exc):
             binding.mla_prefill(**{**ok, **kw})
+
+
+REST = [
+    # q lengths, k lengths, heads, SMs of the plan (so the waves); items, those left over
+    ([300], [2300], 3, 5),                             # 6, 1
+    ([256], [2048], 5, 3),                             # 5, 2
+    ([129, 200, 70], [2500, 2200, 2049], 2, 4),        # 6, 2 of three sequences
+    ([600, 3], [2600, 90], 2, 7),                      # 8, 1 of the short ones
+    ([70, 0, 300, 5], [2100, 10, 0, 700], 3, 8),       # 12, 4, some without keys
+    ([255], [2050], 31, 16),                           # 31, 15: nearly a wave
+    ([256], [2048], 8, 4),                             # 8, none
+    ([2], [700], 4, 9),                                # 4: less than a wave
+]
+
+
+@pytest.mark.parametrize("splits", [2, 7])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", range(len(REST)))
+def test_only_the_last_wave_is_split(case, causal, splits):
+    import torch
+    q_lens, k_lens, heads, sms = REST[case]
+    q, kv, pe = _problem(900 + case, q_lens, k_lens, heads, q_scale=2.0)
+    n, spare = sum(q_lens), 4
+    plan = binding.make_prefill_plan(len(q_lens), heads, n + spare, max(q_lens), max(k_lens),
+                                     num_sms=sms, num_kv_splits=splits)
+    plan.split_rest = 1
+    out = _dev(np.full((n + spare, heads, 128), FILL, np.uint16))
+    lse = torch.full((n + spare, heads), 77.0, device="cuda")
+    ws = binding.new_workspace(plan)
+    ws[binding.STATUS_BYTES:].fill_(0xA5)              # what an earlier call left behind
+    q_all = _dev(np.concatenate([q, np.full((spare, heads, 192), 0x7FC0, np.uint16)]))
+    args = (q_all, _dev(kv), _dev(pe), _int(_starts(q_lens)), _int(_starts(k_lens)), SCALE)
+    for _ in range(2):                                 # and this call itself
+        binding.mla_prefill(*args, causal=causal, plan=plan, workspace=ws, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert binding.read_error(ws) == 0
+    bits, z = bf16_tensor_bits(out), lse.cpu().numpy().astype(np.float64)
+    assert (bits[n:] == FILL).all() and (z[n:] == 77.0).all()
+    _check(bits[:n], z[:n], q, kv, pe, q_lens, k_lens, causal)
+    again = binding.mla_prefill(*args, causal=causal, plan=plan, workspace=ws, return_lse=False)
+    assert again[1] is None
+    assert torch.equal(again[0][:n].view(torch.int16), out[:n].view(torch.int16))
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_split_and_whole_rows_with_values_that_are_not_finite(value):
+    """A result that is NaN is not taken for the mark of a row that was not split."""
+    import torch
+    q, kv, pe = _problem(920, [300], [2300], 3)
+    kv[5, 1, 128:] = 0x7FC0 if np.isnan(value) else 0x7F80
+    kv[7, 2, 0] = kv[9, 0, 3] = 0x7FC0
+    want = None
+    for sms, split in ((5, 1), (152, 0)):
+        plan = binding.make_prefill_plan(1, 3, 300, 300, 2300, num_sms=sms,
+                                         num_kv_splits=4 if split else 1)
+        plan.split_rest = split
+        ws = binding.new_workspace(plan)
+        out, lse = binding.mla_prefill(_dev(q), _dev(kv), _dev(pe), _int([0, 300]), _int([0, 2300]),
+                                       SCALE, plan=plan, workspace=ws)
+        torch.cuda.synchronize()
+        assert binding.read_error(ws) == 0
+        got = (torch.isnan(out), torch.isinf(out), torch.isnan(lse))
+        if want is not None:
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        want = got
+    # (each query sees key 7 and key 9: heads 0 and 2 are NaN; head 1 is what its value is)
+    nan, inf, nan_z = want
+    assert nan[:, [0, 2]].all() and nan_z[:, [0, 2]].all() and not nan_z[:, 1].any()
+    assert (nan if np.isnan(value) else inf)[:, 1].all()

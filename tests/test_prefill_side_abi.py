@@ -250,3 +250,32 @@ def test_prefill_refuses_an_edited_plan(lib, field, value):
     setattr(plan, field, value)
     assert lib.mla_prefill(ctypes.byref(plan), X, X, X, 2000, X, X, 1, 0.1, X, None, X, 1 << 30,
                            None) == binding.MLA_ERR_INVALID_ARG
+
+
+def test_prefill_plan_splits_the_rest_of_few_waves(lib):
+    """More work than SMs, but few waves of it, the last one less than half
+    full, and keys that are long enough."""
+    def rest(**kw):
+        p = _plan(lib, splits=0, **kw)[1]
+        return p.split_rest, p.num_kv_splits > 1
+    few = dict(batch=1, heads=80, total_q=512, max_q=512, max_k=8000)
+    assert rest(**few) == (1, True)                                # 160 items
+    assert rest(**{**few, "heads": 64}) == (0, False)             # 128: one wave, not split
+    assert rest(**{**few, "heads": 120}) == (0, False)            # 240: the last is half full
+    assert rest(**{**few, "heads": 76}) == (0, False)             # 152: no rest
+    assert rest(**{**few, "max_k": 2000}) == (0, False)           # short
+    assert rest(**{**few, "batch": 6, "total_q": 3070}) == (0, False)   # 6.3 waves
+    assert rest(**{**few, "total_q": 1, "max_q": 1}) == (0, True)  # single rows: a cluster
+    assert _plan(lib, splits=4, **few)[1].split_rest == 0         # asked for
+
+
+@pytest.mark.parametrize("field,value", [("split_rest", 2), ("split_rest", -1)])
+def test_prefill_refuses_an_edited_rest(lib, field, value):
+    plan = _plan(lib, splits=3)[1]
+    setattr(plan, field, value)
+    assert lib.mla_prefill(ctypes.byref(plan), X, X, X, 2000, X, X, 1, 0.1, X, None, X, 1 << 30,
+                           None) == binding.MLA_ERR_INVALID_ARG
+    single = _plan(lib, max_q=1, splits=2)[1]
+    single.split_rest = 1
+    assert lib.mla_prefill(ctypes.byref(single), X, X, X, 2000, X, X, 1, 0.1, X, None, X, 1 << 30,
+                           None) == binding.MLA_ERR_INVALID_ARG
