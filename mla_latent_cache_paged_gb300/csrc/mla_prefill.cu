@@ -1044,9 +1044,9 @@ uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
 // and merging than the extra CTAs bring.
 constexpr int kMinSplitSteps = 4;
 // Parts of the items of a last, partly filled wave, and the waves up to which
-// that pays (512 rows over 8,000 keys x 384 heads and sequences, 5.1 waves: 695
-// -> 626 us; over 3,000 keys x 768, 10.1 waves: 496 -> 517 us, for the merge
-// looks at every row).
+// that pays (3 sequences of 512 rows over 8,000 keys, 128 heads, 5.1 waves: 690
+// -> 626 us; 6 over 3,000 keys, 10.1 waves: 496 -> 517 us, for the merge looks
+// at every row).
 constexpr int kRestSplits = 4;
 constexpr int kRestWaves = 6;
 // The single-row kernel: CTAs an SM that its splits aim at, and the fewest
