@@ -442,3 +442,24 @@ def test_split_and_whole_rows_with_values_that_are_not_finite(value):
     nan, inf, nan_z = want
     assert nan[:, [0, 2]].all() and nan_z[:, [0, 2]].all() and not nan_z[:, 1].any()
     assert (nan if np.isnan(value) else inf)[:, 1].all()
+
+
+def test_new_results_are_ordinary_tensors(monkeypatch):
+    """Allocated either way, with and without rows: contiguous, of the stated
+    type and shape, and the same bits."""
+    import torch
+    q, kv, pe = _problem(930, [5], [9], 2)
+    args = (_dev(q), _dev(kv), _dev(pe), _int([0, 5]), _int([0, 9]), SCALE)
+    got = [binding.mla_prefill(*args)]
+    assert binding._empty_strided is not None
+    monkeypatch.setitem(__import__("sys").modules, "torch._C._dynamo.guards", None)
+    monkeypatch.setattr(binding, "_empty_strided", None)
+    got.append(binding.mla_prefill(*args))
+    got.append(binding.mla_prefill(*args, stream=torch.cuda.current_stream()))
+    none = binding.mla_prefill(_dev(q[:0]), _dev(kv), _dev(pe), _int([0, 0]), _int([0, 9]), SCALE)
+    for out, lse in got:
+        assert out.shape == (5, 2, 128) and out.dtype == torch.bfloat16 and out.is_contiguous()
+        assert lse.shape == (5, 2) and lse.dtype == torch.float32 and lse.is_contiguous()
+        assert out.device == args[0].device and torch.equal(out, got[0][0])
+        assert torch.equal(lse, got[0][1])
+    assert none[0].shape == (0, 2, 128) and none[1].shape == (0, 2)
