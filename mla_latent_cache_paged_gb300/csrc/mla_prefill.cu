@@ -1179,7 +1179,7 @@ extern "C" int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const 
     p.ticket = reinterpret_cast<unsigned long long*>(ws + 4 * kTicketWord);
     p.done = reinterpret_cast<uint32_t*>(ws + 4 * kDoneCtasWord);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int e = plan->single_rows ? launch_prefill_row(p, stream)
+    const int e = plan->single_rows ? launch_prefill_row(p, plan->num_sms, stream)
                                     : launch_prefill_tiles(p, plan->num_sms, st);
     if (e != 0) return MLA_ERR_CUDA;
     if (p.splits > 1 && !plan->single_rows) {

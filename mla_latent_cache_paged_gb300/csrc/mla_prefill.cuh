@@ -56,6 +56,6 @@ __device__ __forceinline__ void sequence(const PrefillParams& p, int b, int* q0,
 // The single-row kernel (mla_prefill_row.cu): items of one query row, one head
 // and one split.
 constexpr int kMaxRowSplits = 8;     // the CTAs of a cluster
-int launch_prefill_row(const PrefillParams& p, void* stream);
+int launch_prefill_row(const PrefillParams& p, int num_sms, void* stream);
 
 }  // namespace mla

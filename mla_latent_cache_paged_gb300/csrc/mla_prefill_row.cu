@@ -16,11 +16,15 @@
 // item are the CTAs of a cluster and are joined in the first one's shared
 // memory. Weights stay in fp32, and keys that a row does not see are not read.
 //
-// Measured (CTAs of 128 threads, 2 keys a group in flight, 4 CTAs an SM; 256
-// threads or 3-4 keys were up to 20% slower at most of these): 8 sequences of
-// 186 to 1,400 keys, 16 heads, 14.4 us (54 MB: 8.0 us at the measured HBM
-// rate); 64 x 2,048 keys, 16 heads, 175 us (6.2 TB/s); 4 x 2,048 keys, 128
-// heads, 88 us (6.1 TB/s).
+// Measured with the keys in HBM (3 keys a group in flight: 128 registers, 512
+// threads an SM; 2 and 4 keys were 6-17% slower where there are many items): 8
+// sequences of 186 to 1,400 keys, 16 heads, 16.6 us (54 MB: 8.0 us at the
+// measured HBM rate; the longest ones' chain of reads is what takes the time);
+// 64 x 2,048 keys, 16 heads, 165 us (6.6 TB/s); 4 x 2,048 keys, 128 heads, 83 us
+// (6.5 TB/s). Where there are fewer CTAs than the SMs hold, each has more
+// threads: 8,000 keys, 16 heads, in 8 splits 30.3 us with 128 threads, 20.9 with
+// 256 and 26.5 with 512 (clusters of 8 such CTAs do not all find room at once);
+// 4,000 and 300 keys 17.7 and 13.8 with 128 and 256.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -32,11 +36,8 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = kThreads / 8;
-constexpr int kCtasPerSm = 4;
-constexpr int kKeys = 2;              // keys of a group in flight
+constexpr int kSmThreads = 512;       // at 128 registers
+constexpr int kKeys = 3;              // keys of a group in flight
 
 // 8 bf16 values of 16 bytes.
 __device__ __forceinline__ void widen8(const uint4& u, float* f) {
@@ -68,7 +69,11 @@ __device__ __forceinline__ void join(const float* m, const float* l, const float
     }
 }
 
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill_row_kernel(const PrefillParams p) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, kSmThreads / kThreads)
+prefill_row_kernel(const PrefillParams p) {
+    constexpr int kWarps = kThreads / 32;
+    constexpr int kGroups = kThreads / 8;
     __shared__ float part_m[kWarps], part_l[kWarps], part_o[kWarps][kPrefillV];
     // (read in the cluster's first CTA only)
     __shared__ float split_m[kMaxRowSplits], split_l[kMaxRowSplits];
@@ -221,10 +226,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill_row_kernel(const
 
 }  // namespace
 
-int launch_prefill_row(const PrefillParams& p, void* stream) {
+int launch_prefill_row(const PrefillParams& p, int num_sms, void* stream) {
+    // As many threads a CTA as the SMs have room for (half of it with the
+    // largest: a cluster's CTAs want SMs of one cluster region).
+    const int64_t ctas = int64_t(p.total_q) * p.heads * p.splits;
+    const int threads = 2 * ctas <= num_sms ? 512 : ctas <= 2 * int64_t(num_sms) ? 256 : 128;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(p.total_q), unsigned(p.heads), unsigned(p.splits));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(unsigned(threads));
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -233,7 +242,11 @@ int launch_prefill_row(const PrefillParams& p, void* stream) {
     attr[0].val.clusterDim.z = unsigned(p.splits);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return int(cudaLaunchKernelEx(&cfg, prefill_row_kernel, p));
+    return int(cudaLaunchKernelEx(&cfg,
+                                  threads == 512   ? prefill_row_kernel<512>
+                                  : threads == 256 ? prefill_row_kernel<256>
+                                                   : prefill_row_kernel<128>,
+                                  p));
 }
 
 }  // namespace mla
