@@ -690,12 +690,19 @@ def make_prefill_plan(batch, num_heads, total_q, max_q_len, max_k_len, *, num_kv
 
 
 def mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, softmax_scale, *, causal=True, plan=None,
-                num_kv_splits=0, out=None, lse=None, return_lse=True, workspace=None, stream=None):
+                max_q_len=None, max_k_len=None, num_kv_splits=0, out=None, lse=None,
+                return_lse=True, workspace=None, stream=None):
     """Expanded-form attention of packed sequences: ``q [Tq, N, 192]`` over
     ``kv [Tk, N, 256] = [k_nope | v]`` and ``k_pe [Tk, 64]``; query i of a
     sequence sees its keys up to ``Lk - Lq + i`` (``causal``) or all of them.
     Returns ``(out bf16 [Tq, N, 128], lse fp32 [Tq, N] | None)``; rows past
-    ``cu_seqlens_q[B]`` are not written."""
+    ``cu_seqlens_q[B]`` are not written.
+
+    Without a ``plan`` the call makes one for sequences of up to ``max_q_len``
+    queries and ``max_k_len`` keys; a length that is not given (the starts lie
+    on the device) is taken to be the same for all: ``Tq / B``, ``Tk / B``. The
+    lengths pick the kernel and the splits alone; longer sequences are computed
+    too, more slowly."""
     import torch
     bf16, i32 = torch.bfloat16, torch.int32
     dev = _device_of("q", q)
@@ -705,7 +712,11 @@ def mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, softmax_scale, *, causa
     if B < 0:
         raise ValueError("cu_seqlens_q must be [B + 1]")
     if plan is None:
-        plan = make_prefill_plan(B, N, T, T, Tk, num_kv_splits=num_kv_splits)
+        seqs = max(B, 1)
+        plan = make_prefill_plan(
+            B, N, T, -(-T // seqs) if max_q_len is None else max_q_len,
+            -(-Tk // seqs) if max_k_len is None else max_k_len, num_kv_splits=num_kv_splits,
+            num_sms=torch.cuda.get_device_properties(dev).multi_processor_count)
     elif plan.batch != B or plan.num_heads != N or plan.total_q != T:
         raise ValueError(f"the plan is for (B, N, total_q) = "
                          f"{plan.batch, plan.num_heads, plan.total_q}, not {B, N, T}")
