@@ -562,36 +562,24 @@ def _arg(name, t, dtype, device, shape=None):
     raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-_empty_strided = None
-
-
-def _find_empty_strided():
-    """PyTorch's allocation without its argument parsing (what its compiler's
-    generated code calls): on the current device and stream, and 1-2 us less per
-    result of a call that takes 14-20."""
-    global _empty_strided
-    try:
-        from torch._C._dynamo.guards import _empty_strided_cuda as _empty_strided
-    except ImportError:
-        import torch
-
-        def _empty_strided(size, stride, dtype):
-            return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
-    return _empty_strided
+_empty_strided = None    # torch.empty_strided, once a call has needed it
 
 
 def _result(name, t, shape, dtype, device, stream):
     """The result tensor `t` of one to three dimensions, or a new one, and its address."""
-    import torch
+    global _empty_strided
     if t is not None:
         return t, _arg(name, t, dtype, device, shape)
-    if stream is not None or torch._C._cuda_getDevice() != device.index:
+    if stream is not None:
         t = _empty(shape, dtype, device, stream)
     else:
+        if _empty_strided is None:
+            import torch
+            _empty_strided = torch.empty_strided
         n = len(shape)
         strides = ((1,) if n == 1 else (shape[1], 1) if n == 2
                    else (shape[1] * shape[2], shape[2], 1))
-        t = (_empty_strided or _find_empty_strided())(shape, strides, dtype)
+        t = _empty_strided(shape, strides, dtype=dtype, device=device)
     return t, t.data_ptr()
 
 
