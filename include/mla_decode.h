@@ -547,7 +547,10 @@ int mla_expand_kv_fp8(const void* latent_cache_fp8, float k_scale, int64_t num_b
  *                            + q[i, n, 128:192] . k_pe[j])
  *     lse[i, n] = ln sum_j exp(s),  out[i, n] = sum_j exp(s - lse) kv[j, n, 128:256]
  * A query that sees no key gets out = 0, lse = -inf. A value outside what a
- * query sees, whatever it holds, does not reach its result. Context that does
+ * query sees, whatever it holds, does not reach its result; one that it sees
+ * and that is NaN or infinite counts as its weight in fp32 times itself,
+ * wherever it lies (so an infinity whose weight underflows to 0, and a NaN
+ * whatever its weight, give NaN). Context that does
  * not fit in one call: attend to it chunk by chunk and combine the results
  * with mla_dcp_combine (out and lse stacked chunk-major).
  *

@@ -40,7 +40,7 @@
 // infinity of V out of the product. So, in the steps where some row's limit
 // falls, a helper warp clears V's rows past the end and replaces non-finite
 // values by 0 before the tensor pipe reads them; if it replaced any, the
-// epilogue adds them to the rows that do see them.
+// epilogue adds them, times their weights, to the rows that do see them.
 //
 // Warps: 0-3 and 4-7 = softmax and epilogue of the tiles, 8 = loads (TMA), 9 =
 // MMAs, 10 = helper, 11 = item scheduler. Every wait is bounded
@@ -165,6 +165,27 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
 // sum += 0 * x for a pair of bf16 values.
 __device__ __forceinline__ void add_zero_times(uint32_t x, uint32_t* sum) {
     asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(*sum) : "r"(x), "r"(0));
+}
+
+// q . k of one row (of q [total_q, N]) and one key, not scaled. For the few
+// that need it outside the tensor pipe: rolled loops, little code.
+__device__ __forceinline__ float score(const PrefillParams& p, int64_t q_row, int k_row, int head) {
+    const uint4* q = reinterpret_cast<const uint4*>(p.q + q_row * kQk);
+    const uint4* k = reinterpret_cast<const uint4*>(
+        p.kv + (int64_t(k_row) * p.heads + head) * kKvHead);
+    const uint4* pe = reinterpret_cast<const uint4*>(p.k_pe + int64_t(k_row) * kRope);
+    float s = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < kQk / 8; ++i) {
+        const uint4 a = __ldg(q + i), b = __ldg(i < 16 ? k + i : pe + (i - 16));
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), s);
+            s = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), s);
+        }
+    }
+    return s;
 }
 
 // Pairs of floats: one instruction for two (round to nearest, as the single ones).
@@ -904,26 +925,38 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
                     if (repair) {
                         // The values the helper took out of the product, for
-                        // the keys this row sees: its weight is > 0, so a NaN
-                        // or infinity comes through whatever the weight.
+                        // the keys this row sees, times their weight: an
+                        // infinity whose weight is 0 in fp32 gives NaN, as it
+                        // does in the product.
                         const int last = min(limit, hi * kStep - 1);
 #pragma unroll 1
                         for (int k = it.fix_from * kStep; k <= last; ++k) {
                             const uint4* vr = reinterpret_cast<const uint4*>(
                                 p.kv + (int64_t(it.k_row + k) * p.heads + it.head) * kKvHead +
                                 128 + c);
+                            uint32_t u[16];
+                            bool any = false;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const uint4 x = __ldg(vr + i);
-                                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                                u[4 * i] = x.x;
+                                u[4 * i + 1] = x.y;
+                                u[4 * i + 2] = x.z;
+                                u[4 * i + 3] = x.w;
+                            }
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if ((u[e] & 0x7f80u) == 0x7f80u)
-                                        f[8 * i + 2 * e] += __uint_as_float(u[e] << 16);
-                                    if ((u[e] & 0x7f800000u) == 0x7f800000u)
-                                        f[8 * i + 2 * e + 1] +=
-                                            __uint_as_float(u[e] & 0xffff0000u);
-                                }
+                            for (int i = 0; i < 16; ++i)
+                                any = any || (u[i] & 0x7f80u) == 0x7f80u ||
+                                      (u[i] & 0x7f800000u) == 0x7f800000u;
+                            if (!any) continue;
+                            const float w = ptx::ex2((score(p, out_row, it.k_row + k, it.head) - m) *
+                                                     p.scale_log2);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                if ((u[i] & 0x7f80u) == 0x7f80u)
+                                    f[2 * i] += w * __uint_as_float(u[i] << 16);
+                                if ((u[i] & 0x7f800000u) == 0x7f800000u)
+                                    f[2 * i + 1] += w * __uint_as_float(u[i] & 0xffff0000u);
                             }
                         }
                     }
