@@ -567,12 +567,14 @@ typedef struct mla_prefill_plan {
     int32_t  single_rows;         /* 0: tensor-core kernel; 1: CUDA-core kernel, one query
                                      row at a time */
     uint64_t workspace_bytes;
-    uint64_t partial_offset;      /* byte offset of fp32 [total_q, N, S, 128] (S > 1,
-                                     single_rows = 0) */
-    uint64_t lse_partial_offset;  /* byte offset of fp32 [total_q, N, S] (likewise) */
+    uint64_t partial_offset;      /* byte offset of the partial rows (S > 1, single_rows = 0):
+                                     fp32 [total_q, N, S, 128], or with split_rest [P, 256, 128],
+                                     P <= num_sms */
+    uint64_t lse_partial_offset;  /* byte offset of their LSEs, fp32 (likewise) */
     int32_t  split_rest;          /* 1: only the work that would leave SMs idle at the end is
-                                     cut, into S parts at most (single_rows = 0; the caller may
-                                     set it on a plan with S > 1, or clear it) */
+                                     cut, into S parts at most (single_rows = 0). The caller may
+                                     set it on a plan with S > 1; cleared on a plan that
+                                     mla_prefill_plan made with it, no keys are cut. */
     uint32_t reserved[5];
 } mla_prefill_plan_t;
 

@@ -24,6 +24,7 @@ constexpr int kSegmentCostPages = 5;
 constexpr int kTicketWord = 2;
 constexpr int kDoneCtasWord = 4;
 constexpr int kPageBarrierWord = 5;
+constexpr int kRestWord = 6;
 constexpr int kReadyWord = 64;
 constexpr int kDoneWord = kReadyWord + kMaxBalancedBatch;
 constexpr int kPieceArrivals = 8;   // increments of kReadyWord + b per partial row set
@@ -34,6 +35,8 @@ static_assert((kDoneWord + kMaxBalancedBatch) * 4 <= int(kStatusBytes), "status 
 //   [1] detail: the offending block id / seq_len / wait site
 //   [kTicketWord, +1], [kDoneCtasWord]  mla_prefill: the next item to draw
 //                     (64 bits) and the CTAs done; 0 between calls
+//   [kRestWord, +1]   mla_prefill, only the last items split: how many, and
+//                     their parts (written by each such call for its merge)
 //   [kPageBarrierWord] page bookkeeping: arrivals at the call's grid barriers;
 //                     0 between calls
 //   [kReadyWord + b]  page-balanced schedule: softmax warps (4 per CTA, both

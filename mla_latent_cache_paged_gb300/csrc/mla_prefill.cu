@@ -83,9 +83,6 @@ constexpr float kRescaleThreshold = 8.0f;     // log2 units
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr uint32_t kSuspendNs = 20000;
 constexpr int kMaxSplits = 64;
-// In place of a row's first partial LSE: the row was not split and is written.
-// (A NaN that no arithmetic gives: results of those are 0x7fffffff.)
-constexpr uint32_t kDoneMark = 0x7fc0600du;
 // Keys and values of the heads that run together (a third of the L2).
 constexpr int64_t kGroupBytes = int64_t(40) << 20;
 
@@ -94,7 +91,6 @@ enum PrefillSite : int32_t { kSiteItem = 70, kSiteItemFree, kSiteQ, kSiteQFree, 
 
 struct Item {
     int32_t head;         // -1: no more items
-    int32_t split;
     int32_t q_row;        // packed row of the item's first query
     int32_t q_rows;       // its queries (1..256)
     int32_t k_row;        // packed row of the sequence's first key
@@ -103,7 +99,8 @@ struct Item {
     int32_t step_lo;      // steps of this split, per tile [step_lo, step_hi[t])
     int32_t step_hi[2];
     int32_t fix_from;     // first step whose values need the helper
-    int32_t splits;       // parts that the item's keys are cut into
+    int32_t part_stride;  // 0: all of the item's keys. Else this is a part of them, and query i's
+    int64_t part_row;     // result is partial row part_row + i * part_stride
 };
 
 struct Bars {
@@ -303,13 +300,13 @@ __device__ __forceinline__ Item find_item(const PrefillParams& p, int64_t index,
                                           const Units& units) {
     const int lane = threadIdx.x & 31;
     Item it;
-    it.splits = 1;
-    it.split = 0;
+    int splits = 1, split = 0;
+    int64_t part = 0;
     if (index >= units.whole) {
-        const int64_t i = index - units.whole;
-        it.splits = units.splits;
-        it.split = int(i % units.splits);
-        index = units.whole + i / units.splits;
+        part = index - units.whole;
+        splits = units.splits;
+        split = int(part % splits);
+        index = units.whole + part / splits;
     }
     int cls = 0;
     int64_t tiles = o.tiles[0];
@@ -375,14 +372,18 @@ __device__ __forceinline__ Item find_item(const PrefillParams& p, int64_t index,
         steps[t] = keys / kStep + (keys % kStep != 0);
     }
     const int most = max(steps[0], steps[1]);
-    const int chunk = (most + it.splits - 1) / it.splits;
-    it.step_lo = min(most, it.split * chunk);
+    const int chunk = (most + splits - 1) / splits;
+    it.step_lo = min(most, split * chunk);
     const int hi = min(most, it.step_lo + chunk);
     it.step_hi[0] = max(it.step_lo, min(hi, steps[0]));
     it.step_hi[1] = max(it.step_lo, min(hi, steps[1]));
     // Steps before this one lie wholly within every row's limit.
     const int whole = p.causal ? max(0, min(it.limit0 + 1, lk)) : lk;
     it.fix_from = max(it.step_lo, whole / kStep);
+    // (parts of the last wave: one per CTA at most)
+    it.part_stride = splits == 1 ? 0 : p.split_rest ? 1 : p.heads * splits;
+    it.part_row = p.split_rest ? part * kItemRows
+                               : (int64_t(it.q_row) * p.heads + it.head) * splits + split;
     return it;
 }
 
@@ -731,6 +732,10 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
             const Order order = count_tiles(p);
             const Units units(p, order);
             const int64_t total = units.count();
+            if (p.split_rest && blockIdx.x == 0 && lane == 0) {   // for the merge
+                p.rest[0] = int(units.total - units.whole);
+                p.rest[1] = units.splits;
+            }
             uint32_t n = 0;
             while (true) {
                 // The next item of all CTAs. A CTA holds two at most, the one
@@ -896,19 +901,16 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
             const bool mine = in_item < it.q_rows;
             const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (a NaN sum stays NaN)
             const int64_t out_row = int64_t(it.q_row + in_item) * p.heads + it.head;
+            const int64_t part_row = it.part_row + int64_t(in_item) * it.part_stride;
             if (mine) {
                 const float lse =
                     sum == 0.f ? -INFINITY : m * (p.scale_log2 * kLn2) + logf(sum);
-                if (it.splits > 1) {
-                    p.lse_part[out_row * p.splits + it.split] = lse;
-                    for (int i = it.splits + it.split; i < p.splits; i += it.splits)
-                        p.lse_part[out_row * p.splits + i] = -INFINITY;   // no such part
-                } else {
-                    if (p.lse != nullptr) p.lse[out_row] = lse;
-                    if (p.split_rest)
-                        p.lse_part[out_row * p.splits] = __uint_as_float(kDoneMark);
-                }
+                if (it.part_stride != 0)
+                    p.lse_part[part_row] = lse;
+                else if (p.lse != nullptr)
+                    p.lse[out_row] = lse;
             }
+            if (it.part_stride != 0 && p.split_rest) p.rest_rows[part_row] = mine ? out_row : -1;
             __syncwarp();
 #pragma unroll 1
             for (int c = 0; c < kV; c += 32) {
@@ -960,8 +962,8 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                             }
                         }
                     }
-                    if (it.splits > 1) {
-                        float* dst = p.o_part + (out_row * p.splits + it.split) * kV + c;
+                    if (it.part_stride != 0) {
+                        float* dst = p.o_part + part_row * kV + c;
 #pragma unroll
                         for (int i = 0; i < 32; i += 8) {
                             uint32_t w[8];
@@ -1002,34 +1004,21 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
 #undef MLA_BAR
 }
 
-// The splits' partial rows into the result, with the identity of
-// mla_merge_splits; only rows that a sequence holds are written. One warp per
-// (row, head), four columns per lane.
-__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p) {
+// One row's n partial rows, `stride` rows apart, into the result, with the
+// identity of mla_merge_splits. A warp, four columns per lane.
+__device__ __forceinline__ void merge_row(const PrefillParams& p, int64_t row, int64_t first,
+                                          int64_t stride, int n) {
     const int lane = threadIdx.x & 31;
-    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (row >= int64_t(p.total_q) * p.heads) return;
-    // The row's sequence: the last b with cu_q[b] <= q.
-    const int q = int(row / p.heads);
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu_q[mid] <= q) lo = mid; else hi = mid;
-    }
-    const int begin = p.cu_q[lo], end = p.cu_q[lo + 1];
-    if (begin < 0 || q < begin || q >= end || end > p.total_q) return;
-    const float* ls = p.lse_part + row * p.splits;
-    if (p.split_rest && __float_as_uint(ls[0]) == kDoneMark) return;
     float m = -INFINITY;
-    for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ls[s]);
+    for (int s = 0; s < n; ++s) m = fmaxf(m, p.lse_part[first + s * stride]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float z = 0.f;
-    for (int s = 0; s < p.splits; ++s) {
-        const float l = ls[s];
+    for (int s = 0; s < n; ++s) {
+        const float l = p.lse_part[first + s * stride];
         if (l == -INFINITY) continue;
         const float w = expf(l - m);   // (NaN where a partial is NaN)
         const float4 v = *reinterpret_cast<const float4*>(
-            p.o_part + (row * p.splits + s) * kV + lane * 4);
+            p.o_part + (first + s * stride) * kV + lane * 4);
         z += w;
         acc.x = fmaf(w, v.x, acc.x);
         acc.y = fmaf(w, v.y, acc.y);
@@ -1042,6 +1031,36 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
     o.y = pack_bf16(acc.z * inv, acc.w * inv);
     *reinterpret_cast<uint2*>(p.out + row * kV + lane * 4) = o;
     if (lane == 0 && p.lse != nullptr) p.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
+}
+
+// Every item was split: one warp per (row, head); only rows that a sequence
+// holds are written.
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p) {
+    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= int64_t(p.total_q) * p.heads) return;
+    // The row's sequence: the last b with cu_q[b] <= q.
+    const int q = int(row / p.heads);
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu_q[mid] <= q) lo = mid; else hi = mid;
+    }
+    const int begin = p.cu_q[lo], end = p.cu_q[lo + 1];
+    if (begin < 0 || q < begin || q >= end || end > p.total_q) return;
+    merge_row(p, row, row * p.splits, 1, p.splits);
+}
+
+// The items of the last wave were split: one warp per row of the most items
+// there can be. (What the tensor kernel left is checked against what there is
+// room for: after an expired wait it may be an earlier call's.)
+__global__ void __launch_bounds__(256) prefill_merge_rest_kernel(const PrefillParams p) {
+    const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int item = int(i / kItemRows), splits = p.rest[1];
+    if (item >= p.rest[0] || splits < 1 || int64_t(p.rest[0]) * splits > p.rest_parts) return;
+    const int64_t first = int64_t(item) * splits * kItemRows + i % kItemRows;
+    const int64_t row = p.rest_rows[first];
+    if (row < 0 || row >= int64_t(p.total_q) * p.heads) return;
+    merge_row(p, row, first, kItemRows, splits);
 }
 
 // The tensor kernel.
@@ -1077,9 +1096,10 @@ uint64_t round256(uint64_t x) { return (x + 255) / 256 * 256; }
 // and merging than the extra CTAs bring.
 constexpr int kMinSplitSteps = 4;
 // Parts of the items of a last, partly filled wave, and the waves up to which
-// that pays (3 sequences of 512 rows over 8,000 keys, 128 heads, 5.1 waves: 690
-// -> 626 us; 6 over 3,000 keys, 10.1 waves: 496 -> 517 us, for the merge looks
-// at every row).
+// they are planned: with more of them the wave counts for less (3 sequences of
+// 512 rows over 8,000 keys, 128 heads, 5.1 waves: 675 -> 608 us; 6 over 3,000
+// keys, 10.1 waves: 500 -> 478 us; 4 of 1,024 rows over 4,000 keys, 118 heads,
+// 12.4 waves: 721 and 725 us).
 constexpr int kRestSplits = 4;
 constexpr int kRestWaves = 6;
 // The single-row kernel: CTAs an SM that its splits aim at, and the fewest
@@ -1087,15 +1107,46 @@ constexpr int kRestWaves = 6;
 constexpr int kRowCtasPerSm = 4;
 constexpr int kMinSplitKeys = 128;
 
-void layout(mla_prefill_plan_t* p) {
-    p->partial_offset = kStatusBytes;
-    p->lse_partial_offset = kStatusBytes;
-    p->workspace_bytes = kStatusBytes;
-    if (p->num_kv_splits > 1 && !p->single_rows) {
-        const uint64_t rows = uint64_t(p->total_q) * p->num_heads * p->num_kv_splits;
-        p->lse_partial_offset = p->partial_offset + round256(rows * kV * 4);
-        p->workspace_bytes = p->lse_partial_offset + round256(rows * 4);
+// What a split call keeps in its workspace, by byte offset: fp32 rows of
+// partial results, their LSEs and (split_rest) the result rows they belong to.
+struct Partials {
+    uint64_t rows, lse, rest_rows, end;
+    int64_t rest_parts;
+};
+
+// All items split: S partial rows per (query, head). Only those of the last
+// wave split: 256 rows for each of its parts, of which there is one per CTA at
+// most, whatever the number of queries (512 rows of 3 sequences, 128 heads: 20
+// MB, where S rows for every query are 406).
+Partials partials(const mla_prefill_plan_t& p, bool rest) {
+    Partials l{};
+    l.rows = l.lse = l.rest_rows = l.end = kStatusBytes;
+    if (p.num_kv_splits <= 1 || p.single_rows) return l;
+    uint64_t rows = uint64_t(p.total_q) * p.num_heads * p.num_kv_splits;
+    if (rest) {
+        const int64_t most =
+            (int64_t(p.total_q) / kItemRows + p.batch) * p.num_heads * p.num_kv_splits;
+        l.rest_parts = most < p.num_sms ? most : p.num_sms;
+        rows = uint64_t(l.rest_parts) * kItemRows;
     }
+    l.lse = l.rows + round256(rows * kV * 4);
+    l.rest_rows = l.lse + round256(rows * 4);
+    l.end = l.rest_rows + (rest ? round256(rows * 8) : 0);
+    return l;
+}
+
+// The workspace of a plan. One that splits all items has room for the other
+// way too, so that a caller may set split_rest on it.
+void layout(mla_prefill_plan_t* p) {
+    const Partials l = partials(*p, p->split_rest != 0), other = partials(*p, true);
+    p->partial_offset = l.rows;
+    p->lse_partial_offset = l.lse;
+    p->workspace_bytes = l.end > other.end ? l.end : other.end;
+}
+
+bool same_layout(const mla_prefill_plan_t& a, const mla_prefill_plan_t& b) {
+    return a.partial_offset == b.partial_offset && a.lse_partial_offset == b.lse_partial_offset &&
+           a.workspace_bytes == b.workspace_bytes;
 }
 
 }  // namespace
@@ -1139,9 +1190,9 @@ extern "C" int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q
         if (s > kMaxSplits) s = kMaxSplits;
         p.num_kv_splits = s < 1 ? 1 : int(s);
         // Few waves of long items, the last one not half full: it is split.
-        // (80 heads, 512 rows over 8,000 keys, 160 items: 222 -> 155 us; 90 heads
-        // over 3,000 keys 92 -> 76 us. Where shorter items fill the wave anyway
-        // it costs up to 5%, 92.7 -> 98 us for 160 items of 700 and 300 rows.)
+        // (80 heads, 512 rows over 8,000 keys, 160 items: 224 -> 150 us; 90 heads
+        // over 3,000 keys 92 -> 73 us. Where shorter items fill the wave anyway
+        // it costs up to 5%, 101.7 -> 104.9 us for 160 items of 700 and 300 rows.)
         const int64_t rest = items % slots;
         if (!p.single_rows && items > slots && items < slots * kRestWaves &&
             most >= kRestSplits && rest > 0 && rest * 2 <= slots) {
@@ -1175,10 +1226,12 @@ extern "C" int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const 
         return MLA_ERR_INVALID_ARG;
     mla_prefill_plan_t check = *plan;
     layout(&check);
-    if (check.partial_offset != plan->partial_offset ||
-        check.lse_partial_offset != plan->lse_partial_offset ||
-        check.workspace_bytes != plan->workspace_bytes)
-        return MLA_ERR_INVALID_ARG;
+    const bool as_planned = same_layout(*plan, check);
+    if (!as_planned) {               // split_rest may have been changed since
+        check.split_rest = 1 - plan->split_rest;
+        layout(&check);
+        if (!same_layout(*plan, check)) return MLA_ERR_INVALID_ARG;
+    }
     const float scale_log2 = softmax_scale * 1.4426950408889634f;
     if (!(scale_log2 > 0.f) || !std::isfinite(scale_log2)) return MLA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < plan->workspace_bytes || !aligned(workspace, 256))
@@ -1201,13 +1254,19 @@ extern "C" int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const 
     p.total_q = plan->total_q;
     p.total_k = total_k;
     p.causal = causal ? 1 : 0;
-    p.splits = plan->num_kv_splits;
-    p.split_rest = plan->num_kv_splits > 1 ? plan->split_rest : 0;
+    // (split_rest cleared: there is room for the last wave's parts only, so no
+    // keys are cut)
+    p.splits = as_planned || plan->split_rest ? plan->num_kv_splits : 1;
+    p.split_rest = p.splits > 1 ? plan->split_rest : 0;
+    const Partials parts = partials(*plan, p.split_rest != 0);
     p.scale_log2 = scale_log2;
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
-    p.o_part = reinterpret_cast<float*>(ws + plan->partial_offset);
-    p.lse_part = reinterpret_cast<float*>(ws + plan->lse_partial_offset);
+    p.o_part = reinterpret_cast<float*>(ws + parts.rows);
+    p.lse_part = reinterpret_cast<float*>(ws + parts.lse);
+    p.rest_rows = reinterpret_cast<int64_t*>(ws + parts.rest_rows);
+    p.rest = reinterpret_cast<int32_t*>(ws + 4 * kRestWord);
+    p.rest_parts = int(parts.rest_parts);
     p.status = reinterpret_cast<int32_t*>(ws);
     p.ticket = reinterpret_cast<unsigned long long*>(ws + 4 * kTicketWord);
     p.done = reinterpret_cast<uint32_t*>(ws + 4 * kDoneCtasWord);
@@ -1216,8 +1275,12 @@ extern "C" int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const 
                                     : launch_prefill_tiles(p, plan->num_sms, st);
     if (e != 0) return MLA_ERR_CUDA;
     if (p.splits > 1 && !plan->single_rows) {
-        const int64_t rows = int64_t(p.total_q) * p.heads;
-        prefill_merge_kernel<<<unsigned((rows + 7) / 8), 256, 0, st>>>(p);
+        // (an item that is split has two parts or more)
+        const int64_t rows = p.split_rest ? int64_t(p.rest_parts / 2) * kItemRows
+                                          : int64_t(p.total_q) * p.heads;
+        if (rows == 0) return MLA_OK;     // (one part in all: nothing can be split)
+        (p.split_rest ? prefill_merge_rest_kernel
+                      : prefill_merge_kernel)<<<unsigned((rows + 7) / 8), 256, 0, st>>>(p);
         if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
     }
     return MLA_OK;

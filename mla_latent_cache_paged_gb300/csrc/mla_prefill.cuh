@@ -26,8 +26,13 @@ struct PrefillParams {
     float scale_log2;
     uint16_t* out;            // bf16 [total_q, N, 128]
     float* lse;               // fp32 [total_q, N] or null
-    float* o_part;            // splits > 1: fp32 [total_q, N, S, 128]
-    float* lse_part;          //             fp32 [total_q, N, S]
+    float* o_part;            // splits > 1: fp32 rows of 128, [total_q, N, S] of them or
+                              // (split_rest) [rest_parts, 256]
+    float* lse_part;          //             the rows' LSEs, fp32
+    int64_t* rest_rows;       // split_rest: their result rows (query * N + head), or -1
+    int32_t* rest;            // split_rest: those items, and the parts of each (in the status
+                              // header)
+    int rest_parts;
     int32_t* status;
     unsigned long long* ticket;   // items drawn after the first of each CTA (in the status
                                   // header; 0 between calls)
