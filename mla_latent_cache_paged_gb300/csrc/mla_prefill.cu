@@ -819,13 +819,16 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
 #pragma unroll
                 for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], v[124 + i]);
                 const float m_new = fmaxf(fmaxf(m, ptx::fmax3(m4[0], m4[1], m4[2])), m4[3]);
+                // (what a row does follows from its own scores alone, so that its
+                // result does not depend on the other rows of the warp)
+                const bool grown = (m_new - m) * p.scale_log2 > kRescaleThreshold;
                 if (j == it.step_lo) {
                     m = m_new;
-                } else if (__any_sync(0xffffffffu,
-                                      (m_new - m) * p.scale_log2 > kRescaleThreshold)) {
+                } else if (__any_sync(0xffffffffu, grown)) {
                     // (m = -inf: no key seen so far, O and the sum are 0)
-                    const float alpha = m == -INFINITY ? 1.f : ptx::ex2((m - m_new) * p.scale_log2);
-                    m = m_new;
+                    const float alpha =
+                        grown && m != -INFINITY ? ptx::ex2((m - m_new) * p.scale_log2) : 1.f;
+                    if (grown) m = m_new;
                     sum *= alpha;
                     ok = __all_sync(0xffffffffu, wait(MLA_BAR(pv_done) + 8 * t, s_uses & 1, bars,
                                                       p.status, kSitePv));
@@ -846,8 +849,9 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                 // count (2^-14 at 1024; an overflow at 2^31) m is taken off
                 // the scores first (rare, so it is a small loop as well).
                 float shift = m == -INFINITY ? 0.f : -m * p.scale_log2;
-                if (__any_sync(0xffffffffu, fabsf(shift) > 1024.f)) {
-                    const float base = m == -INFINITY ? 0.f : m;
+                const bool far = fabsf(shift) > 1024.f;
+                if (__any_sync(0xffffffffu, far)) {
+                    const float base = far ? m : 0.f;
 #pragma unroll 1
                     for (int c = 0; c < kStep; c += 32) {
                         uint32_t x[32];
@@ -858,7 +862,7 @@ mla_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap ma
                         ptx::tmem_st32(ts + c, x);
                     }
                     tmem_ld128(ts, v);
-                    shift = 0.f;
+                    if (far) shift = 0.f;
                 }
                 const uint64_t scale2 = pack_f32(p.scale_log2, p.scale_log2);
                 const uint64_t shift2 = pack_f32(shift, shift);
