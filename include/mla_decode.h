@@ -641,9 +641,13 @@ int mla_prefill(const mla_prefill_plan_t* plan, const void* q, const void* kv, c
  *   ref_counts_out      after: the same array (in place) or disjoint ones.
  *   block_table         device, int32 [rows, max_blocks_per_seq].
  *   workspace           device, 256-byte aligned, initialised once with
- *                       mla_workspace_init; >= mla_cache_workspace_bytes
- *                       bytes (mla_cache_free: a status header of 8192 bytes
- *                       is enough). Calls that share one must not overlap.
+ *                       mla_workspace_init, and again after a call that
+ *                       reported MLA_ERR_TIMEOUT (its outputs are not
+ *                       results; until then calls report it at once, with
+ *                       counts and tables changed in place as they were); >=
+ *                       mla_cache_workspace_bytes bytes (mla_cache_free: a
+ *                       status header of 8192 bytes is enough). Calls that
+ *                       share one must not overlap.
  * Device-detected errors go to its status word (mla_read_error). Each call is
  * one cooperative launch on `stream`, no synchronisation, and can be captured.
  *

@@ -44,8 +44,12 @@ constexpr int32_t kSiteGrid = 90;
 
 // Barriers of a cooperative grid on a word that is 0 between calls;
 // arrive_last ends a CTA's part, and the last one of the grid clears the word.
-// (After an expired wait the word stays as it is, as the workspace's other
-// counters do: the workspace is initialised again.)
+// A wait that expires marks the word, if the arrivals are still short then: so
+// either every CTA passes a barrier or none does, and the calls that find the
+// mark (until the workspace is initialised again) stop at their first barrier,
+// before they rely on what an abandoned call left in the workspace.
+constexpr uint32_t kAbandoned = 0x80000000u;
+
 struct GridBarrier {
     uint32_t* word;
     int32_t* status;
@@ -59,8 +63,12 @@ struct GridBarrier {
             *ok = 1;
             atomicAdd(word, 1u);
             const uint64_t t0 = ptx::globaltimer();
-            while (arrivals() < passed * gridDim.x) {
-                if (ptx::globaltimer() - t0 > kBarrierTimeoutNs) {
+            while (true) {
+                const uint32_t v = arrivals();
+                if (v < kAbandoned && v >= passed * gridDim.x) break;
+                if (v >= kAbandoned ||
+                    (ptx::globaltimer() - t0 > kBarrierTimeoutNs &&
+                     atomicCAS(word, v, v | kAbandoned) == v)) {
                     record_error(status, MLA_ERR_TIMEOUT, kSiteGrid);
                     *ok = 0;
                     break;
