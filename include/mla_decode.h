@@ -512,7 +512,7 @@ int mla_decode_v_up_proj(const mla_decode_plan_t* plan, const void* q, const voi
  *   total_k        rows of kv and k_pe; work is sized by it, so it should be
  *                  cu_seqlens_k[batch] or little more. (If it is less, the rows
  *                  that there is room for are written, and MLA_ERR_BAD_SEQ_LEN
- *                  is recorded.)
+ *                  is recorded; with 0 nothing is looked at.)
  *   w_uk_t, w_uv   device, bf16 [N, 128, 512] and [N, 512, 128], 16-byte
  *                  aligned: the weights of mla_q_absorb_concat_cache and
  *                  mla_v_up_proj.
@@ -585,9 +585,10 @@ typedef struct mla_prefill_plan {
  *                      (they steer the kernel and S alone: longer sequences are
  *                      computed too, more slowly).
  *   num_kv_splits      S in 1..64, or 0: the planner splits the keys when the
- *                      query rows alone leave SMs idle, all of them or
- *                      (split_rest) those of the last rows to be worked on.
- *                      (With single_rows it becomes 1, 2, 4 or 8.)
+ *                      query rows alone occupy half of the SMs or fewer, or
+ *                      (split_rest) those of the last rows to be worked on
+ *                      when these do. (With single_rows it becomes 1, 2, 4 or
+ *                      8.)
  *   num_sms            SMs of the target device, >= 1.
  */
 int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q_len, int max_k_len,

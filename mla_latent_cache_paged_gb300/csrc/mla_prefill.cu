@@ -27,12 +27,14 @@
 // clocks of exponentials (32,768 of them) and 80 KB of loads (32 bytes per
 // clock per SM, from L2: the items of a group of heads run together, so that
 // their keys and values stay there).
-// Measured, 4,096 causal tokens x 128 heads (361 us at cuBLAS's rate): 457-469
-// us; 405 us with the softmax left out, 379 us with the key and value loads
-// left out too: the score MMAs take both operands from shared memory, 128 bytes
+// Measured, 4,096 causal tokens x 128 heads (344 us at cuBLAS's burst rate, 394
+// at its rate under the power cap): 442-462 us replayed, 520 in calls back to
+// back under the power cap. Copies of the kernel for timing took 405 us with the
+// softmax left out and 379 us with the key and value loads left out too (468 as
+// it was then): the score MMAs take both operands from shared memory, 128 bytes
 // a clock, which is its rate, and the loads write there as well. 24 prompts of
-// 2 to 886 tokens x 16 heads 67.5 us; four chunks of ~480 rows over 3,589 to
-// 5,711 keys x 32 heads 146 us.
+// 2 to 886 tokens x 16 heads 64-65 us; four chunks of ~480 rows over 3,589 to
+// 5,711 keys x 32 heads 141-147 us.
 //
 // Keys and values of a 128-key step that lie past the sequence's end belong to
 // the next sequence, and those past a row's causal limit are its own future:
@@ -111,7 +113,7 @@ struct Bars {
     uint64_t k_empty[2], v_empty[2];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];       // scores of the step complete
-    uint64_t p_ready[2];      // 128 arrivals: weights in TMEM, O rescaled
+    uint64_t p_ready[2];      // 4 arrivals, one per softmax warp: weights in TMEM, O rescaled
     uint64_t pv_done[2];      // P.V of the step complete
     // A step whose values the helper works on: its V blocks land here, and the
     // helper completes v_full.
@@ -1172,10 +1174,11 @@ extern "C" int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q
     p.total_q = total_q;
     p.num_sms = num_sms;
     p.num_kv_splits = num_kv_splits;
-    // One query row a sequence: HBM is the bound. (Measured, tensor kernel
-    // against single-row kernel: 8 sequences of 816 keys, 16 heads, one row
-    // each 21.6 and 9.8 us, two rows each 21.6 and 24.7 us; 64 sequences of
-    // 2,048 keys, one row 202 and 175 us.)
+    // One query row a sequence: HBM is the bound. (Measured with the keys in
+    // HBM, tensor kernel against single-row kernel: 8 sequences of 816 keys, 16
+    // heads, one row each 21.5 and 14.2 us, two 21.8 and 21.2, three 20.4 and
+    // 28.9; 64 of 2,048 keys, 16 heads, one row 203 and 166 us, two 205 and 246;
+    // 4 of 2,048 keys, 128 heads, one row 106 and 83 us, two 106 and 125.)
     p.single_rows = max_q_len <= 1 ? 1 : 0;
     if (num_kv_splits == 0) {
         const int rows = p.single_rows ? 1 : kItemRows;
@@ -1184,8 +1187,11 @@ extern "C" int mla_prefill_plan(int batch, int num_heads, int total_q, int max_q
         const int64_t bound = int64_t(total_q) / rows + batch;
         if (tiles > bound) tiles = bound;
         const int64_t items = tiles * num_heads;
-        // Split while the items leave room: of the tensor kernel's one CTA
-        // per SM, of the other's kRowCtasPerSm.
+        // Split while every item finds room for S parts: of the tensor
+        // kernel's one CTA per SM, of the other's kRowCtasPerSm. (So items for
+        // more than half of the SMs are not split, and the other SMs are idle:
+        // 1,280 rows over 30,000 keys, 16 heads, 80 items, 404 us, where a
+        // caller's S = 3, in one and a half waves, takes 288.)
         const int64_t slots = p.single_rows ? int64_t(num_sms) * kRowCtasPerSm : num_sms;
         const int64_t most =
             p.single_rows ? max_k_len / kMinSplitKeys : max_k_len / (kStep * kMinSplitSteps);
