@@ -49,7 +49,7 @@
 extern "C" {
 #endif
 
-#define MLA_DECODE_ABI_VERSION 6
+#define MLA_DECODE_ABI_VERSION 7
 
 /* Status codes. */
 #define MLA_OK                 0
@@ -64,7 +64,7 @@ extern "C" {
 #define MLA_ERR_RANGE         -9  /* device: mla_decode_fp8 saw a q entry beyond +-65504 */
 #define MLA_ERR_NO_PAGES     -10  /* device: mla_cache_fork needs more free pages than there are */
 #define MLA_ERR_PAGE_STATE   -11  /* device: a page whose count does not allow the operation */
-#define MLA_ERR_BAD_ROW      -12  /* device: a row index outside the block table */
+#define MLA_ERR_BAD_ROW      -12  /* device: a row index outside the block table or the batch */
 
 /* Kernel variants the planner can choose (mla_decode_plan_t.kernel). */
 #define MLA_KERNEL_SIMT   1  /* CUDA-core split kernel, any 1 <= N <= 128 */
@@ -729,6 +729,155 @@ int mla_cache_compact(void* latent_cache, int num_layers, int64_t layer_stride_b
                       int32_t* block_table_out, int rows, int max_blocks_per_seq,
                       const int32_t* seq_lens, int32_t* page_map, int32_t* num_live,
                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rows of the latent cache, written and read back.
+ *
+ * mla_cache_write -- the entries of new tokens:
+ *     latent_cache row slot_mapping[t] = [kv_c[t, 0:512] | k_pe[t, 0:64]]
+ * (what mla_q_absorb_concat_cache inserts, for any number of tokens and
+ * without the query's side), and mla_cache_write_fp8, which quantises them
+ * into the cache that mla_decode_fp8, mla_expand_kv_fp8 and
+ * mla_cache_gather_fp8 read: the code is the E4M3 number nearest to
+ * x / k_scale (the exact quotient, rounded once, to the even code halfway),
+ * +-448 beyond that and for infinities; a NaN gives the NaN code 0x7F.
+ *
+ *   kv_c, k_pe     device, bf16, 512 and 64 columns, rows kv_c_stride and
+ *                  k_pe_stride elements apart (multiples of 8, so that both
+ *                  may be parts of one projection's rows), 16-byte aligned.
+ *   slot_mapping   device, int64 [num_tokens]: row slot % 64 of block
+ *                  slot / 64; a negative slot writes nothing (padding); a
+ *                  slot >= num_blocks * 64 is recorded as
+ *                  MLA_ERR_BAD_BLOCK_ID (detail: slot / 64) and not written.
+ *                  Non-negative slots must be distinct.
+ *   k_scale        finite, > 0.
+ *   latent_cache   device, bf16 [num_blocks, 64, 576], or E4M3 codes, 16-byte
+ *                  aligned.
+ *   workspace      a status header (>= 8192 bytes, 256-byte aligned).
+ * One launch on `stream`, no synchronisation.
+ */
+int mla_cache_write(const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
+                    const int64_t* slot_mapping, int num_tokens, void* latent_cache,
+                    int64_t num_blocks, void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_write_fp8(const void* kv_c, int64_t kv_c_stride, const void* k_pe,
+                        int64_t k_pe_stride, const int64_t* slot_mapping, int num_tokens,
+                        float k_scale, void* latent_cache_fp8, int64_t num_blocks, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * mla_cache_gather -- cached rows, read through the block table, side by side:
+ * packed row t of request b, t in [cu_seqlens_k[b], cu_seqlens_k[b + 1]), is
+ * the entry of its token first_token[b] + t - cu_seqlens_k[b] (the gather of
+ * vLLM's mla_attention API docs, _compute_prefill_context).
+ * mla_cache_gather_fp8 gives k_scale times the codes' values, rounded once to
+ * bf16 (nearest even).
+ *
+ *   rows           device, bf16 [total_k, 576], 16-byte aligned, written. Rows
+ *                  at cu_seqlens_k[batch] and after are left as they were.
+ *   the others     as for mla_expand_kv; the cache 16-byte aligned.
+ * A token past the block table (MLA_ERR_BAD_SEQ_LEN) or on a page outside the
+ * cache (MLA_ERR_BAD_BLOCK_ID) is recorded and its row is zeros. One launch on
+ * `stream`, no synchronisation.
+ */
+int mla_cache_gather(const void* latent_cache, int64_t num_blocks, const int32_t* block_table,
+                     int max_blocks_per_seq, const int32_t* first_token,
+                     const int32_t* cu_seqlens_k, int batch, int total_k, void* rows,
+                     void* workspace, size_t workspace_bytes, void* stream);
+int mla_cache_gather_fp8(const void* latent_cache_fp8, float k_scale, int64_t num_blocks,
+                         const int32_t* block_table, int max_blocks_per_seq,
+                         const int32_t* first_token, const int32_t* cu_seqlens_k, int batch,
+                         int total_k, void* rows, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * Decode over parts of the cached tokens: prefixes that several requests share,
+ * or a window with sinks. The arithmetic and the arguments are those of
+ * mla_decode and mla_decode_fp8 (softmax weights rounded to bf16, or to f16
+ * with an fp8 cache, for the tensor cores; an fp8 cache's q within +-65504).
+ *
+ * A plan is plain data computed on the host from sizes alone; the lengths and
+ * groups are read on the device, so a captured call can be replayed with
+ * others.
+ */
+typedef struct mla_span_plan {
+    int32_t  batch;               /* B, <= 8192 */
+    int32_t  num_heads;           /* N */
+    int32_t  max_blocks_per_seq;
+    int32_t  max_groups;          /* most groups of mla_decode_shared, <= 8192; 0 for
+                                     mla_decode_window */
+    int32_t  num_sms;
+    int32_t  pairs;               /* CTA pairs that the work is cut over */
+    uint32_t flags;
+    uint32_t reserved0;
+    uint64_t workspace_bytes;
+    uint32_t reserved[6];
+} mla_span_plan_t;
+
+/*
+ * mla_span_plan -- size the workspace. Host only. flags: 0 (or
+ * MLA_PLAN_DEBUG_WITHHOLD_LOAD, tests only: the first CTA withholds a load, so
+ * that a wait for it runs out after 2 ms).
+ */
+int mla_span_plan(int batch, int num_heads, int max_blocks_per_seq, int max_groups, int num_sms,
+                  uint32_t flags, mla_span_plan_t* plan);
+
+/*
+ * mla_decode_shared -- mla_decode of a batch in which neighbouring requests
+ * share a prefix (pages that mla_cache_fork shares): the prefix is attended to
+ * once for all rows of a group, 128 at a time, the rest request by request,
+ * and the parts are merged (fp32). Requests group_starts[g] ..
+ * group_starts[g + 1] - 1 are group g; their first shared_lens[g] tokens are
+ * the same. Of these the whole pages are shared, read through the block-table
+ * row of the group's first request that has tokens, as far as its shortest
+ * request that has any reaches; all other tokens (the rest of the prefix,
+ * requests in no group) are read through each request's own row. out and lse
+ * are those of mla_decode, whatever the groups. A group whose rows would fill
+ * no fewer tiles together than one by one (128 heads, one member) is decoded
+ * request by request.
+ *
+ *   group_starts   device, int32 [num_groups + 1], not decreasing, within
+ *                  [0, B]; else MLA_ERR_BAD_ROW is recorded and nothing shared.
+ *   shared_lens    device, int32 [num_groups]; one that is negative or beyond
+ *                  the block table is recorded (MLA_ERR_BAD_SEQ_LEN) and taken
+ *                  as 0.
+ *   num_groups     0 .. plan->max_groups.
+ *   out            16-byte aligned; the other arguments as for mla_decode.
+ *   workspace      device, >= plan->workspace_bytes, 256-byte aligned,
+ *                  initialised once with mla_workspace_init; calls that share
+ *                  one must not overlap on the device.
+ * A bad page id is recorded (MLA_ERR_BAD_BLOCK_ID) and its rows read as zeros,
+ * a bad length is recorded and its request taken as empty. Results do not
+ * depend on timing. Three launches on `stream`, no synchronisation.
+ */
+int mla_decode_shared(const mla_span_plan_t* plan, const void* q, const void* latent_cache,
+                      int64_t num_blocks, const int32_t* block_table, const int32_t* seq_lens,
+                      const int32_t* group_starts, const int32_t* shared_lens, int num_groups,
+                      float softmax_scale, void* out, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream);
+int mla_decode_shared_fp8(const mla_span_plan_t* plan, const void* q, const void* latent_cache_fp8,
+                          int64_t num_blocks, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* group_starts, const int32_t* shared_lens, int num_groups,
+                          float softmax_scale, float k_scale, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mla_decode_window -- mla_decode in which request b, of L = seq_lens[b]
+ * tokens, sees token t if t >= L - window (its last `window` tokens, the newest
+ * among them) or t < sinks (the first tokens stay visible). Pages of which it
+ * sees nothing are not read, nor are their table entries, so they may have been
+ * given back.
+ *
+ *   window >= 1, sinks >= 0; the others and the errors as for
+ *   mla_decode_shared.
+ */
+int mla_decode_window(const mla_span_plan_t* plan, const void* q, const void* latent_cache,
+                      int64_t num_blocks, const int32_t* block_table, const int32_t* seq_lens,
+                      int window, int sinks, float softmax_scale, void* out, float* lse,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int mla_decode_window_fp8(const mla_span_plan_t* plan, const void* q, const void* latent_cache_fp8,
+                          int64_t num_blocks, const int32_t* block_table, const int32_t* seq_lens,
+                          int window, int sinks, float softmax_scale, float k_scale, void* out,
+                          float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * mla_read_error -- synchronise `stream`, then read and clear the device

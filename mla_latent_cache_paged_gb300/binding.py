@@ -50,6 +50,9 @@ EXPORTED_SYMBOLS = (
     "mla_decode_fp8", "mla_merge_splits_v_up_proj", "mla_decode_v_up_proj",
     "mla_expand_kv", "mla_expand_kv_fp8", "mla_cache_workspace_bytes", "mla_cache_fork",
     "mla_cache_free", "mla_cache_compact", "mla_prefill_plan", "mla_prefill",
+    "mla_cache_write", "mla_cache_write_fp8", "mla_cache_gather", "mla_cache_gather_fp8",
+    "mla_span_plan", "mla_decode_shared", "mla_decode_shared_fp8", "mla_decode_window",
+    "mla_decode_window_fp8",
 )
 
 
@@ -97,6 +100,21 @@ class MlaPrefillPlan(ctypes.Structure):
         ("lse_partial_offset", ctypes.c_uint64),
         ("split_rest", ctypes.c_int32),
         ("reserved", ctypes.c_uint32 * 5),
+    ]
+
+
+class MlaSpanPlan(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("max_groups", ctypes.c_int32),
+        ("num_sms", ctypes.c_int32),
+        ("pairs", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("reserved0", ctypes.c_uint32),
+        ("workspace_bytes", ctypes.c_uint64),
+        ("reserved", ctypes.c_uint32 * 6),
     ]
 
 
@@ -158,6 +176,17 @@ def load_library(path=None):
                                      ctypes.POINTER(MlaPrefillPlan)]
     lib.mla_prefill.argtypes = [ctypes.POINTER(MlaPrefillPlan), vp, vp, vp, i32, vp, vp, i32, f32,
                                 vp, vp, vp, sz, vp]
+    lib.mla_cache_write.argtypes = [vp, i64, vp, i64, vp, i32, vp, i64, vp, sz, vp]
+    lib.mla_cache_write_fp8.argtypes = [vp, i64, vp, i64, vp, i32, f32, vp, i64, vp, sz, vp]
+    lib.mla_cache_gather.argtypes = [vp, i64, vp, i32, vp, vp, i32, i32, vp, vp, sz, vp]
+    lib.mla_cache_gather_fp8.argtypes = [vp, f32, i64, vp, i32, vp, vp, i32, i32, vp, vp, sz, vp]
+    lib.mla_span_plan.argtypes = [i32, i32, i32, i32, i32, ctypes.c_uint32,
+                                  ctypes.POINTER(MlaSpanPlan)]
+    span = [ctypes.POINTER(MlaSpanPlan), vp, vp, i64, vp, vp]
+    lib.mla_decode_shared.argtypes = span + [vp, vp, i32, f32, vp, vp, vp, sz, vp]
+    lib.mla_decode_shared_fp8.argtypes = span + [vp, vp, i32, f32, f32, vp, vp, vp, sz, vp]
+    lib.mla_decode_window.argtypes = span + [i32, i32, f32, vp, vp, vp, sz, vp]
+    lib.mla_decode_window_fp8.argtypes = span + [i32, i32, f32, f32, vp, vp, vp, sz, vp]
     for name in EXPORTED_SYMBOLS:
         if name != "mla_status_string":
             getattr(lib, name).restype = ctypes.c_int
@@ -835,6 +864,212 @@ def mla_cache_compact(latent_cache, ref_counts, block_table, seq_lens, *, worksp
           _arg("seq_lens", seq_lens, i32, dev, (rows,)),
           map_ptr, live_ptr, _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
     return table, out, page_map, num_live
+
+
+def _rows(name, t, width, device):
+    """The address and the row stride of `t` bf16 [T, width], columns contiguous."""
+    import torch
+    if _device_of(name, t) != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
+        raise ValueError(f"{name} must be [T, {width}] with contiguous columns")
+    stride = t.stride(0) if t.shape[0] > 1 else width
+    if stride % 8:
+        raise ValueError(f"{name}'s rows must lie a multiple of 8 elements apart, not {stride}")
+    return t.data_ptr(), stride
+
+
+def _cache_write(fn, cache_dtype, kv_c, k_pe, slot_mapping, latent_cache, k_scale, workspace, stream):
+    import torch
+    dev = _device_of("latent_cache", latent_cache)
+    blocks = _ndim("latent_cache", latent_cache, 3, "[num_blocks, 64, 576]")[0]
+    T = _ndim("slot_mapping", slot_mapping, 1, "[T]")[0]
+    for name, t in (("kv_c", kv_c), ("k_pe", k_pe)):
+        if _ndim(name, t, 2, "of two dimensions")[0] != T:
+            raise ValueError(f"{name} must have a row for each of the {T} slots")
+    _call(dev, stream, fn, *_rows("kv_c", kv_c, KV_LORA_RANK, dev),
+          *_rows("k_pe", k_pe, ROPE_DIM, dev),
+          _arg("slot_mapping", slot_mapping, torch.int64, dev), T,
+          *(() if k_scale is None else (float(k_scale),)),
+          _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM)),
+          blocks, _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
+    return latent_cache
+
+
+def mla_cache_write(kv_c, k_pe, slot_mapping, latent_cache, *, workspace, stream=None):
+    """New tokens' entries ``[kv_c | k_pe]`` (bf16 ``[T, 512]`` and ``[T, 64]``,
+    their rows any multiple of 8 elements apart) into the rows ``slot_mapping``
+    (int64 ``[T]``; negative: none) of ``latent_cache``, which is returned."""
+    import torch
+    return _cache_write(load_library().mla_cache_write, torch.bfloat16, kv_c, k_pe, slot_mapping,
+                        latent_cache, None, workspace, stream)
+
+
+def mla_cache_write_fp8(kv_c, k_pe, slot_mapping, latent_cache_fp8, k_scale, *, workspace,
+                        stream=None):
+    """``mla_cache_write`` into an fp8 cache: the E4M3 codes (uint8) nearest to
+    the entries divided by ``k_scale``, saturating at +-448."""
+    import torch
+    return _cache_write(load_library().mla_cache_write_fp8, torch.uint8, kv_c, k_pe, slot_mapping,
+                        latent_cache_fp8, k_scale, workspace, stream)
+
+
+def _cache_gather(fn, cache_dtype, latent_cache, block_table, cu_seqlens_k, k_scale, total_k,
+                  first_token, rows, workspace, stream):
+    import torch
+    i32 = torch.int32
+    dev = _device_of("latent_cache", latent_cache)
+    blocks = _ndim("latent_cache", latent_cache, 3, "[num_blocks, 64, 576]")[0]
+    B = _ndim("cu_seqlens_k", cu_seqlens_k, 1, "[B + 1]")[0] - 1
+    _, mb = _ndim("block_table", block_table, 2, "[B, max_blocks_per_seq]")
+    T = int(total_k)
+    if B < 0:
+        raise ValueError("cu_seqlens_k must be [B + 1]")
+    if T < 0:
+        raise ValueError("total_k must not be negative")
+    rows, rows_ptr = _result("rows", rows, (T, HEAD_DIM), torch.bfloat16, dev, stream)
+    _call(dev, stream, fn,
+          _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM)),
+          *(() if k_scale is None else (float(k_scale),)), blocks,
+          _arg("block_table", block_table, i32, dev, (B, mb)), mb,
+          None if first_token is None else _arg("first_token", first_token, i32, dev, (B,)),
+          _arg("cu_seqlens_k", cu_seqlens_k, i32, dev), B, T, rows_ptr,
+          _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
+    return rows
+
+
+def mla_cache_gather(latent_cache, block_table, cu_seqlens_k, *, total_k, workspace,
+                     first_token=None, rows=None, stream=None):
+    """Cached entries side by side: packed row t of request b is its token
+    ``first_token[b] + t - cu_seqlens_k[b]``. Returns ``rows`` bf16 ``[total_k,
+    576]``; rows from ``cu_seqlens_k[B]`` on are not written."""
+    import torch
+    return _cache_gather(load_library().mla_cache_gather, torch.bfloat16, latent_cache, block_table,
+                         cu_seqlens_k, None, total_k, first_token, rows, workspace, stream)
+
+
+def mla_cache_gather_fp8(latent_cache_fp8, block_table, cu_seqlens_k, k_scale, *, total_k,
+                         workspace, first_token=None, rows=None, stream=None):
+    """``mla_cache_gather`` over an fp8 cache (uint8 E4M3 codes, per-tensor ``k_scale``)."""
+    import torch
+    return _cache_gather(load_library().mla_cache_gather_fp8, torch.uint8, latent_cache_fp8,
+                         block_table, cu_seqlens_k, k_scale, total_k, first_token, rows, workspace,
+                         stream)
+
+
+def make_span_plan(batch, num_heads, max_blocks_per_seq, *, max_groups=0, num_sms=None,
+                   extra_flags=0):
+    """Call mla_span_plan (host only; no device work): a plan for
+    ``mla_decode_shared`` of up to `max_groups` groups, or ``mla_decode_window``."""
+    if num_sms is None:
+        import torch
+        num_sms = (torch.cuda.get_device_properties(0).multi_processor_count
+                   if torch.cuda.is_available() else 152)
+    plan = MlaSpanPlan()
+    _check(load_library().mla_span_plan(int(batch), int(num_heads), int(max_blocks_per_seq),
+                                        int(max_groups), int(num_sms), int(extra_flags),
+                                        ctypes.byref(plan)), "mla_span_plan")
+    return plan
+
+
+def _decode_span(fn, cache_dtype, q, latent_cache, block_table, seq_lens, middle, groups, scales,
+                 plan, out, lse, return_lse, workspace, stream):
+    """One of the decodes over parts of the tokens; `middle(device, batch)`
+    gives the arguments between the lengths and the scales."""
+    import torch
+    i32 = torch.int32
+    dev = _device_of("q", q)
+    B, N, _ = _ndim("q", q, 3, "[B, N, 576]")
+    blocks = _ndim("latent_cache", latent_cache, 3, "[num_blocks, 64, 576]")[0]
+    _, mb = _ndim("block_table", block_table, 2, "[B, max_blocks_per_seq]")
+    if plan is None:
+        plan = make_span_plan(B, N, mb, max_groups=groups, num_sms=torch.cuda.get_device_properties(
+            dev).multi_processor_count)
+    elif plan.batch != B or plan.num_heads != N or plan.max_blocks_per_seq != mb:
+        raise ValueError(f"the plan is for (B, N, max_blocks_per_seq) = "
+                         f"{plan.batch, plan.num_heads, plan.max_blocks_per_seq}, not {B, N, mb}")
+    elif groups > plan.max_groups:
+        raise ValueError(f"the plan is for up to {plan.max_groups} groups, not {groups}")
+    args = (_arg("q", q, torch.bfloat16, dev, (B, N, HEAD_DIM)),
+            _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM)),
+            blocks, _arg("block_table", block_table, i32, dev, (B, mb)),
+            _arg("seq_lens", seq_lens, i32, dev, (B,)), *middle(dev))
+    out, out_ptr = _result("out", out, (B, N, KV_LORA_RANK), torch.bfloat16, dev, stream)
+    lse_ptr = None
+    if lse is not None or return_lse:
+        lse, lse_ptr = _result("lse", lse, (B, N), torch.float32, dev, stream)
+    if workspace is None:
+        workspace = _empty((int(plan.workspace_bytes),), torch.uint8, dev, stream)
+        _call(dev, stream, load_library().mla_workspace_init, workspace.data_ptr(),
+              workspace.numel())
+    _call(dev, stream, fn, ctypes.byref(plan), *args, *map(float, scales), out_ptr, lse_ptr,
+          _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
+    return out, lse
+
+
+def _groups(group_starts, shared_lens):
+    import torch
+    G = _ndim("shared_lens", shared_lens, 1, "[groups]")[0]
+    return G, lambda dev: (_arg("group_starts", group_starts, torch.int32, dev, (G + 1,)),
+                           _arg("shared_lens", shared_lens, torch.int32, dev), G)
+
+
+def mla_decode_shared(q, latent_cache, block_table, seq_lens, group_starts, shared_lens,
+                      softmax_scale, *, plan=None, out=None, lse=None, return_lse=True,
+                      workspace=None, stream=None):
+    """``mla_decode`` of a batch whose requests ``group_starts[g]`` ..
+    ``group_starts[g + 1] - 1`` (int32 ``[G + 1]``) share their first
+    ``shared_lens[g]`` tokens (int32 ``[G]``), whose whole pages are attended to
+    once for the group's rows together. Returns ``(out bf16 [B, N, 512], lse
+    fp32 [B, N] | None)``, as ``mla_decode`` would."""
+    import torch
+    G, middle = _groups(group_starts, shared_lens)
+    return _decode_span(load_library().mla_decode_shared, torch.bfloat16, q, latent_cache,
+                        block_table, seq_lens, middle, G, (softmax_scale,), plan, out, lse,
+                        return_lse, workspace, stream)
+
+
+def mla_decode_shared_fp8(q, latent_cache_fp8, block_table, seq_lens, group_starts, shared_lens,
+                          softmax_scale, k_scale, *, plan=None, out=None, lse=None,
+                          return_lse=True, workspace=None, stream=None):
+    """``mla_decode_shared`` over an fp8 cache (uint8 E4M3 codes, per-tensor ``k_scale``)."""
+    import torch
+    G, middle = _groups(group_starts, shared_lens)
+    return _decode_span(load_library().mla_decode_shared_fp8, torch.uint8, q, latent_cache_fp8,
+                        block_table, seq_lens, middle, G, (softmax_scale, k_scale), plan, out, lse,
+                        return_lse, workspace, stream)
+
+
+def _window(window, sinks):
+    """(a window or sinks past every length see what the longest lengths would)"""
+    most = 2 ** 31 - 1
+    window, sinks = min(int(window), most), min(int(sinks), most)
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1, sinks at least 0")
+    return lambda dev: (window, sinks)
+
+
+def mla_decode_window(q, latent_cache, block_table, seq_lens, softmax_scale, *, window, sinks=0,
+                      plan=None, out=None, lse=None, return_lse=True, workspace=None, stream=None):
+    """``mla_decode`` in which a request of L tokens sees its last ``window``
+    ones and its first ``sinks`` ones; pages in between are not read. Returns
+    ``(out bf16 [B, N, 512], lse fp32 [B, N] | None)``."""
+    import torch
+    return _decode_span(load_library().mla_decode_window, torch.bfloat16, q, latent_cache,
+                        block_table, seq_lens, _window(window, sinks), 0,
+                        (softmax_scale,), plan, out, lse, return_lse, workspace, stream)
+
+
+def mla_decode_window_fp8(q, latent_cache_fp8, block_table, seq_lens, softmax_scale, k_scale, *,
+                          window, sinks=0, plan=None, out=None, lse=None, return_lse=True,
+                          workspace=None, stream=None):
+    """``mla_decode_window`` over an fp8 cache (uint8 E4M3 codes, per-tensor ``k_scale``)."""
+    import torch
+    return _decode_span(load_library().mla_decode_window_fp8, torch.uint8, q, latent_cache_fp8,
+                        block_table, seq_lens, _window(window, sinks), 0,
+                        (softmax_scale, k_scale), plan, out, lse, return_lse, workspace, stream)
 
 
 def read_error(workspace, stream=None):

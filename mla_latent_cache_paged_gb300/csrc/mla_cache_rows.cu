@@ -1,0 +1,337 @@
+// Rows of the latent cache, written and read back (mla_cache_write,
+// mla_cache_gather and their fp8 forms, declared in include/mla_decode.h).
+//
+//   write:  entry slot_mapping[t] = [kv_c[t] | k_pe[t]], or its E4M3 codes
+//           e4m3(x / k_scale)
+//   gather: rows[t] = the entry of packed token t, or k_scale times its codes
+//
+// Both move a row as 72 pieces of 8 values, one per thread, so that a row's
+// loads and stores are whole lines, with several rows in flight per thread.
+// Bound by HBM; by launch and load latency for a decode step's few rows.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+
+#include "mla_device.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kPieces = kD / 8;              // of 8 values
+constexpr int kLatentPieces = kLkv / 8;
+constexpr int kRowsAtOnce = 4;
+constexpr int kThreads = kRowsAtOnce * kPieces;   // 288
+
+// ------------------------------------------------------------------ write
+
+struct WriteParams {
+    const uint16_t* kv_c;        // rows kv_stride apart
+    const uint16_t* k_pe;        // rows pe_stride apart
+    int64_t kv_stride, pe_stride;
+    const int64_t* slots;        // [T]
+    int tokens;
+    void* cache;
+    int64_t num_slots;
+    // fp8: k_scale = mantissa * 2^e, mantissa in [1, 2); x / k_scale =
+    // x * down0 * down1 / mantissa, the first two exact powers of two.
+    float down0, down1, mantissa, inverse;
+    int32_t* status;
+};
+
+// x / k_scale as an fp32 number that rounds to 8 bits as the exact quotient
+// does: the nearest fp32 number below or above it, the odd one of the two
+// where the quotient is not an fp32 number itself (rounding to odd loses
+// nothing for a later rounding to fewer bits).
+__device__ __forceinline__ float quotient(float x, const WriteParams& p) {
+    float a = fabsf(x) * p.down0 * p.down1;
+    a = a > 1024.f ? 1024.f : a;     // (the quotient is past 448 from there on; a NaN stays one)
+    const float q0 = a * p.inverse;
+    const float q = fmaf(fmaf(-q0, p.mantissa, a), p.inverse, q0);
+    const float rest = fmaf(-q, p.mantissa, a);
+    uint32_t bits = __float_as_uint(q);
+    // (next to zero, where a product may have lost bits, all round to zero)
+    if (rest != 0.f && (bits & 1u) == 0 && q >= 9.5367431640625e-7f)
+        bits = rest > 0.f ? bits + 1 : bits - 1;
+    return copysignf(__uint_as_float(bits), x);
+}
+
+// Two quotients as E4M3 codes: to nearest even, saturating at +-448.
+__device__ __forceinline__ uint32_t codes2(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+template <bool kFp8, int kRounds>
+__global__ void __launch_bounds__(kThreads) mla_cache_write_kernel(const WriteParams p) {
+    const int c = threadIdx.x % kPieces;
+    const int64_t t0 = int64_t(blockIdx.x) * (kRowsAtOnce * kRounds) + threadIdx.x / kPieces;
+    uint4 v[kRounds];
+    int64_t slot[kRounds];
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        const int64_t t = t0 + k * kRowsAtOnce;
+        slot[k] = -1;
+        if (t < p.tokens) {
+            slot[k] = p.slots[t];
+            const uint16_t* src = c < kLatentPieces
+                                      ? p.kv_c + t * p.kv_stride + 8 * c
+                                      : p.k_pe + t * p.pe_stride + 8 * (c - kLatentPieces);
+            v[k] = __ldg(reinterpret_cast<const uint4*>(src));
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        if (slot[k] < 0) continue;
+        if (slot[k] >= p.num_slots) {
+            if (c == 0) {
+                const int64_t page = slot[k] / kPageSize;
+                record_error(p.status, MLA_ERR_BAD_BLOCK_ID,
+                             int32_t(page < INT_MAX ? page : INT_MAX));
+            }
+            continue;
+        }
+        if constexpr (kFp8) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                h[i] = codes2(quotient(__uint_as_float(w[i] << 16), p),
+                              quotient(__uint_as_float(w[i] & 0xffff0000u), p));
+            *reinterpret_cast<uint2*>(static_cast<unsigned char*>(p.cache) + slot[k] * kD + 8 * c) =
+                make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.cache) + slot[k] * kD + 8 * c) =
+                v[k];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ gather
+
+struct GatherParams {
+    const void* cache;
+    int64_t num_blocks;
+    const int32_t* table;        // [B, max_blocks]
+    int max_blocks;
+    const int32_t* first;        // [B] or null
+    const int32_t* cu;           // [B + 1]
+    int batch, total;
+    float scale;
+    uint16_t* rows;              // bf16 [total, 576]
+    int32_t* status;
+};
+
+constexpr int64_t kNoRow = -2;   // the packed row belongs to no request
+constexpr int64_t kNoPage = -1;  // its page is not there: zeros
+
+// The cache slot of packed row t.
+__device__ __forceinline__ int64_t find_slot(const GatherParams& p, int t) {
+    // (the last row speaks for the sequences that the rows have no room for)
+    if (t == p.total - 1 && p.cu[p.batch] > p.total)
+        record_error(p.status, MLA_ERR_BAD_SEQ_LEN, p.cu[p.batch]);
+    int lo = 0, hi = p.batch;       // the last b with cu[b] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu[mid] <= t) lo = mid; else hi = mid;
+    }
+    const int begin = p.cu[lo], end = p.cu[lo + 1];
+    if (begin < 0 || t < begin || t >= end) return kNoRow;
+    const int64_t pos = int64_t(p.first != nullptr ? p.first[lo] : 0) + (t - begin);
+    if (pos < 0 || pos >= int64_t(p.max_blocks) * kPageSize) {
+        record_error(p.status, MLA_ERR_BAD_SEQ_LEN, int32_t(pos < INT_MAX ? pos : INT_MAX));
+        return kNoPage;
+    }
+    const int page = p.table[int64_t(lo) * p.max_blocks + pos / kPageSize];
+    if (page < 0 || int64_t(page) >= p.num_blocks) {
+        record_error(p.status, MLA_ERR_BAD_BLOCK_ID, page);
+        return kNoPage;
+    }
+    return int64_t(page) * kPageSize + pos % kPageSize;
+}
+
+// Two codes times the scale as bf16, one rounding.
+__device__ __forceinline__ uint32_t scaled2(uint32_t codes16, float scale) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(codes16), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    return pack_bf16(f.x * scale, f.y * scale);
+}
+
+template <bool kFp8, int kRounds>
+__global__ void __launch_bounds__(kThreads) mla_cache_gather_kernel(const GatherParams p) {
+    constexpr int kRows = kRowsAtOnce * kRounds;
+    __shared__ int64_t slots[kRows];
+    const int64_t t0 = int64_t(blockIdx.x) * kRows;
+    if (threadIdx.x < kRows) {
+        const int64_t t = t0 + threadIdx.x;
+        slots[threadIdx.x] = t < p.total ? find_slot(p, int(t)) : kNoRow;
+    }
+    __syncthreads();
+    const int c = threadIdx.x % kPieces, r = threadIdx.x / kPieces;
+    uint4 v[kRounds];
+    int64_t slot[kRounds];
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        slot[k] = slots[r + k * kRowsAtOnce];
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (slot[k] < 0) continue;
+        if constexpr (kFp8) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(
+                static_cast<const unsigned char*>(p.cache) + slot[k] * kD + 8 * c));
+            v[k].x = u.x;
+            v[k].y = u.y;
+        } else {
+            v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache) +
+                                                        slot[k] * kD + 8 * c));
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        if (slot[k] == kNoRow) continue;
+        if constexpr (kFp8)
+            v[k] = make_uint4(scaled2(v[k].x & 0xffffu, p.scale), scaled2(v[k].x >> 16, p.scale),
+                              scaled2(v[k].y & 0xffffu, p.scale), scaled2(v[k].y >> 16, p.scale));
+        *reinterpret_cast<uint4*>(p.rows + (t0 + r + k * kRowsAtOnce) * kD + 8 * c) = v[k];
+    }
+}
+
+// Rows per CTA: few while that makes no more CTAs than the GPU holds at once.
+constexpr int kFewRounds = 1, kManyRounds = 4;
+constexpr int kFewRows = 4096;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+template <bool kFp8>
+int write(WriteParams p, float k_scale, int64_t num_blocks, void* workspace,
+          size_t workspace_bytes, void* stream) {
+    if (p.tokens < 0 || num_blocks < 1 || p.kv_stride < 0 || p.pe_stride < 0 ||
+        p.kv_stride % 8 != 0 || p.pe_stride % 8 != 0)
+        return MLA_ERR_INVALID_ARG;
+    if (kFp8 && (!std::isfinite(k_scale) || !(k_scale > 0.f))) return MLA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kStatusBytes || !aligned(workspace, 256))
+        return MLA_ERR_WORKSPACE;
+    if (num_blocks > INT64_MAX / (kPageSize * kD * 2)) return MLA_ERR_UNSUPPORTED;
+    if (p.tokens == 0) return MLA_OK;
+    if (!p.kv_c || !p.k_pe || !p.slots || !p.cache) return MLA_ERR_INVALID_ARG;
+    if (!aligned(p.kv_c, 16) || !aligned(p.k_pe, 16) || !aligned(p.slots, 8) ||
+        !aligned(p.cache, 16))
+        return MLA_ERR_INVALID_ARG;
+    p.num_slots = num_blocks * kPageSize;
+    p.status = static_cast<int32_t*>(workspace);
+    if (kFp8) {
+        int e = 0;
+        p.mantissa = 2.f * std::frexp(k_scale, &e);      // k_scale = mantissa * 2^(e - 1)
+        p.inverse = 1.f / p.mantissa;
+        p.down0 = std::ldexp(1.f, (1 - e) / 2);
+        p.down1 = std::ldexp(1.f, (1 - e) - (1 - e) / 2);
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int rounds = p.tokens <= kFewRows ? kFewRounds : kManyRounds;
+    const int per_cta = kRowsAtOnce * rounds;
+    const unsigned grid = unsigned((int64_t(p.tokens) + per_cta - 1) / per_cta);
+    if (rounds == kFewRounds)
+        mla_cache_write_kernel<kFp8, kFewRounds><<<grid, kThreads, 0, st>>>(p);
+    else
+        mla_cache_write_kernel<kFp8, kManyRounds><<<grid, kThreads, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+template <bool kFp8>
+int gather(GatherParams p, void* workspace, size_t workspace_bytes, void* stream) {
+    if (p.batch < 0 || p.total < 0 || p.num_blocks < 1 || p.max_blocks < 1)
+        return MLA_ERR_INVALID_ARG;
+    if (kFp8 && (!std::isfinite(p.scale) || !(p.scale > 0.f))) return MLA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kStatusBytes || !aligned(workspace, 256))
+        return MLA_ERR_WORKSPACE;
+    if (p.batch == 0 || p.total == 0) return MLA_OK;
+    if (!p.cache || !p.table || !p.cu || !p.rows) return MLA_ERR_INVALID_ARG;
+    if (!aligned(p.cache, 16) || !aligned(p.rows, 16) || !aligned(p.table, 4) ||
+        !aligned(p.cu, 4) || (p.first && !aligned(p.first, 4)))
+        return MLA_ERR_INVALID_ARG;
+    p.status = static_cast<int32_t*>(workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int rounds = p.total <= kFewRows ? kFewRounds : kManyRounds;
+    const int per_cta = kRowsAtOnce * rounds;
+    const unsigned grid = unsigned((int64_t(p.total) + per_cta - 1) / per_cta);
+    if (rounds == kFewRounds)
+        mla_cache_gather_kernel<kFp8, kFewRounds><<<grid, kThreads, 0, st>>>(p);
+    else
+        mla_cache_gather_kernel<kFp8, kManyRounds><<<grid, kThreads, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+WriteParams write_params(const void* kv_c, int64_t kv_stride, const void* k_pe, int64_t pe_stride,
+                         const int64_t* slots, int tokens, void* cache) {
+    WriteParams p{};
+    p.kv_c = static_cast<const uint16_t*>(kv_c);
+    p.k_pe = static_cast<const uint16_t*>(k_pe);
+    p.kv_stride = kv_stride;
+    p.pe_stride = pe_stride;
+    p.slots = slots;
+    p.tokens = tokens;
+    p.cache = cache;
+    return p;
+}
+
+GatherParams gather_params(const void* cache, float scale, int64_t num_blocks,
+                           const int32_t* table, int max_blocks, const int32_t* first,
+                           const int32_t* cu, int batch, int total, void* rows) {
+    GatherParams p{};
+    p.cache = cache;
+    p.scale = scale;
+    p.num_blocks = num_blocks;
+    p.table = table;
+    p.max_blocks = max_blocks;
+    p.first = first;
+    p.cu = cu;
+    p.batch = batch;
+    p.total = total;
+    p.rows = static_cast<uint16_t*>(rows);
+    return p;
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" int mla_cache_write(const void* kv_c, int64_t kv_c_stride, const void* k_pe,
+                               int64_t k_pe_stride, const int64_t* slot_mapping, int num_tokens,
+                               void* latent_cache, int64_t num_blocks, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    return write<false>(write_params(kv_c, kv_c_stride, k_pe, k_pe_stride, slot_mapping, num_tokens,
+                                     latent_cache), 1.f, num_blocks, workspace, workspace_bytes,
+                        stream);
+}
+
+extern "C" int mla_cache_write_fp8(const void* kv_c, int64_t kv_c_stride, const void* k_pe,
+                                   int64_t k_pe_stride, const int64_t* slot_mapping,
+                                   int num_tokens, float k_scale, void* latent_cache_fp8,
+                                   int64_t num_blocks, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    return write<true>(write_params(kv_c, kv_c_stride, k_pe, k_pe_stride, slot_mapping, num_tokens,
+                                    latent_cache_fp8), k_scale, num_blocks, workspace,
+                       workspace_bytes, stream);
+}
+
+extern "C" int mla_cache_gather(const void* latent_cache, int64_t num_blocks,
+                                const int32_t* block_table, int max_blocks_per_seq,
+                                const int32_t* first_token, const int32_t* cu_seqlens_k, int batch,
+                                int total_k, void* rows, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    return gather<false>(gather_params(latent_cache, 1.f, num_blocks, block_table,
+                                       max_blocks_per_seq, first_token, cu_seqlens_k, batch,
+                                       total_k, rows), workspace, workspace_bytes, stream);
+}
+
+extern "C" int mla_cache_gather_fp8(const void* latent_cache_fp8, float k_scale,
+                                    int64_t num_blocks, const int32_t* block_table,
+                                    int max_blocks_per_seq, const int32_t* first_token,
+                                    const int32_t* cu_seqlens_k, int batch, int total_k,
+                                    void* rows, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+    return gather<true>(gather_params(latent_cache_fp8, k_scale, num_blocks, block_table,
+                                      max_blocks_per_seq, first_token, cu_seqlens_k, batch,
+                                      total_k, rows), workspace, workspace_bytes, stream);
+}

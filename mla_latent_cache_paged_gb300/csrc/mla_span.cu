@@ -1,0 +1,912 @@
+// Attention of the items of mla_decode_shared and mla_decode_window
+// (mla_span.cuh): rows of absorbed queries over the pages of a latent cache.
+//
+//   s[t] = softmax_scale q . K[t], out = sum_t exp(s[t] - lse) V[t],
+//   K[t] the 576-wide entry, V[t] its first 512 columns.
+//
+// 128 rows against a page pair are 2 * 128 * 128 * (576 + 512) flops for 147 KB
+// of cache: the tensor pipe and HBM take about the same time, and a prefix
+// that many tiles share is in L2, so the tensor pipe is the bound. 128 rows
+// of 512 fp32 results are all of one SM's TMEM. So a pair of CTAs works on an
+// item with cta_group::2 MMAs of M = 128: each CTA holds 64 of the rows, and
+// TMEM lanes 0..63 and 64..127 of a CTA hold those rows' first and second half
+// of an MMA's columns. Nothing is computed twice:
+//   * Scores: N = 128, the two pages of a step, one from each CTA's shared
+//     memory; lanes 64 f + r get row r's scores of page f. Two buffers.
+//   * P V: K = 128 tokens; CTA f holds value columns 256 f .. 256 f + 255 of
+//     both pages, so lanes 64 f + r get those columns of row r (256 TMEM
+//     columns).
+// A CTA's own page arrives whole (nine 64-column blocks). Of its blocks the
+// four of the other CTA's value columns are done with after the scores, and
+// the other page's blocks of its own value columns take their slots: slots
+// 0..3 hold the first page's values in both CTAs then, slots 4..7 the second
+// page's, at the same addresses in both, as the MMAs need it. Two such stages
+// of eight slots, one slot for the RoPE block, the queries (72 KB) and the
+// weights (16 KB) fill an SM. Each pair of slots is loaded again as soon as
+// the P V MMAs that read it are done.
+//
+// Softmax: a thread has 64 scores of a row; the two threads of a row exchange
+// their maxima through shared memory. fp32, base 2; the reference maximum moves
+// only when a step raises it by more than 8, so that results are seldom
+// rescaled. Weights are rounded to bf16 (f16 with an fp8 cache: half a step,
+// 2^-8 or 2^-11, of each weight) for the tensor cores; results are normalised
+// by the sum of the rounded weights, the LSE keeps the sum of the others.
+//
+// An fp8 cache: codes land in the upper half of the slots that their f16 copies
+// fill, and four warps widen them in place (exact).
+//
+// Warps: 0 = loads, 1 = MMAs (first CTA), 2-5 = softmax and epilogue, 6-9 = fp8
+// widening. Every wait is bounded (MLA_ERR_TIMEOUT).
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cfloat>
+#include <climits>
+#include <cmath>
+#include <cstddef>
+
+#include "mla_span.cuh"
+#include "tc_ptx.cuh"
+#include "tensor_map.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kThreadsFp8 = 320;
+constexpr int kCtaRows = 64;
+constexpr int kBlock = 64 * 128;                  // 64 rows x 64 16-bit columns
+constexpr int kStages = 2;
+constexpr int kSlots = 8;
+constexpr int kStageBytes = kSlots * kBlock;
+constexpr int kOffQ = 0;                          // 9 blocks
+constexpr int kOffStage = 9 * kBlock;
+constexpr int kOffRope = kOffStage + kStages * kStageBytes;
+constexpr int kOffP = kOffRope + kBlock;          // a block per page of the step
+constexpr int kOffBar = kOffP + 2 * kBlock;       // 229,376
+constexpr int kOffSwap = kOffBar + 512;           // 2 x 128 floats that rows' halves exchange
+constexpr int kSmemBytes = kOffSwap + 2 * 128 * 4;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemS = 0;                    // 2 x 64 columns
+constexpr uint32_t kTmemO = 128;                  // 256 columns
+
+constexpr uint32_t kSuspendNs = 20000;
+constexpr uint16_t kBoth = 3;                     // the pair's CTAs
+constexpr float kRescaleThreshold = 8.f;          // log2 units
+constexpr float kLn2 = 0.693147180559945309f;
+
+enum SpanSite : int32_t { kSiteQ = 70, kSiteK, kSiteRope, kSiteV, kSiteSlot, kSiteQkDone,
+                          kSiteP, kSitePv, kSiteStaged, kSiteDrain };
+
+// Step j of a pair uses stage j & 1. Those marked L are used in the pair's
+// first CTA only, the one that issues the MMAs.
+struct Bars {
+    uint64_t q_full;              // L: both CTAs' rows
+    uint64_t k_full[2][4];        // L: slots 2g, 2g + 1 of both CTAs
+    uint64_t rope_full;           // L
+    uint64_t v_full[2];           // this CTA's value blocks of the other page
+    uint64_t qk_part[2];          // the MMAs of slots 0..3 and of the RoPE block are done
+    uint64_t s_full[2];           // all score MMAs of the step
+    uint64_t pv_done[2][4];       // the P V MMAs that read slots 2g, 2g + 1; [3]: all of the step
+    uint64_t p_ready;             // L: 2 x 4 warps: weights written, results rescaled
+    uint64_t drain;               // L
+    uint64_t q_staged;            // fp8 cache: what the widening warps wait for
+    uint64_t k_staged[2][4];
+    uint64_t rope_staged;
+    uint64_t v_staged[2];
+    uint32_t tmem_base;
+    int32_t abort;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Bars* bars, int32_t* status,
+                                       int32_t site, uint64_t limit_ns, bool ignore_abort) {
+    volatile int32_t* abort = &bars->abort;
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+        for (int i = 0; i < 4; ++i)
+            if (ptx::mbar_try_wait_sleep(bar, parity, kSuspendNs)) return true;
+        if (!ignore_abort && *abort != 0) return false;
+        if (ptx::globaltimer() - t0 > limit_ns) {
+            *abort = 1;
+            record_error(status, MLA_ERR_TIMEOUT, site);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Bars* bars, int32_t* status,
+                                     int32_t site, uint64_t limit_ns, bool ignore_abort = false) {
+    if (ptx::mbar_test_wait(bar, parity)) return true;
+    return wait_slow(bar, parity, bars, status, site, limit_ns, ignore_abort);
+}
+
+// Arrive on a barrier of either CTA, with this thread's writes before it.
+__device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+// Four MMAs of a pair of CTAs (M = 128: 64 rows of A and D in each, half of
+// B's columns in each CTA's shared memory), K steps `sa` and `sb` apart.
+__device__ __forceinline__ void mma4_pair(uint32_t d, uint64_t a, uint64_t sa, uint64_t b,
+                                          uint64_t sb, uint32_t idesc, uint32_t acc0) {
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " setp.ne.b32 p, %10, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %5, %9, p;\n"
+        " setp.eq.b32 p, %10, %10;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %2, %6, %9, p;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %3, %7, %9, p;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %4, %8, %9, p;\n}\n"
+        ::"r"(d), "l"(a), "l"(a + sa), "l"(a + 2 * sa), "l"(a + 3 * sa), "l"(b), "l"(b + sb),
+          "l"(b + 2 * sb), "l"(b + 3 * sb), "r"(idesc), "r"(acc0)
+        : "memory");
+}
+
+// ------------------------------------------------------------ a pair's work
+
+struct Piece {
+    SpanItem it;
+    int first, steps;      // steps [first, first + steps) of the item
+    int64_t part_row;      // -1: it writes the results
+};
+
+struct Walk {
+    int64_t g0, g1;
+    int item, items, pair, pairs;
+    int64_t units;
+};
+
+__device__ __forceinline__ Walk walk_begin(const SpanParams& p, int pair) {
+    const SpanHeader h = *p.header;
+    Walk w{0, 0, 0, 0, pair, h.pairs, h.units};
+    if (pair < h.pairs) {
+        w.g0 = pair_begin(pair, h.pairs, h.units);
+        w.g1 = pair_begin(pair + 1, h.pairs, h.units);
+        w.item = p.pair_item[pair];
+        w.items = h.items;
+    }
+    return w;
+}
+
+__device__ __forceinline__ bool walk_next(const SpanParams& p, Walk& w, Piece& pc) {
+    while (w.item < w.items) {
+        const int4* src = reinterpret_cast<const int4*>(p.items + w.item);
+        int4* dst = reinterpret_cast<int4*>(&pc.it);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = src[i];
+        if (pc.it.unit0 >= w.g1) break;
+        ++w.item;
+        if (!span_piece(pc.it, w.g0, w.g1, &pc.first, &pc.steps)) continue;
+        const bool whole = pc.it.unit0 + kSpanItemCost >= w.g0 && pc.it.unit1 <= w.g1;
+        pc.part_row = whole && pc.it.alone ? -1
+                                           : int64_t(pc.it.part_row) + int64_t(w.pair) * kSpanRows;
+        return true;
+    }
+    w.item = w.items;
+    return false;
+}
+
+__device__ __forceinline__ int real_page(const SpanItem& it, int v) {
+    return v < it.head_pages ? v : v + it.page_shift;
+}
+
+// The tokens of virtual page v that are seen: rows [0, a) and [b, e).
+struct PageMask {
+    int a, b, e;
+    __device__ __forceinline__ bool all() const {
+        return e == kPageSize && (b <= 0 || a >= kPageSize || b <= a);
+    }
+    __device__ __forceinline__ bool sees(int i) const { return i < e && (i < a || i >= b); }
+};
+__device__ __forceinline__ PageMask page_mask(const SpanItem& it, int v) {
+    if (v >= it.pages) return PageMask{0, 0, 0};
+    const int t0 = real_page(it, v) * kPageSize;
+    return PageMask{it.sink_end - t0, it.tail_lo - t0, min(it.end - t0, kPageSize)};
+}
+
+// The y coordinate of a page in the cache's tensor map; rows before the first
+// one (which TMA fills with zeros) for one that is not there.
+__device__ __forceinline__ int32_t page_row(const SpanParams& p, const SpanItem& it, int v,
+                                            bool record) {
+    if (v >= it.pages) return -kPageSize;
+    const int page = p.table[int64_t(it.table_row) * p.max_blocks + real_page(it, v)];
+    if (page < 0 || int64_t(page) >= p.num_blocks) {
+        if (record) record_error(p.status, MLA_ERR_BAD_BLOCK_ID, page);
+        return -kPageSize;
+    }
+    return page * kPageSize;
+}
+
+// ------------------------------------------------------------ loads
+// The order in which a CTA's operands are loaded (and widened). In the
+// order of the MMAs (scores of step j, then P V of step j - 1, and at an
+// item's end its last P V before the next item's first scores) no load waits
+// for something that a later one is needed for.
+//   l.queries(piece, n), l.keys(step, j), l.rope(step, j), l.values(step, j)
+// each returns false to stop.
+struct Step {
+    int32_t y[2];       // the two pages' rows
+    bool first;         // of its piece
+};
+
+template <typename L>
+__device__ __forceinline__ void load_order(const SpanParams& p, int pair, int rank, L& l) {
+    Walk w = walk_begin(p, pair);
+    Piece pc;
+    int k = 0;                       // steps of the piece that have been taken
+    bool more = walk_next(p, w, pc);
+    Step cur, nxt;
+    auto take = [&](Step& s) {       // the next step; sets `more`
+        s.first = k == 0;
+        const int v = kSpanStepPages * (pc.first + k);
+        s.y[0] = page_row(p, pc.it, v, rank == 0);
+        s.y[1] = page_row(p, pc.it, v + 1, rank == 1);
+        ++k;
+    };
+    if (!more) return;
+    take(cur);
+    if (!l.queries(pc, 0) || !l.rope(cur, 0) || !l.keys(cur, 0)) return;
+    for (int j = 0;; ++j) {
+        // (the piece's record may be overwritten by the next one's: `cur`
+        // keeps what is needed of it)
+        if (k == pc.steps) {
+            k = 0;
+            more = walk_next(p, w, pc);
+        }
+        if (more) {
+            take(nxt);
+            if (cur.first && !l.keys(nxt, j + 1)) return;
+        }
+        if (!l.values(cur, j)) return;
+        if (!more) return;
+        if (nxt.first && !l.queries(pc, j + 1)) return;
+        if (!l.rope(nxt, j + 1)) return;
+        if (!cur.first && !l.keys(nxt, j + 1)) return;
+        cur = nxt;
+    }
+}
+
+template <bool kFp8>
+struct Loader {
+    const SpanParams& p;
+    const CUtensorMap* map_q;
+    const CUtensorMap* map_c;
+    Bars* bars;
+    uint32_t sbase, b0;
+    int rank;
+    uint64_t limit;
+    // What has been asked for, for the end.
+    int pieces = 0, keys_j = 0, ropes = 0, values_j = 0;
+    int partial = 0;      // pairs of slots of step keys_j
+
+    __device__ __forceinline__ uint32_t bar(size_t off) const { return b0 + uint32_t(off); }
+    __device__ __forceinline__ bool until(uint32_t b, uint32_t parity, int32_t site) const {
+        return wait(b, parity, bars, p.status, site, limit);
+    }
+    // A box of 64 rows x 64 columns into a slot; counts on a barrier of the
+    // pair's first CTA, or (fp8: the codes, into the slot's place `dst`) of
+    // this CTA.
+    __device__ __forceinline__ void box(uint32_t dst, int x, int32_t y, uint32_t bar) const {
+        if constexpr (kFp8)
+            ptx::tma_load_2d(dst, map_c, x, y, bar);
+        else
+            ptx::tma_load_2d_pair(dst, map_c, x, y, ptx::map_to_rank(bar, 0));
+    }
+    // Bytes that a barrier is to expect: of both CTAs on the first one's (which
+    // alone announces them), of this CTA's codes on its own.
+    __device__ __forceinline__ void expect(uint32_t bar, int blocks) const {
+        if constexpr (kFp8)
+            ptx::mbar_arrive_expect_tx(bar, uint32_t(blocks * kBlock / 2));
+        else if (rank == 0)
+            ptx::mbar_arrive_expect_tx(bar, uint32_t(2 * blocks * kBlock));
+    }
+
+    __device__ __forceinline__ bool queries(const Piece& pc, int j) {
+        if (j > 0 && !until(bar(offsetof(Bars, s_full)) + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1,
+                            kSiteQkDone))
+            return false;
+        const uint32_t full = kFp8 ? bar(offsetof(Bars, q_staged)) : bar(offsetof(Bars, q_full));
+        const uint32_t to = kFp8 ? full : ptx::map_to_rank(full, 0);
+        if constexpr (kFp8)
+            ptx::mbar_arrive_expect_tx(full, 9 * kBlock);
+        else if (rank == 0)
+            ptx::mbar_arrive_expect_tx(full, 2 * 9 * kBlock);
+        const int y = pc.it.row0 + rank * kCtaRows;
+        for (int k = 0; k < 9; ++k) {
+            const uint32_t dst = sbase + uint32_t(kOffQ + k * kBlock);
+            if constexpr (kFp8)
+                ptx::tma_load_2d(dst, map_q, 64 * k, y, to);
+            else
+                ptx::tma_load_2d_pair(dst, map_q, 64 * k, y, to);
+        }
+        ++pieces;
+        return true;
+    }
+    __device__ __forceinline__ bool keys(const Step& s, int j) {
+        const int st = j & 1;
+        partial = 0;
+        for (int g = 0; g < 4; ++g) {
+            if (j >= 2 && !until(bar(offsetof(Bars, pv_done)) + 8 * (4 * st + g),
+                                 ((j >> 1) - 1) & 1, kSiteSlot))
+                return false;
+            const uint32_t full =
+                (kFp8 ? bar(offsetof(Bars, k_staged)) : bar(offsetof(Bars, k_full))) +
+                8 * (4 * st + g);
+            expect(full, 2);
+            const uint32_t at = sbase + uint32_t(kOffStage + st * kStageBytes + 2 * g * kBlock);
+            for (int i = 0; i < 2; ++i)
+                box(kFp8 ? at + kBlock + i * (kBlock / 2) : at + i * kBlock, 64 * (2 * g + i),
+                    s.y[rank], full);
+            ++partial;
+        }
+        ++keys_j;
+        partial = 0;
+        return true;
+    }
+    __device__ __forceinline__ bool rope(const Step& s, int j) {
+        if (j > 0 && !until(bar(offsetof(Bars, qk_part)) + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1,
+                            kSiteRope))
+            return false;
+        if (j == 0 && (p.debug & kDebugWithholdLoad) != 0 && blockIdx.x == 0) return true;
+        const uint32_t full =
+            kFp8 ? bar(offsetof(Bars, rope_staged)) : bar(offsetof(Bars, rope_full));
+        expect(full, 1);
+        box(sbase + uint32_t(kOffRope + (kFp8 ? kBlock / 2 : 0)), kLkv, s.y[rank], full);
+        ++ropes;
+        return true;
+    }
+    // The first CTA: the second page's blocks 0..3 into slots 4..7; the second:
+    // the first page's blocks 4..7 into slots 0..3.
+    __device__ __forceinline__ bool values(const Step& s, int j) {
+        const int st = j & 1;
+        const uint32_t done =
+            rank == 0 ? bar(offsetof(Bars, s_full)) : bar(offsetof(Bars, qk_part));
+        if (!until(done + 8 * st, (j >> 1) & 1, kSiteV)) return false;
+        const uint32_t full =
+            (kFp8 ? bar(offsetof(Bars, v_staged)) : bar(offsetof(Bars, v_full))) + 8 * st;
+        ptx::mbar_arrive_expect_tx(full, uint32_t(4 * (kFp8 ? kBlock / 2 : kBlock)));
+        const int slot = rank == 0 ? 4 : 0;
+        const uint32_t at = sbase + uint32_t(kOffStage + st * kStageBytes + slot * kBlock);
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t dst = kFp8 ? at + (k | 1) * kBlock + (k & 1) * (kBlock / 2)
+                                      : at + k * kBlock;
+            ptx::tma_load_2d(dst, map_c, 256 * rank + 64 * k, s.y[1 - rank], full);
+        }
+        ++values_j;
+        return true;
+    }
+    // Every load asked for lands before the CTAs leave. (With fp8 each CTA has
+    // its own barriers; otherwise the first one's count for both, and the
+    // second CTA leaves after the first.)
+    __device__ __forceinline__ void drain() const {
+        auto landed = [&](uint32_t b, int n) {      // phase n of barrier b
+            wait(b, uint32_t(n) & 1, bars, p.status, kSiteDrain, limit, true);
+        };
+        if (kFp8 || rank == 0) {
+            if (pieces > 0)
+                landed(kFp8 ? bar(offsetof(Bars, q_staged)) : bar(offsetof(Bars, q_full)),
+                       pieces - 1);
+            if (ropes > 0)
+                landed(kFp8 ? bar(offsetof(Bars, rope_staged)) : bar(offsetof(Bars, rope_full)),
+                       ropes - 1);
+            const uint32_t kf = kFp8 ? bar(offsetof(Bars, k_staged)) : bar(offsetof(Bars, k_full));
+            for (int j = keys_j > 2 ? keys_j - 2 : 0; j < keys_j; ++j)
+                for (int g = 0; g < 4; ++g) landed(kf + 8 * (4 * (j & 1) + g), j >> 1);
+            for (int g = 0; g < partial; ++g)
+                landed(kf + 8 * (4 * (keys_j & 1) + g), keys_j >> 1);
+        }
+        const uint32_t vf = kFp8 ? bar(offsetof(Bars, v_staged)) : bar(offsetof(Bars, v_full));
+        for (int j = values_j > 2 ? values_j - 2 : 0; j < values_j; ++j)
+            landed(vf + 8 * (j & 1), j >> 1);
+    }
+};
+
+// ------------------------------------------------------------ fp8 widening
+
+// Four codes as two pairs of f16 (exact).
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t* h) {
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w & 0xffffu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> 16), __NV_E4M3);
+    h[0] = uint32_t(lo.x) | (uint32_t(lo.y) << 16);
+    h[1] = uint32_t(hi.x) | (uint32_t(hi.y) << 16);
+}
+
+// Two bf16 as two f16 (exact for |v| <= 65504; `big` is set beyond that).
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, bool& big) {
+    const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+    big = big || !(fabsf(lo) <= 65504.f) || !(fabsf(hi) <= 65504.f);
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+struct Widener {
+    const SpanParams& p;
+    Bars* bars;
+    unsigned char* smem;
+    uint32_t b0;
+    int rank;
+    int tid;              // 0 .. 127
+    uint64_t limit;
+    int pieces = 0;
+
+    __device__ __forceinline__ uint32_t bar(size_t off) const { return b0 + uint32_t(off); }
+    // One answer for the 128 threads: the barriers between reads and writes
+    // need them all.
+    __device__ __forceinline__ bool until(uint32_t b, uint32_t parity) const {
+        const bool ok = wait(b, parity, bars, p.status, kSiteStaged, limit);
+        return !ptx::named_barrier_or(3, 128, !ok);
+    }
+    // The writes before this are the tensor cores' to read.
+    __device__ __forceinline__ void done(uint32_t to) const {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if ((tid & 31) == 0) arrive_release_cluster(to);
+    }
+    // Codes of kN blocks (64 rows x 64 bytes each, one after another) into kN
+    // blocks of f16 in the swizzled layout, whose last half the codes lie in.
+    template <int kN>
+    __device__ __forceinline__ void blocks(unsigned char* at) const {
+        const unsigned char* codes = at + kN * (kBlock / 2);
+        uint4 v[2 * kN];
+#pragma unroll
+        for (int k = 0; k < 2 * kN; ++k)
+            v[k] = *reinterpret_cast<const uint4*>(codes + (tid + 128 * k) * 16);
+        ptx::named_barrier_sync(3, 128);
+#pragma unroll
+        for (int k = 0; k < 2 * kN; ++k) {
+            const int i = tid + 128 * k;               // 256 chunks of 16 codes a block
+            const int r = (i >> 2) & 63, c = i & 3;
+            uint32_t h[8];
+            widen4(v[k].x, h);
+            widen4(v[k].y, h + 2);
+            widen4(v[k].z, h + 4);
+            widen4(v[k].w, h + 6);
+            unsigned char* row = at + (i >> 8) * kBlock + r * 128;
+            *reinterpret_cast<uint4*>(row + (((2 * c) ^ (r & 7)) * 16)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (r & 7)) * 16)) =
+                make_uint4(h[4], h[5], h[6], h[7]);
+        }
+    }
+    __device__ __forceinline__ bool queries(const Piece& pc, int) {
+        if (!until(bar(offsetof(Bars, q_staged)), uint32_t(pieces) & 1)) return false;
+        ++pieces;
+        bool big = false;
+        const int live = pc.it.rows - rank * kCtaRows;
+#pragma unroll 4
+        for (int i = tid; i < 9 * kBlock / 16; i += 128) {
+            uint4* a = reinterpret_cast<uint4*>(smem + kOffQ) + i;
+            const uint4 v = *a;
+            bool b = false;
+            *a = make_uint4(bf16x2_to_f16x2(v.x, b), bf16x2_to_f16x2(v.y, b),
+                            bf16x2_to_f16x2(v.z, b), bf16x2_to_f16x2(v.w, b));
+            big = big || (b && ((i >> 3) & 63) < live);
+        }
+        if (big) record_error(p.status, MLA_ERR_RANGE, pc.it.row0 / p.heads);
+        done(ptx::map_to_rank(bar(offsetof(Bars, q_full)), 0));
+        return true;
+    }
+    __device__ __forceinline__ bool keys(const Step&, int j) {
+        const int st = j & 1;
+        for (int g = 0; g < 4; ++g) {
+            const uint32_t off = uint32_t(8 * (4 * st + g));
+            if (!until(bar(offsetof(Bars, k_staged)) + off, (j >> 1) & 1)) return false;
+            blocks<2>(smem + kOffStage + st * kStageBytes + 2 * g * kBlock);
+            done(ptx::map_to_rank(bar(offsetof(Bars, k_full)) + off, 0));
+        }
+        return true;
+    }
+    __device__ __forceinline__ bool rope(const Step&, int j) {
+        if (!until(bar(offsetof(Bars, rope_staged)), uint32_t(j) & 1)) return false;
+        blocks<1>(smem + kOffRope);
+        done(ptx::map_to_rank(bar(offsetof(Bars, rope_full)), 0));
+        return true;
+    }
+    __device__ __forceinline__ bool values(const Step&, int j) {
+        const int st = j & 1;
+        if (!until(bar(offsetof(Bars, v_staged)) + 8 * st, (j >> 1) & 1)) return false;
+        unsigned char* at = smem + kOffStage + st * kStageBytes + (rank == 0 ? 4 : 0) * kBlock;
+        blocks<2>(at);
+        blocks<2>(at + 2 * kBlock);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if ((tid & 31) == 0) ptx::mbar_arrive(bar(offsetof(Bars, v_full)) + 8 * st);
+        return true;
+    }
+};
+
+// ------------------------------------------------------------ the kernel
+
+template <bool kFp8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
+mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
+                const __grid_constant__ CUtensorMap map_c) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t sbase = ptx::smem_addr(smem);
+    Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
+    const uint32_t b0 = sbase + kOffBar;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = int(ptx::cluster_ctarank());
+    const int pair = blockIdx.x >> 1;
+    auto bar = [&](size_t off) { return b0 + uint32_t(off); };
+
+    // The merge's CTAs may be placed while this grid works; they wait for its end.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if ((sbase & 1023u) != 0) {   // the swizzled tiles need it (the same in both CTAs)
+        if (threadIdx.x == 0) record_error(p.status, MLA_ERR_UNSUPPORTED, 0);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        // With an fp8 cache the widening warps of both CTAs announce operands.
+        const uint32_t full = kFp8 ? 2 * 4 : 1;
+        ptx::mbar_init(bar(offsetof(Bars, q_full)), full);
+        ptx::mbar_init(bar(offsetof(Bars, rope_full)), full);
+        ptx::mbar_init(bar(offsetof(Bars, p_ready)), 2 * 4);
+        ptx::mbar_init(bar(offsetof(Bars, drain)), 1);
+        ptx::mbar_init(bar(offsetof(Bars, q_staged)), 1);
+        ptx::mbar_init(bar(offsetof(Bars, rope_staged)), 1);
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(bar(offsetof(Bars, v_full)) + 8 * s, kFp8 ? 4 : 1);
+            ptx::mbar_init(bar(offsetof(Bars, v_staged)) + 8 * s, 1);
+            ptx::mbar_init(bar(offsetof(Bars, qk_part)) + 8 * s, 1);
+            ptx::mbar_init(bar(offsetof(Bars, s_full)) + 8 * s, 1);
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t off = uint32_t(8 * (4 * s + g));
+                ptx::mbar_init(bar(offsetof(Bars, k_full)) + off, full);
+                ptx::mbar_init(bar(offsetof(Bars, k_staged)) + off, 1);
+                ptx::mbar_init(bar(offsetof(Bars, pv_done)) + off, 1);
+            }
+        }
+        bars->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_addr(&bars->tmem_base), kTmemCols);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();          // (the pair's barriers exist before either uses the other's)
+    ptx::tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    // The schedule is complete (and with it all that came before this call).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint64_t lim_mma = p.timeout_ns, lim_dep = 2 * p.timeout_ns;
+
+    if (warp == 0) {
+        if (ptx::elect_one()) {
+            Loader<kFp8> l{p, &map_q, &map_c, bars, sbase, b0, rank, lim_dep};
+            load_order(p, pair, rank, l);
+            l.drain();
+        }
+        __syncwarp();
+    } else if (kFp8 && warp >= 6) {
+        Widener l{p, bars, smem, b0, rank, int(threadIdx.x) - 192, lim_dep};
+        load_order(p, pair, rank, l);
+    } else if (warp == 1) {
+        if (rank == 0 && ptx::elect_one()) {
+            constexpr uint32_t idesc_qk =
+                kFp8 ? ptx::idesc_f16_f32(128, false) : ptx::idesc_bf16_f32(128, false);
+            constexpr uint32_t idesc_pv =
+                kFp8 ? ptx::idesc_f16_f32(256, true) : ptx::idesc_bf16_f32(256, true);
+            // K-major blocks: 16 k are 32 bytes. Value blocks (MN-major): 16
+            // tokens are 2 KB, 64 columns a block.
+            const uint64_t desc_k = ptx::desc_sw128(0, 16, 1024) + (sbase >> 4);
+            const uint64_t desc_v = ptx::desc_sw128(0, kBlock, 1024) + (sbase >> 4);
+            auto at = [](int off) { return uint64_t(off >> 4); };
+            auto until = [&](uint32_t b, uint32_t parity, int32_t site) {
+                return wait(b, parity, bars, p.status, site, lim_mma);
+            };
+            // Scores of step j.
+            auto scores = [&](int j) {
+                const int st = j & 1;
+                const uint32_t ph = (j >> 1) & 1;
+                const uint32_t d = tmem + kTmemS + uint32_t(st * 64);
+                const uint32_t kf = bar(offsetof(Bars, k_full)) + 32 * st;
+                const uint64_t q = desc_k + at(kOffQ);
+                const uint64_t k = desc_k + at(kOffStage) + uint64_t(st) * at(kStageBytes);
+                auto slots = [&](int g) {
+#pragma unroll
+                    for (int i = 2 * g; i < 2 * g + 2; ++i)
+                        mma4_pair(d, q + at(i * kBlock), 2, k + at(i * kBlock), 2, idesc_qk,
+                                  i > 0 ? 1u : 0u);
+                };
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (g == 2) {
+                        if (!until(bar(offsetof(Bars, rope_full)), j & 1, kSiteRope)) return false;
+                        ptx::tc_fence_after();
+                        mma4_pair(d, q + at(8 * kBlock), 2, desc_k + at(kOffRope), 2, idesc_qk, 1u);
+                        ptx::mma_commit_pair(bar(offsetof(Bars, qk_part)) + 8 * st, kBoth);
+                    }
+                    if (!until(kf + 8 * g, ph, kSiteK)) return false;
+                    ptx::tc_fence_after();
+                    slots(g);
+                }
+                ptx::mma_commit_pair(bar(offsetof(Bars, s_full)) + 8 * st, kBoth);
+                return true;
+            };
+            // P V of step j, the first of its piece or not.
+            auto values = [&](int j, bool first) {
+                const int st = j & 1;
+                if (!until(bar(offsetof(Bars, p_ready)), j & 1, kSiteP)) return false;
+                ptx::tc_fence_after();
+                const uint64_t v = desc_v + at(kOffStage) + uint64_t(st) * at(kStageBytes);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {        // page g / 2, value columns g % 2
+                    mma4_pair(tmem + kTmemO + uint32_t((g & 1) * 128),
+                              desc_k + at(kOffP + (g >> 1) * kBlock), 2, v + at(2 * g * kBlock),
+                              at(16 * 128), idesc_pv, first && g < 2 ? 0u : 1u);
+                    ptx::mma_commit_pair(bar(offsetof(Bars, pv_done)) + 8 * (4 * st + g), kBoth);
+                }
+                return true;
+            };
+            Walk w = walk_begin(p, pair);
+            Piece pc;
+            bool ok = true;
+            int j = 0;
+            for (uint32_t n = 0; ok && walk_next(p, w, pc); ++n) {
+                ok = until(bar(offsetof(Bars, q_full)), n & 1, kSiteQ);
+                for (int k = 0; ok && k < pc.steps; ++k, ++j) {
+                    ok = scores(j);
+                    if (ok && k > 0) ok = values(j - 1, k == 1);
+                }
+                if (ok) ok = values(j - 1, pc.steps == 1);
+            }
+            // Every MMA issued above has completed before TMEM is freed.
+            ptx::mma_commit_pair(bar(offsetof(Bars, drain)), 1);
+            wait(bar(offsetof(Bars, drain)), 0, bars, p.status, kSiteDrain, lim_mma, true);
+        }
+        __syncwarp();
+    } else {
+        // Softmax and epilogue: lane 64 f + r of TMEM holds row r's page f of a
+        // step, and its value columns 256 f .. 256 f + 255.
+        const int l = (warp & 3) * 32 + lane;
+        const int f = l >> 6, r = l & 63;
+        const uint32_t trow = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const uint32_t swap_bar = 1 + (warp & 1);          // the two warps with these rows
+        float* swap = reinterpret_cast<float*>(smem + kOffSwap);
+        const uint32_t to_ready = ptx::map_to_rank(bar(offsetof(Bars, p_ready)), 0);
+        const float scale = fabsf(p.scale_log2);
+        Walk w = walk_begin(p, pair);
+        Piece pc;
+        bool ok = true;
+        int j = 0;
+        // Both threads' answer, and the other one's value.
+        int turn = 0;
+        auto exchange = [&](float v, float* other) {
+            float* at = swap + (turn & 1) * 128;
+            ++turn;
+            at[l] = v;
+            ok = !ptx::named_barrier_or(swap_bar, 64, !ok);
+            *other = at[l ^ 64];
+        };
+        auto until = [&](uint32_t b, uint32_t parity, int32_t site) {
+            return __all_sync(0xffffffffu, wait(b, parity, bars, p.status, site, lim_dep));
+        };
+        while (ok && walk_next(p, w, pc)) {
+            float m_ref = -INFINITY;   // log2 units
+            float l_sum = 0.f;         // of the weights (for the LSE)
+            float l_mma = 0.f;         // of the rounded ones (for the results)
+            for (int k = 0; k < pc.steps; ++k, ++j) {
+                const int st = j & 1;
+                const int v = kSpanStepPages * (pc.first + k);
+                const PageMask mine = page_mask(pc.it, v + f);
+                ok = ok && until(bar(offsetof(Bars, s_full)) + 8 * st, (j >> 1) & 1, kSiteQkDone);
+                float x[64];
+                float mx = -INFINITY;
+                if (ok) {
+                    ptx::tc_fence_after();
+                    uint32_t raw[64];
+                    ptx::tmem_ld64(trow + kTmemS + uint32_t(st * 64), raw);
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) x[i] = __uint_as_float(raw[i]);
+                    if (p.scale_log2 < 0.f) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) x[i] = -x[i];
+                    }
+                    if (!mine.all()) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) x[i] = mine.sees(i) ? x[i] : -INFINITY;
+                    }
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2)
+                        m4[(i >> 1) & 3] = ptx::fmax3(m4[(i >> 1) & 3], x[i], x[i + 1]);
+                    mx = ptx::fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * scale;
+                }
+                float other;
+                exchange(mx, &other);
+                if (!ok) break;
+                const float m_new = fmaxf(m_ref, fmaxf(mx, other));
+                float alpha = 1.f;
+                if (m_new > m_ref + kRescaleThreshold) {
+                    alpha = ptx::ex2(m_ref - m_new);
+                    m_ref = m_new;
+                }
+                // A row that has seen no token yet keeps m_ref = -inf: its
+                // weights are 2^-inf = 0, not NaN.
+                const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+                uint32_t pk[32];
+                float2 ls = make_float2(0.f, 0.f), lm = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float2 d = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]),
+                                                make_float2(scale, scale), make_float2(neg, neg));
+                    const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
+                    ls = __fadd2_rn(ls, e);
+                    if constexpr (kFp8) {
+                        const __half2 h = __floats2half2_rn(e.x, e.y);
+                        pk[i] = *reinterpret_cast<const uint32_t*>(&h);
+                        lm = __fadd2_rn(lm, __half22float2(h));
+                    } else {
+                        pk[i] = pack_bf16(e.x, e.y);
+                        lm = __fadd2_rn(lm, make_float2(__uint_as_float(pk[i] << 16),
+                                                        __uint_as_float(pk[i] & 0xffff0000u)));
+                    }
+                }
+                l_sum = l_sum * alpha + (ls.x + ls.y);
+                l_mma = l_mma * alpha + (lm.x + lm.y);
+                // The step before has read the weights and added to the results.
+                // (A piece's first step: the epilogue has waited for it.)
+                if (k > 0) {
+                    ok = until(bar(offsetof(Bars, pv_done)) + 8 * (4 * (st ^ 1) + 3),
+                               ((j - 1) >> 1) & 1, kSitePv);
+                    if (ok && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        ptx::tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 256; c += 32) {
+                            uint32_t o[32];
+                            ptx::tmem_ld32(trow + kTmemO + uint32_t(c), o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            ptx::tmem_st32(trow + kTmemO + uint32_t(c), o);
+                        }
+                    }
+                }
+                if (ok) {
+                    unsigned char* row = smem + kOffP + f * kBlock + r * 128;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) * 16)) =
+                            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                }
+                // The other page's value blocks are there. Rows that are not
+                // seen may hold anything (even NaN), and 0 times that is to
+                // be 0.
+                ok = ok && until(bar(offsetof(Bars, v_full)) + 8 * st, (j >> 1) & 1, kSiteV);
+                if (ok) {
+#pragma unroll 1
+                    for (int g = 0; g < 2; ++g) {
+                        const PageMask mask = page_mask(pc.it, v + g);
+                        if (v + g >= pc.it.pages || mask.all()) continue;   // (no page: zeros)
+                        unsigned char* vs = smem + kOffStage + st * kStageBytes + 4 * g * kBlock;
+                        for (int i = l; i < 64 * 32; i += 128) {
+                            const int t = i >> 5;
+                            if (!mask.sees(t))
+                                *reinterpret_cast<uint4*>(vs + ((i >> 3) & 3) * kBlock + t * 128 +
+                                                          (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    ptx::fence_proxy_async_smem();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_release_cluster(to_ready);
+                }
+                // (a thread that failed says so at the next exchange)
+            }
+            // Results: normalised, to the output or to the piece's rows.
+            if (ok)
+                ok = until(bar(offsetof(Bars, pv_done)) + 8 * (4 * ((j - 1) & 1) + 3),
+                           ((j - 1) >> 1) & 1, kSitePv);
+            float other_sum, other_mma;
+            exchange(l_sum, &other_sum);
+            exchange(l_mma, &other_mma);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            l_sum += other_sum;
+            l_mma += other_mma;
+            const float inv = l_mma == 0.f ? 0.f : p.v_scale / l_mma;
+            // (a NaN comes through)
+            const float lse = l_sum == 0.f ? -INFINITY : (m_ref + log2f(l_sum)) * kLn2;
+            const int row = rank * kCtaRows + r;           // of the item
+            const bool live = row < pc.it.rows;
+            const int64_t at = pc.part_row < 0 ? int64_t(pc.it.row0) + row : pc.part_row + row;
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+                uint32_t o[32];
+                ptx::tmem_ld32(trow + kTmemO + uint32_t(c), o);
+                if (!live) continue;
+                float y[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    y[i] = l_mma == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
+                const int64_t first = at * kLkv + 256 * f + c;
+                if (pc.part_row < 0) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + first);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[i] = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]),
+                                            pack_bf16(y[8 * i + 2], y[8 * i + 3]),
+                                            pack_bf16(y[8 * i + 4], y[8 * i + 5]),
+                                            pack_bf16(y[8 * i + 6], y[8 * i + 7]));
+                } else {
+                    // (rows of the workspace are 32-byte aligned)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t v8[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v8[k] = __float_as_uint(y[8 * i + k]);
+                        ptx::st_global_v8(p.o_part + first + 8 * i, v8);
+                    }
+                }
+            }
+            if (live && f == 0) {
+                if (pc.part_row >= 0)
+                    p.lse_part[at] = lse;
+                else if (p.lse != nullptr)
+                    p.lse[at] = lse;
+            }
+            // (The next piece's first P V overwrites the results: it waits for
+            // all of these warps.)
+            ptx::tc_fence_before();
+        }
+    }
+    // Neither CTA leaves while the other's MMAs, loads or arrivals may reach it.
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+template <bool kFp8>
+int launch(const SpanParams& p, cudaStream_t st) {
+    CUtensorMap map_q, map_c;
+    if (!encode_2d(&map_q, p.q, kD, uint64_t(p.batch) * p.heads, kCtaRows))
+        return int(cudaErrorInvalidValue);
+    const uint64_t rows = uint64_t(p.num_blocks) * kPageSize;
+    if constexpr (kFp8) {
+        const cuuint64_t dims[2] = {cuuint64_t(kD), rows};
+        const cuuint64_t strides[1] = {cuuint64_t(kD)};
+        const cuuint32_t box[2] = {64, kPageSize}, estr[2] = {1, 1};
+        if (tensor_map_encoder()(&map_c, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                                 const_cast<void*>(p.cache), dims, strides, box, estr,
+                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return int(cudaErrorInvalidValue);
+    } else if (!encode_2d(&map_c, p.cache, kD, rows, kPageSize)) {
+        return int(cudaErrorInvalidValue);
+    }
+    auto kernel = mla_span_kernel<kFp8>;
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_shared_memory(kernel, kSmemBytes, &allowed);
+    if (e != cudaSuccess) return int(e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(2 * p.pairs), 1, 1);
+    cfg.blockDim = dim3(kFp8 ? kThreadsFp8 : kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    // Placed while the schedule is made.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return int(cudaLaunchKernelEx(&cfg, kernel, p, map_q, map_c));
+}
+
+}  // namespace
+
+int launch_span_attention(const SpanParams& p, bool fp8, void* stream) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return fp8 ? launch<true>(p, st) : launch<false>(p, st);
+}
+
+}  // namespace mla

@@ -1,0 +1,105 @@
+// Decode over parts of a batch's cached tokens (mla_decode_shared,
+// mla_decode_window): what the schedule, the attention kernel and the merge
+// share.
+//
+// An item is up to 128 query rows that see the same tokens: the pages
+// 0 .. head_pages - 1 of a block-table row and, `page_shift` pages further on,
+// the pages after them (virtual pages 0 .. pages - 1 in all), of whose tokens
+// t those with t < end and (t < sink_end or t >= tail_lo). Items are
+//   - 128 rows (several requests' heads) of a group that shares a prefix, over
+//     the prefix,
+//   - one request's heads over the tokens that it does not share, or over its
+//     sinks and window.
+// An item's work is its steps of two pages; kSpanItemCost steps of fixed cost
+// (query staging, epilogue) stand before them. The items' units, one after
+// another, are cut into equal contiguous ranges, one per CTA pair. The part of
+// an item that lies in one pair's range is a piece. An item that is the only
+// one of its rows and is not cut writes the results; every other piece leaves
+// its rows (fp32, normalised) and their LSEs in the workspace, piece of pair c
+// from row part_row + 128 c on, which no other piece uses: from one piece to the
+// next either c grows by one or part_row by the item's rows (at most 128).
+#pragma once
+
+#include "mla_device.cuh"
+
+namespace mla {
+
+constexpr int kSpanRows = 128;
+constexpr int kSpanStepPages = 2;
+constexpr int kSpanItemCost = 2;
+constexpr int kSpanMaxBatch = 8192;
+
+struct alignas(16) SpanItem {       // 64 bytes
+    int64_t unit0;      // units [unit0, unit1) of the call's work
+    int64_t unit1;
+    int32_t row0;       // its rows of q, out and lse: row0 .. row0 + rows - 1
+    int32_t rows;
+    int32_t table_row;
+    int32_t pages;
+    int32_t head_pages;
+    int32_t page_shift;
+    int32_t sink_end;
+    int32_t tail_lo;
+    int32_t end;
+    int32_t part_row;
+    int32_t alone;      // the only item of its rows
+    int32_t reserved;
+};
+static_assert(sizeof(SpanItem) == 64, "four 16-byte loads");
+
+struct SpanHeader {
+    int64_t units;      // T
+    int32_t pairs;      // C: ranges that the units are cut into, <= T
+    int32_t items;
+};
+
+struct SpanParams {
+    const uint16_t* q;             // bf16 [B, N, 576]
+    const void* cache;             // bf16 or E4M3 [num_blocks, 64, 576]
+    int64_t num_blocks;
+    const int32_t* table;          // [B, max_blocks]
+    const int32_t* seq_lens;       // [B]
+    const int32_t* group_starts;   // [groups + 1]
+    const int32_t* shared_lens;    // [groups]
+    int32_t groups;
+    int32_t window, sinks;         // window = 0: none
+    int32_t batch, heads, max_blocks;
+    int32_t pairs;                 // CTA pairs of the grid
+    float scale_log2, v_scale;
+    uint16_t* out;
+    float* lse;
+    // In the workspace.
+    int32_t* status;
+    SpanHeader* header;
+    SpanItem* items;               // tiles of shared prefixes first; none without units
+    int32_t* tile_row;             // [B]: 128 * the first of the request's tiles + the row in it, or -1
+    int32_t* own_item;             // [B]: the request's other item, or -1
+    int32_t* pair_item;            // [pairs]: the item that holds the pair's first unit
+    float* o_part;                 // [rows, 512]
+    float* lse_part;               // [rows]
+    uint64_t timeout_ns;
+    uint32_t debug;
+};
+
+// The piece of an item in the units [g0, g1): its steps [first, first + count).
+__device__ __forceinline__ bool span_piece(const SpanItem& it, int64_t g0, int64_t g1, int* first,
+                                           int* count) {
+    const int64_t s0 = it.unit0 + kSpanItemCost;
+    const int64_t lo = s0 > g0 ? s0 : g0, hi = it.unit1 < g1 ? it.unit1 : g1;
+    *first = int(lo - s0);
+    *count = int(hi - lo);
+    return lo < hi;
+}
+
+// The pairs [c0, c1] that work on an item.
+__device__ __forceinline__ void span_pairs(const SpanItem& it, const SpanHeader& h, int* c0,
+                                           int* c1) {
+    *c0 = pair_of_page(it.unit0 + kSpanItemCost, h.pairs, h.units);
+    *c1 = pair_of_page(it.unit1 - 1, h.pairs, h.units);
+}
+
+int launch_span_schedule(const SpanParams& p, void* stream);
+int launch_span_merge(const SpanParams& p, void* stream);
+int launch_span_attention(const SpanParams& p, bool fp8, void* stream);
+
+}  // namespace mla

@@ -41,6 +41,11 @@ Pins (see ``tests/test_oracle.py``):
     fp8 case, and equality (bit for bit in float64) with the bf16 definition
     when the scale is a power of two, so that every dequantized value is
     also a bf16 number.
+  * ``e4m3_codes`` -- every code's value gives the code back, hand-worked
+    halfway cases, torch's conversion where the quotient is exact;
+    ``cache_write`` / ``gather_rows`` -- hand-worked slots, one undoes the
+    other; ``mla_decode_window_reference`` -- a window past the length is
+    the plain decode, otherwise the plain decode over the seen rows alone.
 No function here is "parity unpinned".
 """
 
@@ -451,6 +456,64 @@ def mla_decode_reference_fp8(q, cache_bits, block_table, seq_lens, softmax_scale
 
 
 # ------------------------------------------------------- the prefill side
+
+def e4m3_codes(x, scale):
+    """The E4M3 codes nearest to the exact quotients ``x / scale``: halfway the
+    even code, +-448 beyond the largest, NaN 0x7F. ``x`` holds bf16 and
+    ``scale`` is an fp32 number, so that ``|x|`` against a border between two
+    codes times ``scale`` (5 and 24 bits) compares exactly in float64.
+    """
+    x = np.asarray(x, dtype=np.float64)
+    scale = float(np.float32(scale))
+    values = e4m3_to_float(np.arange(127))
+    borders = (values[:-1] + values[1:]) / 2 * scale        # between codes i and i + 1
+    mag = np.abs(np.where(np.isnan(x), 0.0, x))
+    past = np.searchsorted(borders, mag, side="left")       # borders below |x|
+    on = (past < borders.size) & (borders[np.minimum(past, borders.size - 1)] == mag)
+    code = np.where(on & (past % 2 == 1), past + 1, past)
+    code = np.where(np.signbit(x), code | 0x80, code)
+    return np.where(np.isnan(x), 0x7F, code).astype(np.uint8)
+
+
+def cache_write(cache, kv_c, k_pe, slot_mapping):
+    """The cache after the rows ``[kv_c | k_pe]`` went to their slots (row
+    ``slot % 64`` of block ``slot // 64``); a negative slot, or one past the
+    cache, writes nothing."""
+    out = np.array(cache)
+    blocks, page, _ = out.shape
+    for row, slot in zip(np.concatenate([kv_c, k_pe], 1), slot_mapping):
+        if 0 <= slot < blocks * page:
+            out[slot // page, slot % page] = row
+    return out
+
+
+def gather_rows(cache, block_table, first_token, lens):
+    """Entries ``first_token[b] .. first_token[b] + lens[b] - 1`` of each
+    request's table row, one request after another."""
+    page = cache.shape[1]
+    rows = [gather_request_latent(cache, block_table[b], f + n, page)[f:]
+            for b, (f, n) in enumerate(zip(first_token, lens))]
+    return np.concatenate(rows) if rows else np.zeros((0, cache.shape[2]))
+
+
+def mla_decode_window_reference(q, cache, block_table, seq_lens, softmax_scale, window, sinks,
+                                kv_lora_rank=512):
+    """The decode in which a request of L tokens sees token t if ``t >= L -
+    window`` or ``t < sinks``; pages of which it sees nothing are not looked
+    at."""
+    cache = np.asarray(cache, dtype=np.float64)
+    page = cache.shape[1]
+    batch, n_heads, _ = q.shape
+    out = np.zeros((batch, n_heads, kv_lora_rank))
+    lse = np.full((batch, n_heads), -np.inf)
+    for b in range(batch):
+        L = int(seq_lens[b])
+        rows = [cache[block_table[b][t // page], t % page] for t in range(L)
+                if t >= L - window or t < sinks]
+        if rows:
+            out[b], lse[b] = _attend_one(q[b], np.array(rows), softmax_scale, kv_lora_rank)
+    return out, lse
+
 
 def expand_kv(cache, block_table, first_token, lens, w_uk_t, w_uv):
     """Per-head keys and values of ``lens[b]`` cached tokens of each request
