@@ -32,11 +32,16 @@
 // 2^-8 or 2^-11, of each weight) for the tensor cores; results are normalised
 // by the sum of the rounded weights, the LSE keeps the sum of the others.
 //
-// An fp8 cache: codes land in the upper half of the slots that their f16 copies
-// fill, and four warps widen them in place (exact).
+// What the weights' barrier announces to the first CTA's MMA thread lies in the
+// announcing SM: shared memory, written before a proxy fence and read by that
+// SM's tensor core, and TMEM. So its arrivals release at CTA scope (at cluster
+// scope each took 1,400 cycles, and a step 3,850).
 //
-// Warps: 0 = loads, 1 = MMAs (first CTA), 2-5 = softmax and epilogue, 6-9 = fp8
-// widening. Every wait is bounded (MLA_ERR_TIMEOUT).
+// An fp8 cache: thirteen warps load the codes into registers and widen them into
+// the slots (exact).
+//
+// Warps: 1 = MMAs (first CTA), 2-5 = softmax and epilogue, 0 and 6 = loads (fp8
+// cache: 0 = queries, 6-18 = codes). Every wait is bounded (MLA_ERR_TIMEOUT).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -52,8 +57,8 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kThreadsFp8 = 320;
+constexpr int kThreads = 224;
+constexpr int kThreadsFp8 = 608;
 constexpr int kCtaRows = 64;
 constexpr int kBlock = 64 * 128;                  // 64 rows x 64 16-bit columns
 constexpr int kStages = 2;
@@ -92,10 +97,7 @@ struct Bars {
     uint64_t pv_done[2][4];       // the P V MMAs that read slots 2g, 2g + 1; [3]: all of the step
     uint64_t p_ready;             // L: 2 x 4 warps: weights written, results rescaled
     uint64_t drain;               // L
-    uint64_t q_staged;            // fp8 cache: what the widening warps wait for
-    uint64_t k_staged[2][4];
-    uint64_t rope_staged;
-    uint64_t v_staged[2];
+    uint64_t q_staged;            // fp8 cache: the queries have landed as bf16
     uint32_t tmem_base;
     int32_t abort;
 };
@@ -121,12 +123,6 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Bars* bars, 
                                      int32_t site, uint64_t limit_ns, bool ignore_abort = false) {
     if (ptx::mbar_test_wait(bar, parity)) return true;
     return wait_slow(bar, parity, bars, status, site, limit_ns, ignore_abort);
-}
-
-// Arrive on a barrier of either CTA, with this thread's writes before it.
-__device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
 }
 
 // Four MMAs of a pair of CTAs (M = 128: 64 rows of A and D in each, half of
@@ -221,56 +217,29 @@ __device__ __forceinline__ int32_t page_row(const SpanParams& p, const SpanItem&
     return page * kPageSize;
 }
 
-// ------------------------------------------------------------ loads
-// The order in which a CTA's operands are loaded (and widened). In the
-// order of the MMAs (scores of step j, then P V of step j - 1, and at an
-// item's end its last P V before the next item's first scores) no load waits
-// for something that a later one is needed for.
-//   l.queries(piece, n), l.keys(step, j), l.rope(step, j), l.values(step, j)
-// each returns false to stop.
-struct Step {
-    int32_t y[2];       // the two pages' rows
-    bool first;         // of its piece
+// A pair's steps, one after another over its pieces.
+struct Steps {
+    Walk w;
+    Piece pc;
+    int k;               // the step's number in its piece
+    __device__ __forceinline__ Steps(const SpanParams& p, int pair) : w(walk_begin(p, pair)) {
+        pc.steps = 0;
+        k = -1;
+    }
+    __device__ __forceinline__ bool next(const SpanParams& p) {
+        if (++k < pc.steps) return true;
+        k = 0;
+        return walk_next(p, w, pc);
+    }
+    __device__ __forceinline__ bool first() const { return k == 0; }
+    __device__ __forceinline__ int page() const { return kSpanStepPages * (pc.first + k); }
 };
 
-template <typename L>
-__device__ __forceinline__ void load_order(const SpanParams& p, int pair, int rank, L& l) {
-    Walk w = walk_begin(p, pair);
-    Piece pc;
-    int k = 0;                       // steps of the piece that have been taken
-    bool more = walk_next(p, w, pc);
-    Step cur, nxt;
-    auto take = [&](Step& s) {       // the next step; sets `more`
-        s.first = k == 0;
-        const int v = kSpanStepPages * (pc.first + k);
-        s.y[0] = page_row(p, pc.it, v, rank == 0);
-        s.y[1] = page_row(p, pc.it, v + 1, rank == 1);
-        ++k;
-    };
-    if (!more) return;
-    take(cur);
-    if (!l.queries(pc, 0) || !l.rope(cur, 0) || !l.keys(cur, 0)) return;
-    for (int j = 0;; ++j) {
-        // (the piece's record may be overwritten by the next one's: `cur`
-        // keeps what is needed of it)
-        if (k == pc.steps) {
-            k = 0;
-            more = walk_next(p, w, pc);
-        }
-        if (more) {
-            take(nxt);
-            if (cur.first && !l.keys(nxt, j + 1)) return;
-        }
-        if (!l.values(cur, j)) return;
-        if (!more) return;
-        if (nxt.first && !l.queries(pc, j + 1)) return;
-        if (!l.rope(nxt, j + 1)) return;
-        if (!cur.first && !l.keys(nxt, j + 1)) return;
-        cur = nxt;
-    }
-}
-
-template <bool kFp8>
+// ------------------------------------------------------------ loads
+// Two threads: one loads queries and pages, the other RoPE blocks and the
+// other page's value blocks, so that neither waits for what the other one
+// waits for (with one thread for all, a page's slots, free in the middle of
+// the P V MMAs, waited for the score MMAs: a step took 2,970 cycles).
 struct Loader {
     const SpanParams& p;
     const CUtensorMap* map_q;
@@ -279,140 +248,119 @@ struct Loader {
     uint32_t sbase, b0;
     int rank;
     uint64_t limit;
-    // What has been asked for, for the end.
-    int pieces = 0, keys_j = 0, ropes = 0, values_j = 0;
-    int partial = 0;      // pairs of slots of step keys_j
 
     __device__ __forceinline__ uint32_t bar(size_t off) const { return b0 + uint32_t(off); }
     __device__ __forceinline__ bool until(uint32_t b, uint32_t parity, int32_t site) const {
         return wait(b, parity, bars, p.status, site, limit);
     }
-    // A box of 64 rows x 64 columns into a slot; counts on a barrier of the
-    // pair's first CTA, or (fp8: the codes, into the slot's place `dst`) of
-    // this CTA.
-    __device__ __forceinline__ void box(uint32_t dst, int x, int32_t y, uint32_t bar) const {
-        if constexpr (kFp8)
-            ptx::tma_load_2d(dst, map_c, x, y, bar);
-        else
-            ptx::tma_load_2d_pair(dst, map_c, x, y, ptx::map_to_rank(bar, 0));
+    // Phase n of a barrier that counts loads: they have landed.
+    __device__ __forceinline__ void landed(uint32_t b, int n) const {
+        wait(b, uint32_t(n) & 1, bars, p.status, kSiteDrain, limit, true);
     }
-    // Bytes that a barrier is to expect: of both CTAs on the first one's (which
-    // alone announces them), of this CTA's codes on its own.
+    // A box of 64 rows x 64 columns, an operand of the pair's MMAs: it counts on
+    // a barrier of the first CTA, which alone announces both CTAs' bytes.
+    __device__ __forceinline__ void box(const CUtensorMap* map, int to, int x, int32_t y,
+                                        uint32_t bar) const {
+        ptx::tma_load_2d_pair(sbase + uint32_t(to), map, x, y, ptx::map_to_rank(bar, 0));
+    }
     __device__ __forceinline__ void expect(uint32_t bar, int blocks) const {
-        if constexpr (kFp8)
-            ptx::mbar_arrive_expect_tx(bar, uint32_t(blocks * kBlock / 2));
-        else if (rank == 0)
-            ptx::mbar_arrive_expect_tx(bar, uint32_t(2 * blocks * kBlock));
+        if (rank == 0) ptx::mbar_arrive_expect_tx(bar, uint32_t(2 * blocks * kBlock));
     }
 
-    __device__ __forceinline__ bool queries(const Piece& pc, int j) {
-        if (j > 0 && !until(bar(offsetof(Bars, s_full)) + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1,
-                            kSiteQkDone))
-            return false;
-        const uint32_t full = kFp8 ? bar(offsetof(Bars, q_staged)) : bar(offsetof(Bars, q_full));
-        const uint32_t to = kFp8 ? full : ptx::map_to_rank(full, 0);
-        if constexpr (kFp8)
-            ptx::mbar_arrive_expect_tx(full, 9 * kBlock);
-        else if (rank == 0)
-            ptx::mbar_arrive_expect_tx(full, 2 * 9 * kBlock);
-        const int y = pc.it.row0 + rank * kCtaRows;
-        for (int k = 0; k < 9; ++k) {
-            const uint32_t dst = sbase + uint32_t(kOffQ + k * kBlock);
-            if constexpr (kFp8)
-                ptx::tma_load_2d(dst, map_q, 64 * k, y, to);
-            else
-                ptx::tma_load_2d_pair(dst, map_q, 64 * k, y, to);
+    __device__ __forceinline__ void pages(int pair) const {
+        const uint32_t q_full = bar(offsetof(Bars, q_full)), k_full = bar(offsetof(Bars, k_full));
+        Steps s(p, pair);
+        int pieces = 0, j = 0, part = 0;       // part: pairs of slots of step j asked for
+        bool ok = true;
+        for (; s.next(p); ++j) {
+            const int32_t y = page_row(p, s.pc.it, s.page() + rank, true);
+            if (s.first()) {
+                // (the last scores of the piece before have been formed)
+                ok = j == 0 || until(bar(offsetof(Bars, s_full)) + 8 * ((j - 1) & 1),
+                                     ((j - 1) >> 1) & 1, kSiteQkDone);
+                if (!ok) break;
+                expect(q_full, 9);
+                for (int k = 0; k < 9; ++k)
+                    box(map_q, kOffQ + k * kBlock, 64 * k, s.pc.it.row0 + rank * kCtaRows, q_full);
+                ++pieces;
+            }
+            const int st = j & 1;
+            for (part = 0; part < 4; ++part) {
+                const uint32_t off = uint32_t(8 * (4 * st + part));
+                ok = j < 2 ||
+                     until(bar(offsetof(Bars, pv_done)) + off, ((j >> 1) - 1) & 1, kSiteSlot);
+                if (!ok) break;
+                expect(k_full + off, 2);
+                for (int i = 2 * part; i < 2 * part + 2; ++i)
+                    box(map_c, kOffStage + st * kStageBytes + i * kBlock, 64 * i, y, k_full + off);
+            }
+            if (!ok) break;
         }
-        ++pieces;
-        return true;
+        // Every load asked for lands before the CTAs leave (the second CTA
+        // leaves after the first, whose barriers count for both).
+        if (rank != 0) return;
+        if (pieces > 0) landed(q_full, pieces - 1);
+        for (int i = j > 2 ? j - 2 : 0; i <= j; ++i)
+            for (int g = 0; g < (i < j ? 4 : ok ? 0 : part); ++g)
+                landed(k_full + 8 * (4 * (i & 1) + g), i >> 1);
     }
-    __device__ __forceinline__ bool keys(const Step& s, int j) {
-        const int st = j & 1;
-        partial = 0;
-        for (int g = 0; g < 4; ++g) {
-            if (j >= 2 && !until(bar(offsetof(Bars, pv_done)) + 8 * (4 * st + g),
-                                 ((j >> 1) - 1) & 1, kSiteSlot))
-                return false;
-            const uint32_t full =
-                (kFp8 ? bar(offsetof(Bars, k_staged)) : bar(offsetof(Bars, k_full))) +
-                8 * (4 * st + g);
-            expect(full, 2);
-            const uint32_t at = sbase + uint32_t(kOffStage + st * kStageBytes + 2 * g * kBlock);
-            for (int i = 0; i < 2; ++i)
-                box(kFp8 ? at + kBlock + i * (kBlock / 2) : at + i * kBlock, 64 * (2 * g + i),
-                    s.y[rank], full);
-            ++partial;
-        }
-        ++keys_j;
-        partial = 0;
-        return true;
-    }
-    __device__ __forceinline__ bool rope(const Step& s, int j) {
-        if (j > 0 && !until(bar(offsetof(Bars, qk_part)) + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1,
-                            kSiteRope))
-            return false;
-        if (j == 0 && (p.debug & kDebugWithholdLoad) != 0 && blockIdx.x == 0) return true;
-        const uint32_t full =
-            kFp8 ? bar(offsetof(Bars, rope_staged)) : bar(offsetof(Bars, rope_full));
-        expect(full, 1);
-        box(sbase + uint32_t(kOffRope + (kFp8 ? kBlock / 2 : 0)), kLkv, s.y[rank], full);
-        ++ropes;
-        return true;
-    }
+
     // The first CTA: the second page's blocks 0..3 into slots 4..7; the second:
     // the first page's blocks 4..7 into slots 0..3.
-    __device__ __forceinline__ bool values(const Step& s, int j) {
-        const int st = j & 1;
-        const uint32_t done =
+    __device__ __forceinline__ void values(int pair) const {
+        const uint32_t r_full = bar(offsetof(Bars, rope_full)), v_full = bar(offsetof(Bars, v_full));
+        const uint32_t v_free =
             rank == 0 ? bar(offsetof(Bars, s_full)) : bar(offsetof(Bars, qk_part));
-        if (!until(done + 8 * st, (j >> 1) & 1, kSiteV)) return false;
-        const uint32_t full =
-            (kFp8 ? bar(offsetof(Bars, v_staged)) : bar(offsetof(Bars, v_full))) + 8 * st;
-        ptx::mbar_arrive_expect_tx(full, uint32_t(4 * (kFp8 ? kBlock / 2 : kBlock)));
-        const int slot = rank == 0 ? 4 : 0;
-        const uint32_t at = sbase + uint32_t(kOffStage + st * kStageBytes + slot * kBlock);
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t dst = kFp8 ? at + (k | 1) * kBlock + (k & 1) * (kBlock / 2)
-                                      : at + k * kBlock;
-            ptx::tma_load_2d(dst, map_c, 256 * rank + 64 * k, s.y[1 - rank], full);
-        }
-        ++values_j;
-        return true;
-    }
-    // Every load asked for lands before the CTAs leave. (With fp8 each CTA has
-    // its own barriers; otherwise the first one's count for both, and the
-    // second CTA leaves after the first.)
-    __device__ __forceinline__ void drain() const {
-        auto landed = [&](uint32_t b, int n) {      // phase n of barrier b
-            wait(b, uint32_t(n) & 1, bars, p.status, kSiteDrain, limit, true);
+        Steps s(p, pair);
+        int ropes = 0, j = 0;
+        int32_t other = 0, y[2] = {0, 0};
+        auto rope = [&]() {
+            if (ropes == 0 && (p.debug & kDebugWithholdLoad) != 0 && blockIdx.x == 0) return;
+            expect(r_full, 1);
+            box(map_c, kOffRope, kLkv, y[rank], r_full);
+            ++ropes;
         };
-        if (kFp8 || rank == 0) {
-            if (pieces > 0)
-                landed(kFp8 ? bar(offsetof(Bars, q_staged)) : bar(offsetof(Bars, q_full)),
-                       pieces - 1);
-            if (ropes > 0)
-                landed(kFp8 ? bar(offsetof(Bars, rope_staged)) : bar(offsetof(Bars, rope_full)),
-                       ropes - 1);
-            const uint32_t kf = kFp8 ? bar(offsetof(Bars, k_staged)) : bar(offsetof(Bars, k_full));
-            for (int j = keys_j > 2 ? keys_j - 2 : 0; j < keys_j; ++j)
-                for (int g = 0; g < 4; ++g) landed(kf + 8 * (4 * (j & 1) + g), j >> 1);
-            for (int g = 0; g < partial; ++g)
-                landed(kf + 8 * (4 * (keys_j & 1) + g), keys_j >> 1);
+        auto take = [&]() {
+            const bool more = s.next(p);
+            if (more) {
+                y[0] = page_row(p, s.pc.it, s.page(), false);
+                y[1] = page_row(p, s.pc.it, s.page() + 1, false);
+            }
+            return more;
+        };
+        bool more = take();
+        if (more) rope();
+        for (; more; ++j) {
+            const int st = j & 1;
+            const uint32_t ph = (j >> 1) & 1;
+            other = y[1 - rank];
+            more = take();
+            if (more) {
+                if (!until(bar(offsetof(Bars, qk_part)) + 8 * st, ph, kSiteRope)) break;
+                rope();
+            }
+            if (!until(v_free + 8 * st, ph, kSiteV)) break;
+            ptx::mbar_arrive_expect_tx(v_full + 8 * st, uint32_t(4 * kBlock));
+            for (int k = 0; k < 4; ++k)
+                ptx::tma_load_2d(sbase + uint32_t(kOffStage + st * kStageBytes +
+                                                  ((rank == 0 ? 4 : 0) + k) * kBlock),
+                                 map_c, 256 * rank + 64 * k, other, v_full + 8 * st);
         }
-        const uint32_t vf = kFp8 ? bar(offsetof(Bars, v_staged)) : bar(offsetof(Bars, v_full));
-        for (int j = values_j > 2 ? values_j - 2 : 0; j < values_j; ++j)
-            landed(vf + 8 * (j & 1), j >> 1);
+        if (ropes > 0 && rank == 0) landed(r_full, ropes - 1);
+        for (int i = j > 2 ? j - 2 : 0; i < j; ++i) landed(v_full + 8 * (i & 1), i >> 1);
     }
 };
 
 // ------------------------------------------------------------ fp8 widening
 
 // Four codes as two pairs of f16 (exact).
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t* h) {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> 16), __NV_E4M3);
-    h[0] = uint32_t(lo.x) | (uint32_t(lo.y) << 16);
-    h[1] = uint32_t(hi.x) | (uint32_t(hi.y) << 16);
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+    uint2 h;
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n"
+        " cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+        : "=r"(h.x), "=r"(h.y)
+        : "r"(w));
+    return h;
 }
 
 // Two bf16 as two f16 (exact for |v| <= 65504; `big` is set beyond that).
@@ -423,62 +371,114 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, bool& big) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Each of thirteen warps has one 64-column block of every step (a page's
+// eight, the RoPE block, four of the other page's value blocks): it holds the
+// block's codes in registers, loaded while the slot was still in use, and
+// widens them into the slot when that is free, so that between one use of a
+// slot and the next there is no load, only the conversion. (Six warps that
+// loaded codes into the slot by TMA and widened them in place: 6,500 cycles a
+// step.)
 struct Widener {
     const SpanParams& p;
+    const CUtensorMap* map_q;
     Bars* bars;
     unsigned char* smem;
-    uint32_t b0;
-    int rank;
-    int tid;              // 0 .. 127
+    uint32_t sbase, b0;
+    int rank, lane;
     uint64_t limit;
-    int pieces = 0;
 
     __device__ __forceinline__ uint32_t bar(size_t off) const { return b0 + uint32_t(off); }
-    // One answer for the 128 threads: the barriers between reads and writes
-    // need them all.
-    __device__ __forceinline__ bool until(uint32_t b, uint32_t parity) const {
-        const bool ok = wait(b, parity, bars, p.status, kSiteStaged, limit);
-        return !ptx::named_barrier_or(3, 128, !ok);
+    // One answer for the warp.
+    __device__ __forceinline__ bool until(uint32_t b, uint32_t parity, int32_t site) const {
+        return __all_sync(0xffffffffu, wait(b, parity, bars, p.status, site, limit));
     }
     // The writes before this are the tensor cores' to read.
     __device__ __forceinline__ void done(uint32_t to) const {
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if ((tid & 31) == 0) arrive_release_cluster(to);
+        if (lane == 0) ptx::mbar_arrive_cluster(to);
     }
-    // Codes of kN blocks (64 rows x 64 bytes each, one after another) into kN
-    // blocks of f16 in the swizzled layout, whose last half the codes lie in.
-    template <int kN>
-    __device__ __forceinline__ void blocks(unsigned char* at) const {
-        const unsigned char* codes = at + kN * (kBlock / 2);
-        uint4 v[2 * kN];
+    // 64 rows of 64 codes from row y of the cache, columns 64 kb ..; zeros for
+    // a page that is not there (y < 0).
+    __device__ __forceinline__ void load(int32_t y, int kb, uint4 (&v)[8]) const {
+        const unsigned char* src = static_cast<const unsigned char*>(p.cache) +
+                                   (int64_t(y) + (lane >> 2)) * kD + 64 * kb + 16 * (lane & 3);
 #pragma unroll
-        for (int k = 0; k < 2 * kN; ++k)
-            v[k] = *reinterpret_cast<const uint4*>(codes + (tid + 128 * k) * 16);
-        ptx::named_barrier_sync(3, 128);
+        for (int k = 0; k < 8; ++k)
+            v[k] = y >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + 8 * k * kD))
+                          : make_uint4(0, 0, 0, 0);
+    }
+    // Them as f16 in the swizzled layout.
+    __device__ __forceinline__ void store(const uint4 (&v)[8], int at) const {
+        const int r = lane >> 2, c = lane & 3;
+        unsigned char* row = smem + at + r * 128;
+        const int even = ((2 * c) ^ r) * 16, odd = ((2 * c + 1) ^ r) * 16;
 #pragma unroll
-        for (int k = 0; k < 2 * kN; ++k) {
-            const int i = tid + 128 * k;               // 256 chunks of 16 codes a block
-            const int r = (i >> 2) & 63, c = i & 3;
-            uint32_t h[8];
-            widen4(v[k].x, h);
-            widen4(v[k].y, h + 2);
-            widen4(v[k].z, h + 4);
-            widen4(v[k].w, h + 6);
-            unsigned char* row = at + (i >> 8) * kBlock + r * 128;
-            *reinterpret_cast<uint4*>(row + (((2 * c) ^ (r & 7)) * 16)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (r & 7)) * 16)) =
-                make_uint4(h[4], h[5], h[6], h[7]);
+        for (int k = 0; k < 8; ++k) {
+            const uint2 a = widen4(v[k].x), b = widen4(v[k].y);
+            const uint2 d = widen4(v[k].z), e = widen4(v[k].w);
+            *reinterpret_cast<uint4*>(row + k * 1024 + even) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4*>(row + k * 1024 + odd) = make_uint4(d.x, d.y, e.x, e.y);
         }
     }
-    __device__ __forceinline__ bool queries(const Piece& pc, int) {
-        if (!until(bar(offsetof(Bars, q_staged)), uint32_t(pieces) & 1)) return false;
-        ++pieces;
+
+    // Warp w: block w (0 .. 7) of this CTA's page, 8: its RoPE block, 9 .. 12:
+    // block w - 9 of this CTA's value columns of the other page.
+    __device__ __forceinline__ void blocks(int pair, int w) const {
+        const bool own = w <= 8;
+        const int kb = own ? w : 4 * rank + w - 9;
+        const int slot = own ? w : (rank == 0 ? 4 : 0) + w - 9;
+        const int side = own ? rank : 1 - rank;
+        Steps s(p, pair);
+        uint4 v[8];
+        bool more = s.next(p), first = true;
+        int rows = 0, row0 = 0;
+        uint32_t pieces = 0;
+        int32_t y = -1;
+        if (more) load(page_row(p, s.pc.it, s.page() + side, w == 0), kb, v);
+        for (int j = 0; more; ++j) {
+            const int st = j & 1;
+            const uint32_t ph = (j >> 1) & 1;
+            if (first) {
+                rows = s.pc.it.rows;
+                row0 = s.pc.it.row0;
+            }
+            const bool begins = first;
+            // The next step's page is looked up now, its codes are loaded below.
+            more = s.next(p);
+            first = more && s.first();
+            if (more) y = page_row(p, s.pc.it, s.page() + side, w == 0);
+            if (w < 8) {
+                if (begins) {
+                    if (!until(bar(offsetof(Bars, q_staged)), pieces++ & 1, kSiteStaged)) return;
+                    widen_queries(w, rows - rank * kCtaRows, row0);
+                }
+                const uint32_t off = uint32_t(8 * (4 * st + (w >> 1)));
+                if (j >= 2 && !until(bar(offsetof(Bars, pv_done)) + off, ph ^ 1, kSiteSlot)) return;
+                store(v, kOffStage + st * kStageBytes + slot * kBlock);
+                done(ptx::map_to_rank(bar(offsetof(Bars, k_full)) + off, 0));
+            } else if (w == 8) {
+                if (j > 0 && !until(bar(offsetof(Bars, qk_part)) + 8 * (st ^ 1),
+                                    ((j - 1) >> 1) & 1, kSiteRope))
+                    return;
+                if (j == 0 && (p.debug & kDebugWithholdLoad) != 0 && blockIdx.x == 0) return;
+                store(v, kOffRope);
+                done(ptx::map_to_rank(bar(offsetof(Bars, rope_full)), 0));
+            } else {
+                const uint32_t v_free =
+                    rank == 0 ? bar(offsetof(Bars, s_full)) : bar(offsetof(Bars, qk_part));
+                if (!until(v_free + 8 * st, ph, kSiteV)) return;
+                store(v, kOffStage + st * kStageBytes + slot * kBlock);
+                done(ptx::map_to_rank(bar(offsetof(Bars, v_full)) + 8 * st, uint32_t(rank)));
+            }
+            if (more) load(y, kb, v);
+        }
+    }
+    // An eighth of the queries, from bf16, in place.
+    __device__ __forceinline__ void widen_queries(int w, int live, int row0) const {
         bool big = false;
-        const int live = pc.it.rows - rank * kCtaRows;
-#pragma unroll 4
-        for (int i = tid; i < 9 * kBlock / 16; i += 128) {
+#pragma unroll 2
+        for (int i = 32 * w + lane; i < 9 * kBlock / 16; i += 256) {
             uint4* a = reinterpret_cast<uint4*>(smem + kOffQ) + i;
             const uint4 v = *a;
             bool b = false;
@@ -486,36 +486,30 @@ struct Widener {
                             bf16x2_to_f16x2(v.z, b), bf16x2_to_f16x2(v.w, b));
             big = big || (b && ((i >> 3) & 63) < live);
         }
-        if (big) record_error(p.status, MLA_ERR_RANGE, pc.it.row0 / p.heads);
+        if (big) record_error(p.status, MLA_ERR_RANGE, row0 / p.heads);
         done(ptx::map_to_rank(bar(offsetof(Bars, q_full)), 0));
-        return true;
     }
-    __device__ __forceinline__ bool keys(const Step&, int j) {
-        const int st = j & 1;
-        for (int g = 0; g < 4; ++g) {
-            const uint32_t off = uint32_t(8 * (4 * st + g));
-            if (!until(bar(offsetof(Bars, k_staged)) + off, (j >> 1) & 1)) return false;
-            blocks<2>(smem + kOffStage + st * kStageBytes + 2 * g * kBlock);
-            done(ptx::map_to_rank(bar(offsetof(Bars, k_full)) + off, 0));
+    // One thread: a piece's queries, when the scores of the piece before it have
+    // been formed. (It waits for every step in turn: a phase is told from the one
+    // before the last by nothing.)
+    __device__ __forceinline__ void queries(int pair) const {
+        const uint32_t staged = bar(offsetof(Bars, q_staged));
+        Steps s(p, pair);
+        int pieces = 0;
+        for (int j = 0; s.next(p); ++j) {
+            if (s.first()) {
+                ptx::mbar_arrive_expect_tx(staged, 9 * kBlock);
+                for (int k = 0; k < 9; ++k)
+                    ptx::tma_load_2d(sbase + uint32_t(kOffQ + k * kBlock), map_q, 64 * k,
+                                     s.pc.it.row0 + rank * kCtaRows, staged);
+                ++pieces;
+            }
+            if (!wait(bar(offsetof(Bars, s_full)) + 8 * (j & 1), (j >> 1) & 1, bars, p.status,
+                      kSiteQkDone, limit))
+                break;
         }
-        return true;
-    }
-    __device__ __forceinline__ bool rope(const Step&, int j) {
-        if (!until(bar(offsetof(Bars, rope_staged)), uint32_t(j) & 1)) return false;
-        blocks<1>(smem + kOffRope);
-        done(ptx::map_to_rank(bar(offsetof(Bars, rope_full)), 0));
-        return true;
-    }
-    __device__ __forceinline__ bool values(const Step&, int j) {
-        const int st = j & 1;
-        if (!until(bar(offsetof(Bars, v_staged)) + 8 * st, (j >> 1) & 1)) return false;
-        unsigned char* at = smem + kOffStage + st * kStageBytes + (rank == 0 ? 4 : 0) * kBlock;
-        blocks<2>(at);
-        blocks<2>(at + 2 * kBlock);
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if ((tid & 31) == 0) ptx::mbar_arrive(bar(offsetof(Bars, v_full)) + 8 * st);
-        return true;
+        if (pieces > 0)
+            wait(staged, uint32_t(pieces - 1) & 1, bars, p.status, kSiteDrain, limit, true);
     }
 };
 
@@ -542,22 +536,18 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
     }
     if (threadIdx.x == 0) {
         // With an fp8 cache the widening warps of both CTAs announce operands.
-        const uint32_t full = kFp8 ? 2 * 4 : 1;
-        ptx::mbar_init(bar(offsetof(Bars, q_full)), full);
-        ptx::mbar_init(bar(offsetof(Bars, rope_full)), full);
+        ptx::mbar_init(bar(offsetof(Bars, q_full)), kFp8 ? 2 * 8 : 1);
+        ptx::mbar_init(bar(offsetof(Bars, rope_full)), kFp8 ? 2 : 1);
         ptx::mbar_init(bar(offsetof(Bars, p_ready)), 2 * 4);
         ptx::mbar_init(bar(offsetof(Bars, drain)), 1);
         ptx::mbar_init(bar(offsetof(Bars, q_staged)), 1);
-        ptx::mbar_init(bar(offsetof(Bars, rope_staged)), 1);
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(bar(offsetof(Bars, v_full)) + 8 * s, kFp8 ? 4 : 1);
-            ptx::mbar_init(bar(offsetof(Bars, v_staged)) + 8 * s, 1);
             ptx::mbar_init(bar(offsetof(Bars, qk_part)) + 8 * s, 1);
             ptx::mbar_init(bar(offsetof(Bars, s_full)) + 8 * s, 1);
             for (int g = 0; g < 4; ++g) {
                 const uint32_t off = uint32_t(8 * (4 * s + g));
-                ptx::mbar_init(bar(offsetof(Bars, k_full)) + off, full);
-                ptx::mbar_init(bar(offsetof(Bars, k_staged)) + off, 1);
+                ptx::mbar_init(bar(offsetof(Bars, k_full)) + off, kFp8 ? 2 * 2 : 1);
                 ptx::mbar_init(bar(offsetof(Bars, pv_done)) + off, 1);
             }
         }
@@ -577,16 +567,22 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint64_t lim_mma = p.timeout_ns, lim_dep = 2 * p.timeout_ns;
 
-    if (warp == 0) {
+    if (!kFp8 && (warp == 0 || warp == 6)) {
         if (ptx::elect_one()) {
-            Loader<kFp8> l{p, &map_q, &map_c, bars, sbase, b0, rank, lim_dep};
-            load_order(p, pair, rank, l);
-            l.drain();
+            const Loader l{p, &map_q, &map_c, bars, sbase, b0, rank, lim_dep};
+            if (warp == 0)
+                l.pages(pair);
+            else
+                l.values(pair);
         }
         __syncwarp();
-    } else if (kFp8 && warp >= 6) {
-        Widener l{p, bars, smem, b0, rank, int(threadIdx.x) - 192, lim_dep};
-        load_order(p, pair, rank, l);
+    } else if (kFp8 && (warp == 0 || warp >= 6)) {
+        const Widener l{p, &map_q, bars, smem, sbase, b0, rank, lane, lim_dep};
+        if (warp >= 6)
+            l.blocks(pair, warp - 6);
+        else if (ptx::elect_one())
+            l.queries(pair);
+        __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && ptx::elect_one()) {
             constexpr uint32_t idesc_qk =
@@ -697,26 +693,39 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
                 const int v = kSpanStepPages * (pc.first + k);
                 const PageMask mine = page_mask(pc.it, v + f);
                 ok = ok && until(bar(offsetof(Bars, s_full)) + 8 * st, (j >> 1) & 1, kSiteQkDone);
-                float x[64];
-                float mx = -INFINITY;
-                if (ok) {
-                    ptx::tc_fence_after();
-                    uint32_t raw[64];
-                    ptx::tmem_ld64(trow + kTmemS + uint32_t(st * 64), raw);
+                // With an fp8 cache the scores are read twice, half of them at a
+                // time: its many warps leave 96 registers a thread.
+                constexpr int kPart = kFp8 ? 32 : 64;
+                float x[kPart];
+                auto read_scores = [&](int first) {
+                    uint32_t raw[kPart];
+                    if constexpr (kFp8)
+                        ptx::tmem_ld32(trow + kTmemS + uint32_t(st * 64 + first), raw);
+                    else
+                        ptx::tmem_ld64(trow + kTmemS + uint32_t(st * 64), raw);
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) x[i] = __uint_as_float(raw[i]);
+                    for (int i = 0; i < kPart; ++i) x[i] = __uint_as_float(raw[i]);
                     if (p.scale_log2 < 0.f) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) x[i] = -x[i];
+                        for (int i = 0; i < kPart; ++i) x[i] = -x[i];
                     }
                     if (!mine.all()) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) x[i] = mine.sees(i) ? x[i] : -INFINITY;
+                        for (int i = 0; i < kPart; ++i)
+                            x[i] = mine.sees(first + i) ? x[i] : -INFINITY;
                     }
+                };
+                float mx = -INFINITY;
+                if (ok) {
+                    ptx::tc_fence_after();
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 64; i += 2)
-                        m4[(i >> 1) & 3] = ptx::fmax3(m4[(i >> 1) & 3], x[i], x[i + 1]);
+                    for (int first = 0; first < 64; first += kPart) {
+                        read_scores(first);
+#pragma unroll
+                        for (int i = 0; i < kPart; i += 2)
+                            m4[(i >> 1) & 3] = ptx::fmax3(m4[(i >> 1) & 3], x[i], x[i + 1]);
+                    }
                     mx = ptx::fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * scale;
                 }
                 float other;
@@ -735,7 +744,9 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
                 float2 ls = make_float2(0.f, 0.f), lm = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const float2 d = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]),
+                    const int at = (2 * i) % kPart;
+                    if (kFp8 && at == 0) read_scores(2 * i);
+                    const float2 d = __ffma2_rn(make_float2(x[at], x[at + 1]),
                                                 make_float2(scale, scale), make_float2(neg, neg));
                     const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
                     ls = __fadd2_rn(ls, e);
@@ -796,7 +807,7 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
                     ptx::fence_proxy_async_smem();
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_release_cluster(to_ready);
+                    if (lane == 0) ptx::mbar_arrive_cluster(to_ready);
                 }
                 // (a thread that failed says so at the next exchange)
             }
