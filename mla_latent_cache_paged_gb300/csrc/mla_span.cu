@@ -152,18 +152,19 @@ struct Piece {
 
 struct Walk {
     int64_t g0, g1;
-    int item, items, pair, pairs;
-    int64_t units;
+    int item, items, pair;
 };
 
 __device__ __forceinline__ Walk walk_begin(const SpanParams& p, int pair) {
     const SpanHeader h = *p.header;
-    Walk w{0, 0, 0, 0, pair, h.pairs, h.units};
+    Walk w{0, 0, 0, 0, pair};
     if (pair < h.pairs) {
-        w.g0 = pair_begin(pair, h.pairs, h.units);
-        w.g1 = pair_begin(pair + 1, h.pairs, h.units);
-        w.item = p.pair_item[pair];
-        w.items = h.items;
+        w.g0 = p.cuts[pair];
+        w.g1 = p.cuts[pair + 1];
+        if (w.g0 < w.g1) {                    // (else nothing has been written for it)
+            w.item = p.pair_item[pair];
+            w.items = h.items;
+        }
     }
     return w;
 }
@@ -448,29 +449,36 @@ struct Widener {
             more = s.next(p);
             first = more && s.first();
             if (more) y = page_row(p, s.pc.it, s.page() + side, w == 0);
-            if (w < 8) {
-                if (begins) {
-                    if (!until(bar(offsetof(Bars, q_staged)), pieces++ & 1, kSiteStaged)) return;
-                    widen_queries(w, rows - rank * kCtaRows, row0);
-                }
-                const uint32_t off = uint32_t(8 * (4 * st + (w >> 1)));
-                if (j >= 2 && !until(bar(offsetof(Bars, pv_done)) + off, ph ^ 1, kSiteSlot)) return;
-                store(v, kOffStage + st * kStageBytes + slot * kBlock);
-                done(ptx::map_to_rank(bar(offsetof(Bars, k_full)) + off, 0));
-            } else if (w == 8) {
-                if (j > 0 && !until(bar(offsetof(Bars, qk_part)) + 8 * (st ^ 1),
-                                    ((j - 1) >> 1) & 1, kSiteRope))
-                    return;
-                if (j == 0 && (p.debug & kDebugWithholdLoad) != 0 && blockIdx.x == 0) return;
-                store(v, kOffRope);
-                done(ptx::map_to_rank(bar(offsetof(Bars, rope_full)), 0));
-            } else {
-                const uint32_t v_free =
-                    rank == 0 ? bar(offsetof(Bars, s_full)) : bar(offsetof(Bars, qk_part));
-                if (!until(v_free + 8 * st, ph, kSiteV)) return;
-                store(v, kOffStage + st * kStageBytes + slot * kBlock);
-                done(ptx::map_to_rank(bar(offsetof(Bars, v_full)) + 8 * st, uint32_t(rank)));
+            if (w < 8 && begins) {
+                if (!until(bar(offsetof(Bars, q_staged)), pieces++ & 1, kSiteStaged)) return;
+                widen_queries(w, rows - rank * kCtaRows, row0);
             }
+            // (The stores are there once: the warps' code has to fit the
+            // instruction caches.)
+            uint32_t free_at = 0, free_ph = ph, to;
+            int32_t site = kSiteV;
+            int at = kOffStage + st * kStageBytes + slot * kBlock;
+            if (w < 8) {
+                const uint32_t off = uint32_t(8 * (4 * st + (w >> 1)));
+                if (j >= 2) free_at = bar(offsetof(Bars, pv_done)) + off;
+                free_ph = ph ^ 1;
+                site = kSiteSlot;
+                to = ptx::map_to_rank(bar(offsetof(Bars, k_full)) + off, 0);
+            } else if (w == 8) {
+                if (j > 0) free_at = bar(offsetof(Bars, qk_part)) + 8 * (st ^ 1);
+                free_ph = ((j - 1) >> 1) & 1;
+                site = kSiteRope;
+                at = kOffRope;
+                to = ptx::map_to_rank(bar(offsetof(Bars, rope_full)), 0);
+                if (j == 0 && (p.debug & kDebugWithholdLoad) != 0 && blockIdx.x == 0) return;
+            } else {
+                free_at = (rank == 0 ? bar(offsetof(Bars, s_full)) : bar(offsetof(Bars, qk_part))) +
+                          8 * st;
+                to = ptx::map_to_rank(bar(offsetof(Bars, v_full)) + 8 * st, uint32_t(rank));
+            }
+            if (free_at != 0 && !until(free_at, free_ph, site)) return;
+            store(v, at);
+            done(to);
             if (more) load(y, kb, v);
         }
     }
@@ -826,42 +834,59 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
             // (a NaN comes through)
             const float lse = l_sum == 0.f ? -INFINITY : (m_ref + log2f(l_sum)) * kLn2;
             const int row = rank * kCtaRows + r;           // of the item
-            const bool live = row < pc.it.rows;
-            const int64_t at = pc.part_row < 0 ? int64_t(pc.it.row0) + row : pc.part_row + row;
+            const int64_t row0 = pc.part_row < 0 ? int64_t(pc.it.row0) : pc.part_row;
+            // 128 bytes of a warp's 32 rows at a time, through the weights' place
+            // (these rows' own, which the last P V has read), 16-byte piece c of
+            // row i at c ^ i % 8: a lane reads TMEM by rows and writes whole lines
+            // (rows from registers, 32 bytes of each a store, took 7,000 cycles).
+            unsigned char* tile = smem + kOffP + (warp & 3) * (32 * 128);
+            const int first_row = rank * kCtaRows + (r & 32);   // of the warp's rows
+            auto put = [&](int c, const uint32_t* w) {
+                *reinterpret_cast<uint4*>(tile + lane * 128 + ((c ^ (lane & 7)) * 16)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            };
+            auto flush = [&](char* base, int64_t row_bytes) {
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = 4 * k + (lane >> 3), c = lane & 7;
+                    const uint4 v = *reinterpret_cast<const uint4*>(tile + i * 128 +
+                                                                    ((c ^ (i & 7)) * 16));
+                    if (first_row + i < pc.it.rows)
+                        *reinterpret_cast<uint4*>(base + (row0 + first_row + i) * row_bytes +
+                                                  c * 16) = v;
+                }
+                __syncwarp();
+            };
 #pragma unroll 1
             for (int c = 0; c < 256; c += 32) {
                 uint32_t o[32];
                 ptx::tmem_ld32(trow + kTmemO + uint32_t(c), o);
-                if (!live) continue;
                 float y[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     y[i] = l_mma == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
-                const int64_t first = at * kLkv + 256 * f + c;
                 if (pc.part_row < 0) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + first);
+                    // (64 columns are a line)
+                    uint32_t h[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]),
-                                            pack_bf16(y[8 * i + 2], y[8 * i + 3]),
-                                            pack_bf16(y[8 * i + 4], y[8 * i + 5]),
-                                            pack_bf16(y[8 * i + 6], y[8 * i + 7]));
+                    for (int i = 0; i < 16; ++i) h[i] = pack_bf16(y[2 * i], y[2 * i + 1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) put(((c & 32) >> 3) + i, h + 4 * i);
+                    if ((c & 32) != 0)
+                        flush(reinterpret_cast<char*>(p.out + 256 * f + c - 32), kLkv * 2);
                 } else {
-                    // (rows of the workspace are 32-byte aligned)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t v8[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v8[k] = __float_as_uint(y[8 * i + k]);
-                        ptx::st_global_v8(p.o_part + first + 8 * i, v8);
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        put(i, reinterpret_cast<const uint32_t*>(y) + 4 * i);
+                    flush(reinterpret_cast<char*>(p.o_part + 256 * f + c), kLkv * 4);
                 }
             }
-            if (live && f == 0) {
+            if (row < pc.it.rows && f == 0) {
                 if (pc.part_row >= 0)
-                    p.lse_part[at] = lse;
+                    p.lse_part[row0 + row] = lse;
                 else if (p.lse != nullptr)
-                    p.lse[at] = lse;
+                    p.lse[row0 + row] = lse;
             }
             // (The next piece's first P V overwrites the results: it waits for
             // all of these warps.)

@@ -12,8 +12,8 @@
 //     sinks and window.
 // An item's work is its steps of two pages; kSpanItemCost steps of fixed cost
 // (query staging, epilogue) stand before them. The items' units, one after
-// another, are cut into equal contiguous ranges, one per CTA pair. The part of
-// an item that lies in one pair's range is a piece. An item that is the only
+// another, are cut into contiguous ranges, one per CTA pair, of about equal
+// length. The part of an item that lies in one pair's range is a piece. An item that is the only
 // one of its rows and is not cut writes the results; every other piece leaves
 // its rows (fp32, normalised) and their LSEs in the workspace, piece of pair c
 // from row part_row + 128 c on, which no other piece uses: from one piece to the
@@ -27,6 +27,8 @@ namespace mla {
 constexpr int kSpanRows = 128;
 constexpr int kSpanStepPages = 2;
 constexpr int kSpanItemCost = 2;
+constexpr int kSpanCutCost = 6;
+constexpr int kSpanSnap = 1;
 constexpr int kSpanMaxBatch = 8192;
 
 struct alignas(16) SpanItem {       // 64 bytes
@@ -43,7 +45,8 @@ struct alignas(16) SpanItem {       // 64 bytes
     int32_t end;
     int32_t part_row;
     int32_t alone;      // the only item of its rows
-    int32_t reserved;
+    int16_t first_pair; // the pairs that work on it
+    int16_t last_pair;
 };
 static_assert(sizeof(SpanItem) == 64, "four 16-byte loads");
 
@@ -75,6 +78,7 @@ struct SpanParams {
     int32_t* tile_row;             // [B]: 128 * the first of the request's tiles + the row in it, or -1
     int32_t* own_item;             // [B]: the request's other item, or -1
     int32_t* pair_item;            // [pairs]: the item that holds the pair's first unit
+    int64_t* cuts;                 // [pairs + 1]: pair c has units [cuts[c], cuts[c + 1])
     float* o_part;                 // [rows, 512]
     float* lse_part;               // [rows]
     uint64_t timeout_ns;
@@ -89,13 +93,6 @@ __device__ __forceinline__ bool span_piece(const SpanItem& it, int64_t g0, int64
     *first = int(lo - s0);
     *count = int(hi - lo);
     return lo < hi;
-}
-
-// The pairs [c0, c1] that work on an item.
-__device__ __forceinline__ void span_pairs(const SpanItem& it, const SpanHeader& h, int* c0,
-                                           int* c1) {
-    *c0 = pair_of_page(it.unit0 + kSpanItemCost, h.pairs, h.units);
-    *c1 = pair_of_page(it.unit1 - 1, h.pairs, h.units);
 }
 
 int launch_span_schedule(const SpanParams& p, void* stream);

@@ -10,9 +10,10 @@
 // meanwhile.
 //
 // Merge: out = sum_p w_p o_p with w_p = exp(lse_p - lse), lse the log of the
-// sum of exp(lse_p), over the pieces of a row's one or two items. One CTA per
-// row, a thread per four columns: the pieces of an item lie a constant
-// distance apart, so their loads do not wait for one another.
+// sum of exp(lse_p), over the pieces of a row's one or two items. The pieces of
+// an item lie a constant distance apart, so their loads do not wait for one
+// another. A warp per row; where there are few rows, which then have many
+// pieces, a CTA per row, its warps taking the pieces in turn.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -80,6 +81,7 @@ __global__ void __launch_bounds__(kScheduleThreads) mla_span_schedule_kernel(con
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ int64_t group_smem[];
     __shared__ uint64_t warps[32];
+    __shared__ int64_t cuts[kMaxBalancedPairs + 1], edges[kMaxBalancedPairs + 1];
     const int tid = threadIdx.x;
     int G = p.groups;
     int64_t* unit0 = group_smem;                 // the group's first unit
@@ -218,23 +220,63 @@ __global__ void __launch_bounds__(kScheduleThreads) mla_span_schedule_kernel(con
             }
         }
     }
+    // The cuts between the pairs' ranges: equal ones, moved to an item's edge
+    // where that is near, or all of them if that costs no pair much.
     const int items = items_of(done);
     const int64_t T = units_of(done);
     const int C = int(T < p.pairs ? T : p.pairs);
-    if (tid == 0) *p.header = SpanHeader{T, C, items};
     __syncthreads();
-    // The item that holds each pair's first unit.
     for (int i = tid; i < items; i += kScheduleThreads) {
         const int64_t u0 = p.items[i].unit0, u1 = p.items[i].unit1;
-        for (int64_t c = (u0 * C + T - 1) / T; c < C && pair_begin(int(c), C, T) < u1; ++c)
-            p.pair_item[c] = i;
+        for (int64_t c = (u0 * C + T - 1) / T; c < C && pair_begin(int(c), C, T) < u1; ++c) {
+            const int64_t g = pair_begin(int(c), C, T);
+            const int64_t edge = g - u0 <= u1 - g ? u0 : u1;
+            cuts[c] = g;
+            edges[c] = edge;
+        }
     }
+    if (tid == 0) cuts[C] = edges[C] = T;
+    __syncthreads();
+    if (tid < 32 && C > 0) {
+        int64_t most = 0;
+        for (int c = tid; c < C; c += 32) most = max(most, edges[c + 1] - edges[c]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const bool whole = most <= (T + C - 1) / C + kSpanCutCost;
+        for (int c = tid; c < C; c += 32) {
+            const int64_t d = edges[c] - cuts[c];
+            if (whole || (d <= kSpanSnap && d >= -kSpanSnap)) cuts[c] = edges[c];
+        }
+    }
+    if (tid == 0) *p.header = SpanHeader{T, C, items};
+    __syncthreads();
+    // The pairs that work on each item, and the item that each pair begins
+    // with: the one that holds its first unit.
+    for (int i = tid; i < items; i += kScheduleThreads) {
+        const int64_t u0 = p.items[i].unit0, u1 = p.items[i].unit1;
+        auto pair_of = [&](int64_t u) {          // the last pair that begins at u or before
+            int lo = 0, hi = C;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cuts[mid] <= u) lo = mid; else hi = mid;
+            }
+            return lo;
+        };
+        const int c0 = pair_of(u0 + kSpanItemCost), c1 = pair_of(u1 - 1);
+        p.items[i].first_pair = int16_t(c0);
+        p.items[i].last_pair = int16_t(c1);
+        for (int c = pair_of(u0); c <= c1; ++c)
+            if (cuts[c] >= u0) p.pair_item[c] = i;
+    }
+    for (int c = tid; c <= C; c += kScheduleThreads) p.cuts[c] = cuts[c];
 }
 
 // ------------------------------------------------------------------ merge
 
-constexpr int kMergeThreads = 128;           // 4 columns each
+constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMaxPieces = 2 * kMaxBalancedPairs;
+constexpr int kMergeFewRows = 1024;
 
 // The weight of a part with LSE `l` among parts whose greatest is m. (A NaN
 // comes through; -inf has none.)
@@ -242,79 +284,99 @@ __device__ __forceinline__ float part_weight(float l, float m) {
     return l == -INFINITY ? 0.f : __expf(l - m);
 }
 
+// kWarps warps per row: 1, or all of a CTA's, which take its pieces in turn.
+template <int kWarps>
 __global__ void __launch_bounds__(kMergeThreads) mla_span_merge_kernel(const SpanParams p) {
-    __shared__ float weight[kMaxPieces];
-    __shared__ float red[2 * kMergeThreads / 32];
+    __shared__ float weights[kMergeWarps / kWarps][kMaxPieces];
+    __shared__ float4 sums[kWarps > 1 ? kMergeWarps : 1][kLkv / 4];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int row = blockIdx.x, tid = threadIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x * (kMergeWarps / kWarps) + warp / kWarps;
+    const int sub = warp % kWarps;
+    if (row >= p.batch * p.heads) return;
     const int b = row / p.heads, h = row - b * p.heads;
-    const SpanHeader head = *p.header;
     const int tr = p.tile_row[b], own = p.own_item[b];
-    const float* part[2] = {nullptr, nullptr};     // first piece's row of each item
-    const float* lses[2] = {nullptr, nullptr};
+    // The pieces of the row's one or two items: n[k] of them, 128 rows apart.
+    int64_t at[2] = {0, 0};
     int n[2] = {0, 0};
-    auto add = [&](int k, int item, int r) {
-        const SpanItem it = p.items[item];
-        int c0, c1;
-        span_pairs(it, head, &c0, &c1);
-        if (it.alone && c0 == c1) return false;    // its results are written
-        const int64_t at = int64_t(it.part_row) + r + int64_t(c0) * kSpanRows;
-        part[k] = p.o_part + at * kLkv;
-        lses[k] = p.lse_part + at;
-        n[k] = c1 - c0 + 1;
-        return true;
-    };
-    if (own >= 0 && !add(0, own, h)) return;
-    if (tr >= 0) add(1, (tr + h) / kSpanRows, (tr + h) % kSpanRows);
-
+    if (own >= 0) {
+        const SpanItem it = p.items[own];
+        if (it.alone && it.first_pair == it.last_pair) return;    // its results are written
+        at[0] = int64_t(it.part_row) + h + int64_t(it.first_pair) * kSpanRows;
+        n[0] = it.last_pair - it.first_pair + 1;
+    }
+    if (tr >= 0) {
+        const SpanItem it = p.items[(tr + h) / kSpanRows];
+        at[1] = int64_t(it.part_row) + (tr + h) % kSpanRows + int64_t(it.first_pair) * kSpanRows;
+        n[1] = it.last_pair - it.first_pair + 1;
+    }
     const int pieces = n[0] + n[1];
-    auto lse_at = [&](int i) {
-        return i < n[0] ? lses[0][int64_t(i) * kSpanRows] : lses[1][int64_t(i - n[0]) * kSpanRows];
-    };
+    float* weight = weights[warp / kWarps];
     float m = -INFINITY;
-    for (int i = tid; i < pieces; i += kMergeThreads) {
-        const float l = lse_at(i);
-        weight[i] = l;
+    for (int i = lane; i < pieces; i += 32) {
+        const float l = i < n[0] ? p.lse_part[at[0] + int64_t(i) * kSpanRows]
+                                 : p.lse_part[at[1] + int64_t(i - n[0]) * kSpanRows];
+        if (sub == 0) weight[i] = l;
         m = fmaxf(m, l);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) red[tid >> 5] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    if (kWarps > 1) __syncthreads(); else __syncwarp();
     float z = 0.f;
-    for (int i = tid; i < pieces; i += kMergeThreads) {
-        weight[i] = part_weight(weight[i], m);
-        z += weight[i];
-    }
+    for (int i = lane; i < pieces; i += 32) z += part_weight(weight[i], m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    if ((tid & 31) == 0) red[4 + (tid >> 5)] = z;
-    __syncthreads();
-    z = (red[4] + red[5]) + (red[6] + red[7]);
 
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    int w0 = 0;
-#pragma unroll 1
+    // 512 columns: a lane has four of each 128.
+    float4 acc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const float* src = part[k] + 4 * tid;
-#pragma unroll 4
-        for (int i = 0; i < n[k]; ++i) {
-            const float w = weight[w0 + i];
-            const float4 v = *reinterpret_cast<const float4*>(src + int64_t(i) * kSpanRows * kLkv);
-            acc.x += w * v.x;
-            acc.y += w * v.y;
-            acc.z += w * v.z;
-            acc.w += w * v.w;
+        const int begin = (sub + kWarps - (k == 0 ? 0 : n[0] % kWarps)) % kWarps;
+        const float* src = p.o_part + at[k] * kLkv + 4 * lane;
+#pragma unroll 2
+        for (int i = begin; i < n[k]; i += kWarps) {
+            const float w = part_weight(weight[(k == 0 ? 0 : n[0]) + i], m);
+            const float* piece = src + int64_t(i) * kSpanRows * kLkv;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float4 v = *reinterpret_cast<const float4*>(piece + 128 * c);
+                acc[c].x += w * v.x;
+                acc[c].y += w * v.y;
+                acc[c].z += w * v.z;
+                acc[c].w += w * v.w;
+            }
         }
-        w0 += n[k];
     }
     const float inv = z == 0.f ? 0.f : 1.f / z;
-    uint2 o;
-    o.x = pack_bf16(acc.x * inv, acc.y * inv);
-    o.y = pack_bf16(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(p.out + int64_t(row) * kLkv + 4 * tid) = o;
-    if (tid == 0 && p.lse != nullptr) p.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
+    uint16_t* out = p.out + int64_t(row) * kLkv;
+    if constexpr (kWarps == 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint2*>(out + 128 * c + 4 * lane) =
+                make_uint2(pack_bf16(acc[c].x * inv, acc[c].y * inv),
+                           pack_bf16(acc[c].z * inv, acc[c].w * inv));
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sums[warp][32 * c + lane] = acc[c];
+        __syncthreads();
+        const int tid = threadIdx.x;
+        if (tid < kLkv / 4) {
+            float4 s = sums[0][tid];
+#pragma unroll
+            for (int w = 1; w < kMergeWarps; ++w) {
+                const float4 v = sums[w][tid];
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+            }
+            *reinterpret_cast<uint2*>(out + 4 * tid) =
+                make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
+        }
+    }
+    if (sub == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
 }
 
 }  // namespace
@@ -330,8 +392,10 @@ int launch_span_schedule(const SpanParams& p, void* stream) {
 }
 
 int launch_span_merge(const SpanParams& p, void* stream) {
+    const int rows = p.batch * p.heads;
+    const bool few = rows <= kMergeFewRows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(p.batch) * unsigned(p.heads), 1, 1);
+    cfg.gridDim = dim3(unsigned(few ? rows : (rows + kMergeWarps - 1) / kMergeWarps), 1, 1);
     cfg.blockDim = dim3(kMergeThreads, 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
@@ -339,7 +403,8 @@ int launch_span_merge(const SpanParams& p, void* stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return int(cudaLaunchKernelEx(&cfg, mla_span_merge_kernel, p));
+    return int(cudaLaunchKernelEx(&cfg, few ? mla_span_merge_kernel<kMergeWarps>
+                                            : mla_span_merge_kernel<1>, p));
 }
 
 }  // namespace mla
