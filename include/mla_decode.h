@@ -800,10 +800,10 @@ int mla_cache_gather_fp8(const void* latent_cache_fp8, float k_scale, int64_t nu
  * others.
  */
 typedef struct mla_span_plan {
-    int32_t  batch;               /* B, <= 8192 */
+    int32_t  batch;               /* B, <= 4096 */
     int32_t  num_heads;           /* N */
     int32_t  max_blocks_per_seq;
-    int32_t  max_groups;          /* most groups of mla_decode_shared, <= 8192; 0 for
+    int32_t  max_groups;          /* most groups of mla_decode_shared, <= 4096; 0 for
                                      mla_decode_window */
     int32_t  num_sms;
     int32_t  pairs;               /* CTA pairs that the work is cut over */
@@ -847,7 +847,7 @@ int mla_span_plan(int batch, int num_heads, int max_blocks_per_seq, int max_grou
  *                  one must not overlap on the device.
  * A bad page id is recorded (MLA_ERR_BAD_BLOCK_ID) and its rows read as zeros,
  * a bad length is recorded and its request taken as empty. Results do not
- * depend on timing. Three launches on `stream`, no synchronisation.
+ * depend on timing. Two launches on `stream`, no synchronisation.
  */
 int mla_decode_shared(const mla_span_plan_t* plan, const void* q, const void* latent_cache,
                       int64_t num_blocks, const int32_t* block_table, const int32_t* seq_lens,

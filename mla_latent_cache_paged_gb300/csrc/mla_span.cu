@@ -50,7 +50,7 @@
 #include <cmath>
 #include <cstddef>
 
-#include "mla_span.cuh"
+#include "mla_span_schedule.cuh"
 #include "tc_ptx.cuh"
 #include "tensor_map.cuh"
 
@@ -70,8 +70,10 @@ constexpr int kOffRope = kOffStage + kStages * kStageBytes;
 constexpr int kOffP = kOffRope + kBlock;          // a block per page of the step
 constexpr int kOffBar = kOffP + 2 * kBlock;       // 229,376
 constexpr int kOffSwap = kOffBar + 512;           // 2 x 128 floats that rows' halves exchange
-constexpr int kSmemBytes = kOffSwap + 2 * 128 * 4;
+constexpr int kOffRange = kOffSwap + 2 * 128 * 4;
+constexpr int kSmemBytes = kOffRange + int(sizeof(SpanRange));
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+static_assert(sizeof(SpanScratch) <= kOffBar, "the schedule is made where the operands go");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0;                    // 2 x 64 columns
@@ -151,39 +153,30 @@ struct Piece {
 };
 
 struct Walk {
-    int64_t g0, g1;
-    int item, items, pair;
+    const SpanRange* range;
+    int item, pair;
 };
 
-__device__ __forceinline__ Walk walk_begin(const SpanParams& p, int pair) {
-    const SpanHeader h = *p.header;
-    Walk w{0, 0, 0, 0, pair};
-    if (pair < h.pairs) {
-        w.g0 = p.cuts[pair];
-        w.g1 = p.cuts[pair + 1];
-        if (w.g0 < w.g1) {                    // (else nothing has been written for it)
-            w.item = p.pair_item[pair];
-            w.items = h.items;
-        }
-    }
-    return w;
-}
-
 __device__ __forceinline__ bool walk_next(const SpanParams& p, Walk& w, Piece& pc) {
-    while (w.item < w.items) {
-        const int4* src = reinterpret_cast<const int4*>(p.items + w.item);
+    const SpanRange& r = *w.range;
+    while (w.item < r.end) {
+        const int i = w.item++ - r.first;
+        const int4* src = reinterpret_cast<const int4*>(i < kSpanKept ? r.kept + i
+                                                                      : p.items + r.first + i);
         int4* dst = reinterpret_cast<int4*>(&pc.it);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = src[i];
-        if (pc.it.unit0 >= w.g1) break;
-        ++w.item;
-        if (!span_piece(pc.it, w.g0, w.g1, &pc.first, &pc.steps)) continue;
-        const bool whole = pc.it.unit0 + kSpanItemCost >= w.g0 && pc.it.unit1 <= w.g1;
-        pc.part_row = whole && pc.it.alone ? -1
-                                           : int64_t(pc.it.part_row) + int64_t(w.pair) * kSpanRows;
+        for (int k = 0; k < 4; ++k) dst[k] = src[k];
+        // Its steps [first, first + steps) in the pair's units.
+        const int64_t s0 = pc.it.unit0 + kSpanItemCost;
+        const int64_t lo = s0 > r.g0 ? s0 : r.g0, hi = pc.it.unit1 < r.g1 ? pc.it.unit1 : r.g1;
+        if (lo >= hi) continue;      // (of its units only the fixed cost)
+        pc.first = int(lo - s0);
+        pc.steps = int(hi - lo);
+        pc.part_row = pc.it.alone && pc.it.first_pair == pc.it.last_pair
+                          ? -1
+                          : int64_t(pc.it.part_row) + int64_t(w.pair) * kSpanRows;
         return true;
     }
-    w.item = w.items;
     return false;
 }
 
@@ -223,7 +216,8 @@ struct Steps {
     Walk w;
     Piece pc;
     int k;               // the step's number in its piece
-    __device__ __forceinline__ Steps(const SpanParams& p, int pair) : w(walk_begin(p, pair)) {
+    __device__ __forceinline__ Steps(const SpanRange* range, int pair)
+        : w{range, range->first, pair} {
         pc.steps = 0;
         k = -1;
     }
@@ -268,9 +262,9 @@ struct Loader {
         if (rank == 0) ptx::mbar_arrive_expect_tx(bar, uint32_t(2 * blocks * kBlock));
     }
 
-    __device__ __forceinline__ void pages(int pair) const {
+    __device__ __forceinline__ void pages(const SpanRange* range, int pair) const {
         const uint32_t q_full = bar(offsetof(Bars, q_full)), k_full = bar(offsetof(Bars, k_full));
-        Steps s(p, pair);
+        Steps s(range, pair);
         int pieces = 0, j = 0, part = 0;       // part: pairs of slots of step j asked for
         bool ok = true;
         for (; s.next(p); ++j) {
@@ -308,11 +302,11 @@ struct Loader {
 
     // The first CTA: the second page's blocks 0..3 into slots 4..7; the second:
     // the first page's blocks 4..7 into slots 0..3.
-    __device__ __forceinline__ void values(int pair) const {
+    __device__ __forceinline__ void values(const SpanRange* range, int pair) const {
         const uint32_t r_full = bar(offsetof(Bars, rope_full)), v_full = bar(offsetof(Bars, v_full));
         const uint32_t v_free =
             rank == 0 ? bar(offsetof(Bars, s_full)) : bar(offsetof(Bars, qk_part));
-        Steps s(p, pair);
+        Steps s(range, pair);
         int ropes = 0, j = 0;
         int32_t other = 0, y[2] = {0, 0};
         auto rope = [&]() {
@@ -425,12 +419,12 @@ struct Widener {
 
     // Warp w: block w (0 .. 7) of this CTA's page, 8: its RoPE block, 9 .. 12:
     // block w - 9 of this CTA's value columns of the other page.
-    __device__ __forceinline__ void blocks(int pair, int w) const {
+    __device__ __forceinline__ void blocks(const SpanRange* range, int pair, int w) const {
         const bool own = w <= 8;
         const int kb = own ? w : 4 * rank + w - 9;
         const int slot = own ? w : (rank == 0 ? 4 : 0) + w - 9;
         const int side = own ? rank : 1 - rank;
-        Steps s(p, pair);
+        Steps s(range, pair);
         uint4 v[8];
         bool more = s.next(p), first = true;
         int rows = 0, row0 = 0;
@@ -500,9 +494,9 @@ struct Widener {
     // One thread: a piece's queries, when the scores of the piece before it have
     // been formed. (It waits for every step in turn: a phase is told from the one
     // before the last by nothing.)
-    __device__ __forceinline__ void queries(int pair) const {
+    __device__ __forceinline__ void queries(const SpanRange* range, int pair) const {
         const uint32_t staged = bar(offsetof(Bars, q_staged));
-        Steps s(p, pair);
+        Steps s(range, pair);
         int pieces = 0;
         for (int j = 0; s.next(p); ++j) {
             if (s.first()) {
@@ -566,30 +560,31 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
         ptx::tmem_alloc_pair(ptx::smem_addr(&bars->tmem_base), kTmemCols);
         ptx::tmem_relinquish_pair();
     }
+    SpanRange* range = reinterpret_cast<SpanRange*>(smem + kOffRange);
+    span_schedule(p, *reinterpret_cast<SpanScratch*>(smem), pair, blockIdx.x == 0, range);
+    ptx::fence_proxy_async_smem();     // (loads go where that was)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::cluster_sync();          // (the pair's barriers exist before either uses the other's)
     ptx::tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
-    // The schedule is complete (and with it all that came before this call).
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint64_t lim_mma = p.timeout_ns, lim_dep = 2 * p.timeout_ns;
 
     if (!kFp8 && (warp == 0 || warp == 6)) {
         if (ptx::elect_one()) {
             const Loader l{p, &map_q, &map_c, bars, sbase, b0, rank, lim_dep};
             if (warp == 0)
-                l.pages(pair);
+                l.pages(range, pair);
             else
-                l.values(pair);
+                l.values(range, pair);
         }
         __syncwarp();
     } else if (kFp8 && (warp == 0 || warp >= 6)) {
         const Widener l{p, &map_q, bars, smem, sbase, b0, rank, lane, lim_dep};
         if (warp >= 6)
-            l.blocks(pair, warp - 6);
+            l.blocks(range, pair, warp - 6);
         else if (ptx::elect_one())
-            l.queries(pair);
+            l.queries(range, pair);
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && ptx::elect_one()) {
@@ -649,7 +644,7 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
                 }
                 return true;
             };
-            Walk w = walk_begin(p, pair);
+            Walk w{range, range->first, pair};
             Piece pc;
             bool ok = true;
             int j = 0;
@@ -676,7 +671,7 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
         float* swap = reinterpret_cast<float*>(smem + kOffSwap);
         const uint32_t to_ready = ptx::map_to_rank(bar(offsetof(Bars, p_ready)), 0);
         const float scale = fabsf(p.scale_log2);
-        Walk w = walk_begin(p, pair);
+        Walk w{range, range->first, pair};
         Piece pc;
         bool ok = true;
         int j = 0;
@@ -924,18 +919,8 @@ int launch(const SpanParams& p, cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_shared_memory(kernel, kSmemBytes, &allowed);
     if (e != cudaSuccess) return int(e);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(2 * p.pairs), 1, 1);
-    cfg.blockDim = dim3(kFp8 ? kThreadsFp8 : kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = st;
-    // Placed while the schedule is made.
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return int(cudaLaunchKernelEx(&cfg, kernel, p, map_q, map_c));
+    kernel<<<2 * p.pairs, kFp8 ? kThreadsFp8 : kThreads, kSmemBytes, st>>>(p, map_q, map_c);
+    return int(cudaGetLastError());
 }
 
 }  // namespace

@@ -29,7 +29,7 @@ constexpr int kSpanStepPages = 2;
 constexpr int kSpanItemCost = 2;
 constexpr int kSpanCutCost = 6;
 constexpr int kSpanSnap = 1;
-constexpr int kSpanMaxBatch = 8192;
+constexpr int kSpanMaxBatch = 4096;
 
 struct alignas(16) SpanItem {       // 64 bytes
     int64_t unit0;      // units [unit0, unit1) of the call's work
@@ -50,12 +50,6 @@ struct alignas(16) SpanItem {       // 64 bytes
 };
 static_assert(sizeof(SpanItem) == 64, "four 16-byte loads");
 
-struct SpanHeader {
-    int64_t units;      // T
-    int32_t pairs;      // C: ranges that the units are cut into, <= T
-    int32_t items;
-};
-
 struct SpanParams {
     const uint16_t* q;             // bf16 [B, N, 576]
     const void* cache;             // bf16 or E4M3 [num_blocks, 64, 576]
@@ -73,30 +67,16 @@ struct SpanParams {
     float* lse;
     // In the workspace.
     int32_t* status;
-    SpanHeader* header;
     SpanItem* items;               // tiles of shared prefixes first; none without units
     int32_t* tile_row;             // [B]: 128 * the first of the request's tiles + the row in it, or -1
     int32_t* own_item;             // [B]: the request's other item, or -1
-    int32_t* pair_item;            // [pairs]: the item that holds the pair's first unit
-    int64_t* cuts;                 // [pairs + 1]: pair c has units [cuts[c], cuts[c + 1])
     float* o_part;                 // [rows, 512]
     float* lse_part;               // [rows]
     uint64_t timeout_ns;
     uint32_t debug;
 };
 
-// The piece of an item in the units [g0, g1): its steps [first, first + count).
-__device__ __forceinline__ bool span_piece(const SpanItem& it, int64_t g0, int64_t g1, int* first,
-                                           int* count) {
-    const int64_t s0 = it.unit0 + kSpanItemCost;
-    const int64_t lo = s0 > g0 ? s0 : g0, hi = it.unit1 < g1 ? it.unit1 : g1;
-    *first = int(lo - s0);
-    *count = int(hi - lo);
-    return lo < hi;
-}
-
-int launch_span_schedule(const SpanParams& p, void* stream);
-int launch_span_merge(const SpanParams& p, void* stream);
 int launch_span_attention(const SpanParams& p, bool fp8, void* stream);
+int launch_span_merge(const SpanParams& p, void* stream);
 
 }  // namespace mla

@@ -17,7 +17,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 // Where the workspace's arrays lie.
 struct SpanLayout {
-    uint64_t header, tile_row, own_item, pair_item, cuts, items, lse_part, o_part, bytes;
+    uint64_t tile_row, own_item, items, lse_part, o_part, bytes;
 };
 
 SpanLayout layout_of(int64_t batch, int64_t heads, int64_t groups, int64_t pairs) {
@@ -28,12 +28,9 @@ SpanLayout layout_of(int64_t batch, int64_t heads, int64_t groups, int64_t pairs
     const int64_t tiles = groups > 0 ? batch * heads / kSpanRows + shared : 0;
     const int64_t rows = tiles * kSpanRows + batch * heads + pairs * kSpanRows;
     SpanLayout s{};
-    s.header = kStatusBytes;
-    s.tile_row = s.header + 256;
+    s.tile_row = kStatusBytes;
     s.own_item = s.tile_row + up(uint64_t(batch) * 4);
-    s.pair_item = s.own_item + up(uint64_t(batch) * 4);
-    s.cuts = s.pair_item + up(uint64_t(pairs) * 4);
-    s.items = s.cuts + up(uint64_t(pairs + 1) * 8);
+    s.items = s.own_item + up(uint64_t(batch) * 4);
     s.lse_part = s.items + up(uint64_t(tiles + batch) * sizeof(SpanItem));
     s.o_part = s.lse_part + up(uint64_t(rows) * 4);
     s.bytes = s.o_part + uint64_t(rows) * kLkv * 4;
@@ -84,12 +81,9 @@ int decode_spans(const mla_span_plan_t* plan, SpanParams p, bool fp8, const void
     const SpanLayout s = layout_of(plan->batch, plan->num_heads, plan->max_groups, plan->pairs);
     char* ws = static_cast<char*>(workspace);
     p.status = reinterpret_cast<int32_t*>(ws);
-    p.header = reinterpret_cast<SpanHeader*>(ws + s.header);
     p.items = reinterpret_cast<SpanItem*>(ws + s.items);
     p.tile_row = reinterpret_cast<int32_t*>(ws + s.tile_row);
     p.own_item = reinterpret_cast<int32_t*>(ws + s.own_item);
-    p.pair_item = reinterpret_cast<int32_t*>(ws + s.pair_item);
-    p.cuts = reinterpret_cast<int64_t*>(ws + s.cuts);
     p.o_part = reinterpret_cast<float*>(ws + s.o_part);
     p.lse_part = reinterpret_cast<float*>(ws + s.lse_part);
     p.timeout_ns = kDefaultTimeoutNs;
@@ -97,8 +91,7 @@ int decode_spans(const mla_span_plan_t* plan, SpanParams p, bool fp8, const void
         p.debug = kDebugWithholdLoad;
         p.timeout_ns = kDebugTimeoutNs;
     }
-    if (launch_span_schedule(p, stream) != 0 || launch_span_attention(p, fp8, stream) != 0 ||
-        launch_span_merge(p, stream) != 0)
+    if (launch_span_attention(p, fp8, stream) != 0 || launch_span_merge(p, stream) != 0)
         return MLA_ERR_CUDA;
     return MLA_OK;
 }

@@ -69,7 +69,7 @@ def test_fp8_scales(lib, op, scale):
 @pytest.mark.parametrize("op", ["shared", "window"])
 def test_plans_that_do_not_follow_from_their_sizes(lib, op):
     for field, value in (("pairs", 77), ("pairs", 0), ("workspace_bytes", 8192), ("batch", 5), ("batch", -1),
-                         ("num_heads", 129), ("max_groups", 9000), ("flags", 1), ("reserved0", 1)):
+                         ("num_heads", 129), ("max_groups", 5000), ("flags", 1), ("reserved0", 1)):
         plan = _plan()
         nbytes = plan.workspace_bytes
         setattr(plan, field, value)
@@ -86,7 +86,7 @@ def test_an_empty_batch_needs_no_tensors(lib):
 @pytest.mark.parametrize("kw,code", [
     (dict(batch=-1), BAD), (dict(heads=0), BAD), (dict(mb=0), BAD), (dict(groups=-1), BAD), (dict(sms=0), BAD),
     (dict(extra_flags=1), BAD), (dict(heads=129), binding.MLA_ERR_UNSUPPORTED),
-    (dict(batch=8193), binding.MLA_ERR_UNSUPPORTED), (dict(groups=8193), binding.MLA_ERR_UNSUPPORTED),
+    (dict(batch=4097), binding.MLA_ERR_UNSUPPORTED), (dict(groups=4097), binding.MLA_ERR_UNSUPPORTED),
     (dict(mb=2 ** 31 - 1), binding.MLA_ERR_UNSUPPORTED),
 ])
 def test_plan_refusals(lib, kw, code):
@@ -98,7 +98,7 @@ def test_plan_refusals(lib, kw, code):
 def test_the_workspace_holds_the_pieces():
     """A row of fp32 results and its LSE for every row of every tile and
     request, and 128 more for every cut."""
-    for batch, heads, groups, sms in ((1, 1, 0, 2), (64, 128, 1, 152), (48, 16, 5, 152), (8192, 128, 8192, 512)):
+    for batch, heads, groups, sms in ((1, 1, 0, 2), (64, 128, 1, 152), (48, 16, 5, 152), (4096, 128, 4096, 512)):
         plan = _plan(batch, heads, 10, groups, sms)
         assert plan.pairs == min(256, max(1, sms // 2))
         tiles = (batch * heads // 128 + min(groups, batch // 2)) if groups else 0
