@@ -18,10 +18,8 @@
 namespace mla {
 namespace {
 
-constexpr int kMergeThreads = 256;
-constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMaxPieces = 2 * kMaxBalancedPairs;
-constexpr int kMergeFewRows = 1024;
+constexpr int kMergeRows8 = 304, kMergeRows4 = 1216;
 
 // The weight of a part with LSE `l` among parts whose greatest is m. (A NaN
 // comes through; -inf has none.)
@@ -29,16 +27,10 @@ __device__ __forceinline__ float part_weight(float l, float m) {
     return l == -INFINITY ? 0.f : __expf(l - m);
 }
 
-// kWarps warps per row: 1, or all of a CTA's, which take its pieces in turn.
+// One row, by kWarps warps: 1, or all of a CTA's, which take its pieces in turn.
 template <int kWarps>
-__global__ void __launch_bounds__(kMergeThreads) mla_span_merge_kernel(const SpanParams p) {
-    __shared__ float weights[kMergeWarps / kWarps][kMaxPieces];
-    __shared__ float4 sums[kWarps > 1 ? kMergeWarps : 1][kLkv / 4];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x * (kMergeWarps / kWarps) + warp / kWarps;
-    const int sub = warp % kWarps;
-    if (row >= p.batch * p.heads) return;
+__device__ __forceinline__ void merge_row(const SpanParams& p, int row, int lane, int sub,
+                                          float* weight, float4 (*sums)[kLkv / 4]) {
     const int b = row / p.heads, h = row - b * p.heads;
     const int tr = p.tile_row[b], own = p.own_item[b];
     // The pieces of the row's one or two items: n[k] of them, 128 rows apart.
@@ -56,7 +48,6 @@ __global__ void __launch_bounds__(kMergeThreads) mla_span_merge_kernel(const Spa
         n[1] = it.last_pair - it.first_pair + 1;
     }
     const int pieces = n[0] + n[1];
-    float* weight = weights[warp / kWarps];
     float m = -INFINITY;
     for (int i = lane; i < pieces; i += 32) {
         const float l = i < n[0] ? p.lse_part[at[0] + int64_t(i) * kSpanRows]
@@ -104,13 +95,13 @@ __global__ void __launch_bounds__(kMergeThreads) mla_span_merge_kernel(const Spa
                            pack_bf16(acc[c].z * inv, acc[c].w * inv));
     } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sums[warp][32 * c + lane] = acc[c];
+        for (int c = 0; c < 4; ++c) sums[sub][32 * c + lane] = acc[c];
         __syncthreads();
         const int tid = threadIdx.x;
-        if (tid < kLkv / 4) {
+        if (tid < kLkv / 4) {                    // (128 threads or more)
             float4 s = sums[0][tid];
 #pragma unroll
-            for (int w = 1; w < kMergeWarps; ++w) {
+            for (int w = 1; w < kWarps; ++w) {
                 const float4 v = sums[w][tid];
                 s.x += v.x;
                 s.y += v.y;
@@ -124,22 +115,44 @@ __global__ void __launch_bounds__(kMergeThreads) mla_span_merge_kernel(const Spa
     if (sub == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
 }
 
-}  // namespace
+// Warps of a CTA, and rows that they merge at once.
+template <int kWarps>
+constexpr int kCtaWarps = kWarps == 1 ? 8 : kWarps;
 
-int launch_span_merge(const SpanParams& p, void* stream) {
-    const int rows = p.batch * p.heads;
-    const bool few = rows <= kMergeFewRows;
+template <int kWarps>
+__global__ void __launch_bounds__(32 * kCtaWarps<kWarps>)
+mla_span_merge_kernel(const SpanParams p) {
+    constexpr int kRows = kCtaWarps<kWarps> / kWarps;
+    __shared__ float weights[kRows][kMaxPieces];
+    __shared__ float4 sums[kWarps][kLkv / 4];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x * kRows + warp / kWarps;
+    if (row < p.batch * p.heads)
+        merge_row<kWarps>(p, row, lane, warp % kWarps, weights[warp / kWarps], sums);
+}
+
+template <int kWarps>
+int launch(const SpanParams& p, void* stream) {
+    constexpr int kRows = kCtaWarps<kWarps> / kWarps;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(few ? rows : (rows + kMergeWarps - 1) / kMergeWarps), 1, 1);
-    cfg.blockDim = dim3(kMergeThreads, 1, 1);
+    cfg.gridDim = dim3(unsigned((p.batch * p.heads + kRows - 1) / kRows), 1, 1);
+    cfg.blockDim = dim3(32 * kCtaWarps<kWarps>, 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return int(cudaLaunchKernelEx(&cfg, few ? mla_span_merge_kernel<kMergeWarps>
-                                            : mla_span_merge_kernel<1>, p));
+    return int(cudaLaunchKernelEx(&cfg, mla_span_merge_kernel<kWarps>, p));
+}
+
+}  // namespace
+
+int launch_span_merge(const SpanParams& p, void* stream) {
+    const int rows = p.batch * p.heads;
+    return rows <= kMergeRows8 ? launch<8>(p, stream)
+           : rows <= kMergeRows4 ? launch<4>(p, stream) : launch<1>(p, stream);
 }
 
 }  // namespace mla

@@ -96,6 +96,11 @@ __device__ __forceinline__ int span_find(const T* a, int n, T v) {
     return lo;
 }
 
+// a / b, in 32 bits where that does (a division in 64 takes some 400 cycles).
+__device__ __forceinline__ int64_t span_div(int64_t a, int b) {
+    return (a >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 // Called by all threads of the CTA.
 __device__ __forceinline__ void span_schedule(const SpanParams& p, SpanScratch& s, int pair,
                                               bool first_cta, SpanRange* range) {
@@ -221,12 +226,12 @@ __device__ __forceinline__ void span_schedule(const SpanParams& p, SpanScratch& 
     auto find_request = [&](int64_t u) { return span_find(s.req_unit0, B, u); };
     auto find_tile = [&](int64_t u, int* g) {
         *g = span_find(s.group_unit0, G, u);
-        return int((u - s.group_unit0[*g]) / tile_units_of(*g));
+        return int(span_div(u - s.group_unit0[*g], tile_units_of(*g)));
     };
     // The cuts between the pairs' ranges: equal ones, moved to an item's edge
     // where that is near, or all of them if that costs no pair much.
     for (int c = tid; c < C; c += threads) {
-        const int64_t u = pair_begin(c, C, T);
+        const int64_t u = span_div(c * T, C);
         int64_t u0, u1;
         if (u < tile_units) {
             int g;
@@ -247,7 +252,7 @@ __device__ __forceinline__ void span_schedule(const SpanParams& p, SpanScratch& 
         for (int c = tid; c < C; c += 32) most = max(most, s.edges[c + 1] - s.edges[c]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        const bool whole = C > 0 && most <= (T + C - 1) / C + kSpanCutCost;
+        const bool whole = C > 0 && most <= span_div(T + C - 1, C) + kSpanCutCost;
         for (int c = tid; c < C; c += 32) {
             const int64_t d = s.edges[c] - s.cuts[c];
             if (whole || (d <= kSpanSnap && d >= -kSpanSnap)) s.cuts[c] = s.edges[c];
