@@ -323,12 +323,28 @@ struct Loader {
             }
             return more;
         };
+        // A window's pages come from HBM, whose answer takes longer than the two
+        // stages cover: a step's page is pulled into L2 a step before its slots
+        // are free (128 requests x 128 heads, window 1,024: 64 -> 58 us; two
+        // steps before: 61; pages that requests share are in L2).
+        Steps ahead(range, pair);
+        bool far = p.window > 0;
+        auto pull = [&]() {
+            far = far && ahead.next(p);
+            if (!far) return;
+            const int32_t page = page_row(p, ahead.pc.it, ahead.page() + rank, false);
+            if (page >= 0)
+                ptx::prefetch_l2(static_cast<const uint16_t*>(p.cache) + int64_t(page) * kD,
+                                 kPageSize * kD * 2);
+        };
+        far = far && ahead.next(p);
         bool more = take();
         if (more) rope();
         for (; more; ++j) {
             const int st = j & 1;
             const uint32_t ph = (j >> 1) & 1;
             other = y[1 - rank];
+            pull();
             more = take();
             if (more) {
                 if (!until(bar(offsetof(Bars, qk_part)) + 8 * st, ph, kSiteRope)) break;
