@@ -27,8 +27,7 @@ namespace mla {
 constexpr int kSpanRows = 128;
 constexpr int kSpanStepPages = 2;
 constexpr int kSpanItemCost = 2;
-constexpr int kSpanCutCost = 6;
-constexpr int kSpanSnap = 1;
+constexpr int kSpanCutCost = 4;
 constexpr int kSpanMaxBatch = 4096;
 
 struct alignas(16) SpanItem {       // 64 bytes

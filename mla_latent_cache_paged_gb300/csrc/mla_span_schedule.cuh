@@ -228,8 +228,8 @@ __device__ __forceinline__ void span_schedule(const SpanParams& p, SpanScratch& 
         *g = span_find(s.group_unit0, G, u);
         return int(span_div(u - s.group_unit0[*g], tile_units_of(*g)));
     };
-    // The cuts between the pairs' ranges: equal ones, moved to an item's edge
-    // where that is near, or all of them if that costs no pair much.
+    // The cuts between the pairs' ranges: equal ones, or all moved to an item's
+    // edge if that costs no pair much (then no item leaves pieces).
     for (int c = tid; c < C; c += threads) {
         const int64_t u = span_div(c * T, C);
         int64_t u0, u1;
@@ -253,10 +253,8 @@ __device__ __forceinline__ void span_schedule(const SpanParams& p, SpanScratch& 
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
         const bool whole = C > 0 && most <= span_div(T + C - 1, C) + kSpanCutCost;
-        for (int c = tid; c < C; c += 32) {
-            const int64_t d = s.edges[c] - s.cuts[c];
-            if (whole || (d <= kSpanSnap && d >= -kSpanSnap)) s.cuts[c] = s.edges[c];
-        }
+        for (int c = tid; c < C; c += 32)
+            if (whole) s.cuts[c] = s.edges[c];
     }
     __syncthreads();
 
