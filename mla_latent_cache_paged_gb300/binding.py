@@ -866,16 +866,17 @@ def mla_cache_compact(latent_cache, ref_counts, block_table, seq_lens, *, worksp
     return table, out, page_map, num_live
 
 
-def _rows(name, t, width, device):
-    """The address and the row stride of `t` bf16 [T, width], columns contiguous."""
+def _rows(name, t, rows, width, device):
+    """The address and the row stride of `t` bf16 [rows, width], columns contiguous."""
     import torch
     if _device_of(name, t) != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
-        raise ValueError(f"{name} must be [T, {width}] with contiguous columns")
-    stride = t.stride(0) if t.shape[0] > 1 else width
+    if t.shape != (rows, width) or t.stride(1) != 1:
+        raise ValueError(f"{name} must be [{rows}, {width}], a row for each slot, with "
+                         "contiguous columns")
+    stride = t.stride(0) if rows > 1 else width
     if stride % 8:
         raise ValueError(f"{name}'s rows must lie a multiple of 8 elements apart, not {stride}")
     return t.data_ptr(), stride
@@ -886,15 +887,17 @@ def _cache_write(fn, cache_dtype, kv_c, k_pe, slot_mapping, latent_cache, k_scal
     dev = _device_of("latent_cache", latent_cache)
     blocks = _ndim("latent_cache", latent_cache, 3, "[num_blocks, 64, 576]")[0]
     T = _ndim("slot_mapping", slot_mapping, 1, "[T]")[0]
-    for name, t in (("kv_c", kv_c), ("k_pe", k_pe)):
-        if _ndim(name, t, 2, "of two dimensions")[0] != T:
-            raise ValueError(f"{name} must have a row for each of the {T} slots")
-    _call(dev, stream, fn, *_rows("kv_c", kv_c, KV_LORA_RANK, dev),
-          *_rows("k_pe", k_pe, ROPE_DIM, dev),
-          _arg("slot_mapping", slot_mapping, torch.int64, dev), T,
-          *(() if k_scale is None else (float(k_scale),)),
-          _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM)),
-          blocks, _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
+    kv_ptr, kv_stride = _rows("kv_c", kv_c, T, KV_LORA_RANK, dev)
+    pe_ptr, pe_stride = _rows("k_pe", k_pe, T, ROPE_DIM, dev)
+    cache_ptr = _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM))
+    slots_ptr = _arg("slot_mapping", slot_mapping, torch.int64, dev)
+    ws_ptr = _arg("workspace", workspace, torch.uint8, dev)
+    if k_scale is None:
+        _call(dev, stream, fn, kv_ptr, kv_stride, pe_ptr, pe_stride, slots_ptr, T, cache_ptr,
+              blocks, ws_ptr, workspace.numel())
+    else:
+        _call(dev, stream, fn, kv_ptr, kv_stride, pe_ptr, pe_stride, slots_ptr, T, float(k_scale),
+              cache_ptr, blocks, ws_ptr, workspace.numel())
     return latent_cache
 
 
@@ -976,14 +979,14 @@ def make_span_plan(batch, num_heads, max_blocks_per_seq, *, max_groups=0, num_sm
 
 def _decode_span(fn, cache_dtype, q, latent_cache, block_table, seq_lens, middle, groups, scales,
                  plan, out, lse, return_lse, workspace, stream):
-    """One of the decodes over parts of the tokens; `middle(device, batch)`
-    gives the arguments between the lengths and the scales."""
+    """One of the decodes over parts of the tokens; `middle` are the arguments
+    between the lengths and the scales (tensors as (name, tensor, shape))."""
     import torch
     i32 = torch.int32
     dev = _device_of("q", q)
     B, N, _ = _ndim("q", q, 3, "[B, N, 576]")
     blocks = _ndim("latent_cache", latent_cache, 3, "[num_blocks, 64, 576]")[0]
-    _, mb = _ndim("block_table", block_table, 2, "[B, max_blocks_per_seq]")
+    mb = _ndim("block_table", block_table, 2, "[B, max_blocks_per_seq]")[1]
     if plan is None:
         plan = make_span_plan(B, N, mb, max_groups=groups, num_sms=torch.cuda.get_device_properties(
             dev).multi_processor_count)
@@ -992,10 +995,13 @@ def _decode_span(fn, cache_dtype, q, latent_cache, block_table, seq_lens, middle
                          f"{plan.batch, plan.num_heads, plan.max_blocks_per_seq}, not {B, N, mb}")
     elif groups > plan.max_groups:
         raise ValueError(f"the plan is for up to {plan.max_groups} groups, not {groups}")
-    args = (_arg("q", q, torch.bfloat16, dev, (B, N, HEAD_DIM)),
+    args = [_arg("q", q, torch.bfloat16, dev, (B, N, HEAD_DIM)),
             _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM)),
             blocks, _arg("block_table", block_table, i32, dev, (B, mb)),
-            _arg("seq_lens", seq_lens, i32, dev, (B,)), *middle(dev))
+            _arg("seq_lens", seq_lens, i32, dev, (B,))]
+    for m in middle:
+        args.append(_arg(m[0], m[1], i32, dev, m[2]) if type(m) is tuple else m)
+    args.extend(scales)
     out, out_ptr = _result("out", out, (B, N, KV_LORA_RANK), torch.bfloat16, dev, stream)
     lse_ptr = None
     if lse is not None or return_lse:
@@ -1004,16 +1010,14 @@ def _decode_span(fn, cache_dtype, q, latent_cache, block_table, seq_lens, middle
         workspace = _empty((int(plan.workspace_bytes),), torch.uint8, dev, stream)
         _call(dev, stream, load_library().mla_workspace_init, workspace.data_ptr(),
               workspace.numel())
-    _call(dev, stream, fn, ctypes.byref(plan), *args, *map(float, scales), out_ptr, lse_ptr,
+    _call(dev, stream, fn, ctypes.byref(plan), *args, out_ptr, lse_ptr,
           _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
     return out, lse
 
 
 def _groups(group_starts, shared_lens):
-    import torch
     G = _ndim("shared_lens", shared_lens, 1, "[groups]")[0]
-    return G, lambda dev: (_arg("group_starts", group_starts, torch.int32, dev, (G + 1,)),
-                           _arg("shared_lens", shared_lens, torch.int32, dev), G)
+    return G, (("group_starts", group_starts, (G + 1,)), ("shared_lens", shared_lens, (G,)), G)
 
 
 def mla_decode_shared(q, latent_cache, block_table, seq_lens, group_starts, shared_lens,
@@ -1027,7 +1031,7 @@ def mla_decode_shared(q, latent_cache, block_table, seq_lens, group_starts, shar
     import torch
     G, middle = _groups(group_starts, shared_lens)
     return _decode_span(load_library().mla_decode_shared, torch.bfloat16, q, latent_cache,
-                        block_table, seq_lens, middle, G, (softmax_scale,), plan, out, lse,
+                        block_table, seq_lens, middle, G, (float(softmax_scale),), plan, out, lse,
                         return_lse, workspace, stream)
 
 
@@ -1038,8 +1042,8 @@ def mla_decode_shared_fp8(q, latent_cache_fp8, block_table, seq_lens, group_star
     import torch
     G, middle = _groups(group_starts, shared_lens)
     return _decode_span(load_library().mla_decode_shared_fp8, torch.uint8, q, latent_cache_fp8,
-                        block_table, seq_lens, middle, G, (softmax_scale, k_scale), plan, out, lse,
-                        return_lse, workspace, stream)
+                        block_table, seq_lens, middle, G, (float(softmax_scale), float(k_scale)),
+                        plan, out, lse, return_lse, workspace, stream)
 
 
 def _window(window, sinks):
@@ -1048,7 +1052,7 @@ def _window(window, sinks):
     window, sinks = min(int(window), most), min(int(sinks), most)
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1, sinks at least 0")
-    return lambda dev: (window, sinks)
+    return window, sinks
 
 
 def mla_decode_window(q, latent_cache, block_table, seq_lens, softmax_scale, *, window, sinks=0,
@@ -1059,7 +1063,7 @@ def mla_decode_window(q, latent_cache, block_table, seq_lens, softmax_scale, *, 
     import torch
     return _decode_span(load_library().mla_decode_window, torch.bfloat16, q, latent_cache,
                         block_table, seq_lens, _window(window, sinks), 0,
-                        (softmax_scale,), plan, out, lse, return_lse, workspace, stream)
+                        (float(softmax_scale),), plan, out, lse, return_lse, workspace, stream)
 
 
 def mla_decode_window_fp8(q, latent_cache_fp8, block_table, seq_lens, softmax_scale, k_scale, *,
@@ -1069,7 +1073,8 @@ def mla_decode_window_fp8(q, latent_cache_fp8, block_table, seq_lens, softmax_sc
     import torch
     return _decode_span(load_library().mla_decode_window_fp8, torch.uint8, q, latent_cache_fp8,
                         block_table, seq_lens, _window(window, sinks), 0,
-                        (softmax_scale, k_scale), plan, out, lse, return_lse, workspace, stream)
+                        (float(softmax_scale), float(k_scale)), plan, out, lse, return_lse,
+                        workspace, stream)
 
 
 def read_error(workspace, stream=None):

@@ -81,8 +81,16 @@ def test_write_against_the_oracle(tokens, fp8):
     assert np.array_equal(_bits(cache, fp8), cache_write(before, *new, slots))
 
 
-@pytest.mark.parametrize("k_scale", [1.0, 0.25, 3.0, 1 / 3, 5.5 / 448, 7.03125 / 448, 448.0, 1.9999999,
-                                     1e-30, 2.0 ** -126, 2.0 ** -149, 7 * 2.0 ** -149, 1e30, 3.0e38])
+def _steps(x, n):
+    """The fp32 number ``n`` steps above ``x``."""
+    return float((np.asarray(x, np.float32).view(np.int32) + n).view(np.float32))
+
+
+@pytest.mark.parametrize("k_scale", [
+    1.0, 0.25, 3.0, 1 / 3, 5.5 / 448, 7.03125 / 448, 448.0, 1.9999999, 1e-30, 2.0 ** -126, 2.0 ** -149,
+    7 * 2.0 ** -149, 1e30, 3.0e38, _steps(1, 1), _steps(1, -1), _steps(255 / 31, 0), _steps(255 / 31, 1),
+    _steps(255 / 31, -1), _steps(0.2, 500), _steps(0.2, -500), _steps(129 / 13, 600), _steps(129 / 13, -600),
+    _steps(11.0, 400), _steps(11.0, -700), 1.2345e-5, 77.7])
 def test_every_bf16_value_gets_the_nearest_code(k_scale):
     import torch
     bits = np.arange(65536, dtype=np.uint16)

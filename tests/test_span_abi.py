@@ -111,4 +111,4 @@ def test_binding_checks(lib):
         binding._window(0, 0)
     with pytest.raises(ValueError):
         binding._window(1, -1)
-    assert binding._window(2 ** 40, 2 ** 33)(None) == (2 ** 31 - 1, 2 ** 31 - 1)
+    assert binding._window(2 ** 40, 2 ** 33) == (2 ** 31 - 1, 2 ** 31 - 1)
