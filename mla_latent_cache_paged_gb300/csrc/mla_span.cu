@@ -167,11 +167,11 @@ __device__ __forceinline__ bool walk_next(const SpanParams& p, Walk& w, Piece& p
 #pragma unroll
         for (int k = 0; k < 4; ++k) dst[k] = src[k];
         // Its steps [first, first + steps) in the pair's units.
-        const int64_t s0 = pc.it.unit0 + kSpanItemCost;
-        const int64_t lo = s0 > r.g0 ? s0 : r.g0, hi = pc.it.unit1 < r.g1 ? pc.it.unit1 : r.g1;
+        const int s0 = pc.it.unit0 + kSpanItemCost;
+        const int lo = max(s0, r.g0), hi = min(pc.it.unit1, r.g1);
         if (lo >= hi) continue;      // (of its units only the fixed cost)
-        pc.first = int(lo - s0);
-        pc.steps = int(hi - lo);
+        pc.first = lo - s0;
+        pc.steps = hi - lo;
         pc.part_row = pc.it.alone && pc.it.first_pair == pc.it.last_pair
                           ? -1
                           : int64_t(pc.it.part_row) + int64_t(w.pair) * kSpanRows;
@@ -576,12 +576,16 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
         ptx::tmem_alloc_pair(ptx::smem_addr(&bars->tmem_base), kTmemCols);
         ptx::tmem_relinquish_pair();
     }
+    // The pair's barriers exist, and its TMEM, before either uses the other's:
+    // the wait for that is over when the schedule is made.
+    ptx::tc_fence_before();
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     SpanRange* range = reinterpret_cast<SpanRange*>(smem + kOffRange);
     span_schedule(p, *reinterpret_cast<SpanScratch*>(smem), pair, blockIdx.x == 0, range);
     ptx::fence_proxy_async_smem();     // (loads go where that was)
-    ptx::tc_fence_before();
     __syncthreads();
-    ptx::cluster_sync();          // (the pair's barriers exist before either uses the other's)
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     ptx::tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     const uint64_t lim_mma = p.timeout_ns, lim_dep = 2 * p.timeout_ns;

@@ -31,8 +31,8 @@ constexpr int kSpanCutCost = 4;
 constexpr int kSpanMaxBatch = 4096;
 
 struct alignas(16) SpanItem {       // 64 bytes
-    int64_t unit0;      // units [unit0, unit1) of the call's work
-    int64_t unit1;
+    int32_t unit0;      // units [unit0, unit1) of the call's work
+    int32_t unit1;
     int32_t row0;       // its rows of q, out and lse: row0 .. row0 + rows - 1
     int32_t rows;
     int32_t table_row;

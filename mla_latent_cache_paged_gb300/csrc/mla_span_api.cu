@@ -141,7 +141,10 @@ extern "C" int mla_span_plan(int batch, int num_heads, int max_blocks_per_seq, i
         return MLA_ERR_INVALID_ARG;
     if (flags & ~MLA_PLAN_DEBUG_WITHHOLD_LOAD) return MLA_ERR_INVALID_ARG;
     if (num_heads > kMaxHeads || batch > kSpanMaxBatch || max_groups > kSpanMaxBatch ||
-        max_blocks_per_seq > tc_max_blocks())
+        max_blocks_per_seq > tc_max_blocks() ||
+        // (the schedule counts units, at most a page of each table row and six
+        // for its two items, in 32 bits)
+        int64_t(batch) * (int64_t(max_blocks_per_seq) + 6) > INT_MAX)
         return MLA_ERR_UNSUPPORTED;
     std::memset(plan, 0, sizeof(*plan));
     plan->batch = batch;
