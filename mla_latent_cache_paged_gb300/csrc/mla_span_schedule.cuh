@@ -26,7 +26,9 @@ struct SpanRange {
 // counted from the first of their own (the tiles' come before them).
 struct SpanScratch {
     int4 warps[32];
-    int32_t cuts[kMaxBalancedPairs + 1], edges[kMaxBalancedPairs + 1];
+    // Where the pairs' ranges may begin (equal ones, ranges of whole items): the
+    // unit, and twice its item's number, plus one if it is not the item's first.
+    int2 cuts[kMaxBalancedPairs + 1], edges[kMaxBalancedPairs + 1];
     int32_t lens[kSpanMaxBatch];
     int32_t req_unit0[kSpanMaxBatch + 1];     // requests' own items: where their units begin
     int32_t req_item[kSpanMaxBatch + 1];      // the items before the request's own
@@ -43,24 +45,28 @@ __device__ __forceinline__ int4 operator+(int4 a, int4 b) {
     return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// Exclusive prefix sums over the CTA's threads; *total: the sums.
-__device__ __forceinline__ int4 span_scan(int4 v, int4* warps, int4* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, count = blockDim.x >> 5;
+// Exclusive prefix sums over the CTA's threads, of which the first n have
+// something to add; *total: the sums.
+__device__ __forceinline__ int4 span_scan(int4 v, int n, int4* warps, int4* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int count = (min(n, int(blockDim.x)) + 31) >> 5;
     int4 incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int4 n = make_int4(__shfl_up_sync(0xffffffffu, incl.x, o),
-                                 __shfl_up_sync(0xffffffffu, incl.y, o),
-                                 __shfl_up_sync(0xffffffffu, incl.z, o),
-                                 __shfl_up_sync(0xffffffffu, incl.w, o));
-        if (lane >= o) incl = incl + n;
+        const int4 up = make_int4(__shfl_up_sync(0xffffffffu, incl.x, o),
+                                  __shfl_up_sync(0xffffffffu, incl.y, o),
+                                  __shfl_up_sync(0xffffffffu, incl.z, o),
+                                  __shfl_up_sync(0xffffffffu, incl.w, o));
+        if (lane >= o) incl = incl + up;
     }
     if (lane == 31) warps[warp] = incl;
     __syncthreads();
     int4 before = make_int4(0, 0, 0, 0), all = before;
+#pragma unroll 4
     for (int w = 0; w < count; ++w) {
-        if (w == warp) before = all;
-        all = all + warps[w];
+        const int4 sum = warps[w];
+        if (w < warp) before = before + sum;
+        all = all + sum;
     }
     *total = all;
     return make_int4(before.x + incl.x - v.x, before.y + incl.y - v.y, before.z + incl.z - v.z,
@@ -192,7 +198,7 @@ __device__ __forceinline__ void span_schedule(const SpanParams& p, SpanScratch& 
             v.w = kSpanItemCost + steps;
         }
         if (i0 > 0) __syncthreads();       // (the scan before has been read)
-        const int4 at = done + span_scan(v, s.warps, &total);
+        const int4 at = done + span_scan(v, max(B, G) - i0, s.warps, &total);
         done = done + total;
         if (i < G) {
             s.tile0[i] = at.x;
@@ -208,99 +214,73 @@ __device__ __forceinline__ void span_schedule(const SpanParams& p, SpanScratch& 
     if (tid == 0) {
         s.req_item[B] = done.z;
         s.req_unit0[B] = done.w;
-        s.cuts[C] = s.edges[C] = T;
+        s.cuts[C] = s.edges[C] = make_int2(T, 2 * (done.x + done.z));
     }
     __syncthreads();
 
-    // The item that holds unit u: of a request (its number), or a tile.
-    auto tile_units_of = [&](int g) { return kSpanItemCost + span_steps(s.pages[g]); };
-    auto find_request = [&](int u) { return span_find(s.req_unit0, B, u - tile_units); };
-    auto find_tile = [&](int u, int* g) {
-        *g = span_find(s.group_unit0, G, u);
-        return int(unsigned(u - s.group_unit0[*g]) / unsigned(tile_units_of(*g)));
-    };
     // The cuts between the pairs' ranges: equal ones, or all moved to an item's
     // edge if that costs no pair much (then no item leaves pieces).
+    auto tile_units_of = [&](int g) { return kSpanItemCost + span_steps(s.pages[g]); };
     const int share = C > 0 ? int(unsigned(T) / unsigned(C)) : 0, rest = T - share * C;
     for (int c = tid; c < C; c += threads) {
-        const int u = c * share + int(unsigned(c * rest) / unsigned(C));
-        int u0, u1;
+        const int u = c * share + min(c, rest);
+        int u0, u1, index;
         if (u < tile_units) {
-            int g;
-            const int k = find_tile(u, &g);
-            u0 = s.group_unit0[g] + k * tile_units_of(g);
-            u1 = u0 + tile_units_of(g);
+            const int g = span_find(s.group_unit0, G, u), each = tile_units_of(g);
+            const int k = int(unsigned(u - s.group_unit0[g]) / unsigned(each));
+            index = s.tile0[g] + k;
+            u0 = s.group_unit0[g] + k * each;
+            u1 = u0 + each;
         } else {
-            const int b = find_request(u);
+            const int b = span_find(s.req_unit0, B, u - tile_units);
+            index = tiles + s.req_item[b];
             u0 = tile_units + s.req_unit0[b];
             u1 = tile_units + s.req_unit0[b + 1];
         }
-        s.cuts[c] = u;
-        s.edges[c] = u - u0 <= u1 - u ? u0 : u1;
+        s.cuts[c] = make_int2(u, 2 * index + (u > u0 ? 1 : 0));
+        s.edges[c] = u - u0 <= u1 - u ? make_int2(u0, 2 * index) : make_int2(u1, 2 * index + 2);
     }
     __syncthreads();
     const int most = share + (rest > 0 ? 1 : 0) + kSpanCutCost;
     bool far = false;
-    for (int c = tid; c < C; c += threads) far = far || s.edges[c + 1] - s.edges[c] > most;
-    const int32_t* cuts = __syncthreads_or(far ? 1 : 0) ? s.cuts : s.edges;
+    for (int c = tid; c < C; c += threads) far = far || s.edges[c + 1].x - s.edges[c].x > most;
+    const bool whole = __syncthreads_or(far ? 1 : 0) == 0;
 
     // The pair's items, and the pairs that work on each.
-    const int g0 = pair < C ? cuts[pair] : 0, g1 = pair < C ? cuts[pair + 1] : 0;
+    const int2* cuts = whole ? s.edges : s.cuts;
+    const int2 from = pair < C ? cuts[pair] : make_int2(0, 0);
+    const int2 to = pair < C ? cuts[pair + 1] : from;
+    const int g0 = from.x, g1 = to.x;
     if (g0 < g1) {
-        auto place = [&](SpanItem it, int index, int first) {
-            // (both searches in one loop: the last cut that is not behind v[i])
-            const int v[2] = {it.unit0 + kSpanItemCost, it.unit1 - 1};
-            int lo[2] = {0, 0}, hi[2] = {C, C};
-            while (hi[0] - lo[0] > 1 || hi[1] - lo[1] > 1) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int mid = (lo[i] + hi[i]) >> 1;
-                    if (cuts[mid] <= v[i]) lo[i] = mid; else hi[i] = mid;
-                }
-            }
-            it.first_pair = int16_t(lo[0]);
-            it.last_pair = int16_t(lo[1]);
-            p.items[index] = it;
-            if (index - first < kSpanKept) range->kept[index - first] = it;
+        auto pair_of = [&](int u) {
+            const int longer = rest * (share + 1);       // units of the pairs with one more
+            return u < longer ? int(unsigned(u) / unsigned(share + 1))
+                              : rest + int(unsigned(u - longer) / unsigned(share));
         };
-        int first = -1, end = 0;
-        if (g0 < tile_units) {
-            int g;
-            const int k = find_tile(g0, &g);
-            first = s.tile0[g] + k;
-            end = tiles;
-            if (g1 <= tile_units) {
-                int ge;
-                const int ke = find_tile(g1 - 1, &ge);
-                end = s.tile0[ge] + ke + 1;
-            }
-            for (int i = first + tid; i < end; i += threads) {
-                const int gi = span_find(s.tile0, G, i), ki = i - s.tile0[gi];
-                SpanItem it{};
-                it.unit0 = s.group_unit0[gi] + ki * tile_units_of(gi);
-                it.unit1 = it.unit0 + tile_units_of(gi);
-                it.row0 = s.starts[gi] * p.heads + ki * kSpanRows;
-                it.rows = min(kSpanRows, s.starts[gi + 1] * p.heads - it.row0);
-                it.table_row = s.leader[gi];
-                it.pages = s.pages[gi];
-                it.end = s.pages[gi] * kPageSize;
+        const int first = from.y >> 1, end = (to.y + 1) >> 1;
+        for (int i = first + tid; i < end; i += threads) {
+            SpanItem it{};
+            if (i < tiles) {
+                const int g = span_find(s.tile0, G, i), k = i - s.tile0[g], each = tile_units_of(g);
+                it.unit0 = s.group_unit0[g] + k * each;
+                it.unit1 = it.unit0 + each;
+                it.row0 = s.starts[g] * p.heads + k * kSpanRows;
+                it.rows = min(kSpanRows, s.starts[g + 1] * p.heads - it.row0);
+                it.table_row = s.leader[g];
+                it.pages = s.pages[g];
+                it.end = s.pages[g] * kPageSize;
                 it.part_row = i * kSpanRows;
-                place(it, i, first);
-            }
-        }
-        if (g1 > tile_units) {
-            const int b0 = find_request(g0 > tile_units ? g0 : tile_units);
-            const int b1 = find_request(g1 - 1);
-            if (first < 0) first = tiles + s.req_item[b0];
-            end = tiles + s.req_item[b1] + 1;
-            for (int b = b0 + tid; b <= b1; b += threads) {
-                if (s.req_unit0[b + 1] == s.req_unit0[b]) continue;      // (nothing to do)
-                SpanItem it = own_item(b);
+            } else {
+                const int b = span_find(s.req_item, B, i - tiles);
+                it = own_item(b);
                 it.unit0 = tile_units + s.req_unit0[b];
                 it.unit1 = tile_units + s.req_unit0[b + 1];
-                it.part_row = tiles * kSpanRows + s.req_item[b] * p.heads;
-                place(it, tiles + s.req_item[b], first);
+                it.part_row = tiles * kSpanRows + (i - tiles) * p.heads;
             }
+            it.first_pair = int16_t(whole ? pair : pair_of(it.unit0 + kSpanItemCost));
+            it.last_pair = int16_t(whole ? pair : pair_of(it.unit1 - 1));
+            p.items[i] = it;
+            if (i - first < kSpanKept) range->kept[i - first] = it;
         }
         if (tid == 0) {
             range->first = first;
