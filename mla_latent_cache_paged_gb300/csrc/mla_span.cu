@@ -546,8 +546,6 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
     const int pair = blockIdx.x >> 1;
     auto bar = [&](size_t off) { return b0 + uint32_t(off); };
 
-    // The merge's CTAs may be placed while this grid works; they wait for its end.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if ((sbase & 1023u) != 0) {   // the swizzled tiles need it (the same in both CTAs)
         if (threadIdx.x == 0) record_error(p.status, MLA_ERR_UNSUPPORTED, 0);
         return;
@@ -581,6 +579,10 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
     ptx::tc_fence_before();
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    // What this call reads is there, and what it writes is no longer read.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The merge's CTAs may be placed while this grid works; they wait for its end.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     SpanRange* range = reinterpret_cast<SpanRange*>(smem + kOffRange);
     span_schedule(p, *reinterpret_cast<SpanScratch*>(smem), pair, blockIdx.x == 0, range);
     ptx::fence_proxy_async_smem();     // (loads go where that was)
@@ -939,8 +941,17 @@ int launch(const SpanParams& p, cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_shared_memory(kernel, kSmemBytes, &allowed);
     if (e != cudaSuccess) return int(e);
-    kernel<<<2 * p.pairs, kFp8 ? kThreadsFp8 : kThreads, kSmemBytes, st>>>(p, map_q, map_c);
-    return int(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(2 * p.pairs), 1, 1);
+    cfg.blockDim = dim3(kFp8 ? kThreadsFp8 : kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return int(cudaLaunchKernelEx(&cfg, kernel, p, map_q, map_c));
 }
 
 }  // namespace
