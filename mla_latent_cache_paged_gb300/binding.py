@@ -866,8 +866,16 @@ def mla_cache_compact(latent_cache, ref_counts, block_table, seq_lens, *, worksp
     return table, out, page_map, num_live
 
 
-def _rows(name, t, rows, width, device):
-    """The address and the row stride of `t` bf16 [rows, width], columns contiguous."""
+# The GPU is done with the smallest of the calls below in a few microseconds, so
+# what they cost is what the host takes. Each has its checks in one expression
+# (a decode over a shared prefix: 20.3 -> 17.4 us of the host's time a call); only
+# a call that fails it goes through them one by one, to the error.
+
+_NOT_FINE = (AttributeError, IndexError, TypeError, ValueError)
+
+
+def _check_rows(name, t, rows, width, device):
+    """`t` is bf16 [rows, width], columns contiguous, rows a multiple of 8 elements apart."""
     import torch
     if _device_of(name, t) != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
@@ -876,28 +884,47 @@ def _rows(name, t, rows, width, device):
     if t.shape != (rows, width) or t.stride(1) != 1:
         raise ValueError(f"{name} must be [{rows}, {width}], a row for each slot, with "
                          "contiguous columns")
-    stride = t.stride(0) if rows > 1 else width
-    if stride % 8:
-        raise ValueError(f"{name}'s rows must lie a multiple of 8 elements apart, not {stride}")
-    return t.data_ptr(), stride
+    if rows > 1 and t.stride(0) % 8:
+        raise ValueError(f"{name}'s rows must lie a multiple of 8 elements apart, not {t.stride(0)}")
 
 
-def _cache_write(fn, cache_dtype, kv_c, k_pe, slot_mapping, latent_cache, k_scale, workspace, stream):
+def _check_write(cache_dtype, kv_c, k_pe, slot_mapping, latent_cache, workspace):
     import torch
     dev = _device_of("latent_cache", latent_cache)
     blocks = _ndim("latent_cache", latent_cache, 3, "[num_blocks, 64, 576]")[0]
     T = _ndim("slot_mapping", slot_mapping, 1, "[T]")[0]
-    kv_ptr, kv_stride = _rows("kv_c", kv_c, T, KV_LORA_RANK, dev)
-    pe_ptr, pe_stride = _rows("k_pe", k_pe, T, ROPE_DIM, dev)
-    cache_ptr = _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM))
-    slots_ptr = _arg("slot_mapping", slot_mapping, torch.int64, dev)
-    ws_ptr = _arg("workspace", workspace, torch.uint8, dev)
-    if k_scale is None:
-        _call(dev, stream, fn, kv_ptr, kv_stride, pe_ptr, pe_stride, slots_ptr, T, cache_ptr,
-              blocks, ws_ptr, workspace.numel())
-    else:
-        _call(dev, stream, fn, kv_ptr, kv_stride, pe_ptr, pe_stride, slots_ptr, T, float(k_scale),
-              cache_ptr, blocks, ws_ptr, workspace.numel())
+    _check_rows("kv_c", kv_c, T, KV_LORA_RANK, dev)
+    _check_rows("k_pe", k_pe, T, ROPE_DIM, dev)
+    _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM))
+    _arg("slot_mapping", slot_mapping, torch.int64, dev)
+    _arg("workspace", workspace, torch.uint8, dev)
+
+
+def _cache_write(fn, cache_dtype, kv_c, k_pe, slot_mapping, latent_cache, scales, workspace, stream):
+    import torch
+    bf16 = torch.bfloat16
+    try:
+        dev, shape, T = latent_cache.device, latent_cache.shape, slot_mapping.shape[0]
+        fine = (latent_cache.is_cuda and latent_cache.dtype is cache_dtype
+                and shape == (shape[0], PAGE_SIZE, HEAD_DIM) and latent_cache.is_contiguous()
+                and slot_mapping.dtype is torch.int64 and slot_mapping.device == dev
+                and slot_mapping.shape == (T,) and slot_mapping.is_contiguous()
+                and kv_c.dtype is bf16 and kv_c.device == dev and kv_c.shape == (T, KV_LORA_RANK)
+                and k_pe.dtype is bf16 and k_pe.device == dev and k_pe.shape == (T, ROPE_DIM)
+                and workspace.dtype is torch.uint8 and workspace.device == dev
+                and workspace.is_contiguous())
+        if fine:
+            (kv_stride, kv_inner), (pe_stride, pe_inner) = kv_c.stride(), k_pe.stride()
+            fine = kv_inner == 1 and pe_inner == 1 and (T == 1 or not (kv_stride | pe_stride) & 7)
+    except _NOT_FINE:
+        fine = False
+    if not fine:
+        _check_write(cache_dtype, kv_c, k_pe, slot_mapping, latent_cache, workspace)
+    if T <= 1:                          # (the distance of rows means nothing)
+        kv_stride, pe_stride = KV_LORA_RANK, ROPE_DIM
+    _call(dev, stream, fn, kv_c.data_ptr(), kv_stride, k_pe.data_ptr(), pe_stride,
+          slot_mapping.data_ptr(), T, *scales, latent_cache.data_ptr(), shape[0],
+          workspace.data_ptr(), workspace.numel())
     return latent_cache
 
 
@@ -907,7 +934,7 @@ def mla_cache_write(kv_c, k_pe, slot_mapping, latent_cache, *, workspace, stream
     (int64 ``[T]``; negative: none) of ``latent_cache``, which is returned."""
     import torch
     return _cache_write(load_library().mla_cache_write, torch.bfloat16, kv_c, k_pe, slot_mapping,
-                        latent_cache, None, workspace, stream)
+                        latent_cache, (), workspace, stream)
 
 
 def mla_cache_write_fp8(kv_c, k_pe, slot_mapping, latent_cache_fp8, k_scale, *, workspace,
@@ -916,30 +943,55 @@ def mla_cache_write_fp8(kv_c, k_pe, slot_mapping, latent_cache_fp8, k_scale, *, 
     the entries divided by ``k_scale``, saturating at +-448."""
     import torch
     return _cache_write(load_library().mla_cache_write_fp8, torch.uint8, kv_c, k_pe, slot_mapping,
-                        latent_cache_fp8, k_scale, workspace, stream)
+                        latent_cache_fp8, (float(k_scale),), workspace, stream)
 
 
-def _cache_gather(fn, cache_dtype, latent_cache, block_table, cu_seqlens_k, k_scale, total_k,
-                  first_token, rows, workspace, stream):
+def _check_gather(cache_dtype, latent_cache, block_table, cu_seqlens_k, total_k, first_token,
+                  workspace):
     import torch
     i32 = torch.int32
     dev = _device_of("latent_cache", latent_cache)
     blocks = _ndim("latent_cache", latent_cache, 3, "[num_blocks, 64, 576]")[0]
     B = _ndim("cu_seqlens_k", cu_seqlens_k, 1, "[B + 1]")[0] - 1
     _, mb = _ndim("block_table", block_table, 2, "[B, max_blocks_per_seq]")
-    T = int(total_k)
     if B < 0:
         raise ValueError("cu_seqlens_k must be [B + 1]")
-    if T < 0:
+    if total_k < 0:
         raise ValueError("total_k must not be negative")
+    _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM))
+    _arg("block_table", block_table, i32, dev, (B, mb))
+    if first_token is not None:
+        _arg("first_token", first_token, i32, dev, (B,))
+    _arg("cu_seqlens_k", cu_seqlens_k, i32, dev)
+    _arg("workspace", workspace, torch.uint8, dev)
+
+
+def _cache_gather(fn, cache_dtype, latent_cache, block_table, cu_seqlens_k, scales, total_k,
+                  first_token, rows, workspace, stream):
+    import torch
+    i32, T = torch.int32, int(total_k)
+    try:
+        dev, shape, (B, mb) = latent_cache.device, latent_cache.shape, block_table.shape
+        fine = (latent_cache.is_cuda and latent_cache.dtype is cache_dtype
+                and shape == (shape[0], PAGE_SIZE, HEAD_DIM) and latent_cache.is_contiguous()
+                and block_table.dtype is i32 and block_table.device == dev
+                and block_table.is_contiguous() and cu_seqlens_k.dtype is i32
+                and cu_seqlens_k.device == dev and cu_seqlens_k.shape == (B + 1,)
+                and cu_seqlens_k.is_contiguous()
+                and (first_token is None or first_token.dtype is i32
+                     and first_token.device == dev and first_token.shape == (B,)
+                     and first_token.is_contiguous())
+                and workspace.dtype is torch.uint8 and workspace.device == dev
+                and workspace.is_contiguous() and T >= 0)
+    except _NOT_FINE:
+        fine = False
+    if not fine:
+        _check_gather(cache_dtype, latent_cache, block_table, cu_seqlens_k, T, first_token,
+                      workspace)
     rows, rows_ptr = _result("rows", rows, (T, HEAD_DIM), torch.bfloat16, dev, stream)
-    _call(dev, stream, fn,
-          _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM)),
-          *(() if k_scale is None else (float(k_scale),)), blocks,
-          _arg("block_table", block_table, i32, dev, (B, mb)), mb,
-          None if first_token is None else _arg("first_token", first_token, i32, dev, (B,)),
-          _arg("cu_seqlens_k", cu_seqlens_k, i32, dev), B, T, rows_ptr,
-          _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
+    _call(dev, stream, fn, latent_cache.data_ptr(), *scales, shape[0], block_table.data_ptr(), mb,
+          None if first_token is None else first_token.data_ptr(), cu_seqlens_k.data_ptr(), B, T,
+          rows_ptr, workspace.data_ptr(), workspace.numel())
     return rows
 
 
@@ -950,7 +1002,7 @@ def mla_cache_gather(latent_cache, block_table, cu_seqlens_k, *, total_k, worksp
     576]``; rows from ``cu_seqlens_k[B]`` on are not written."""
     import torch
     return _cache_gather(load_library().mla_cache_gather, torch.bfloat16, latent_cache, block_table,
-                         cu_seqlens_k, None, total_k, first_token, rows, workspace, stream)
+                         cu_seqlens_k, (), total_k, first_token, rows, workspace, stream)
 
 
 def mla_cache_gather_fp8(latent_cache_fp8, block_table, cu_seqlens_k, k_scale, *, total_k,
@@ -958,8 +1010,8 @@ def mla_cache_gather_fp8(latent_cache_fp8, block_table, cu_seqlens_k, k_scale, *
     """``mla_cache_gather`` over an fp8 cache (uint8 E4M3 codes, per-tensor ``k_scale``)."""
     import torch
     return _cache_gather(load_library().mla_cache_gather_fp8, torch.uint8, latent_cache_fp8,
-                         block_table, cu_seqlens_k, k_scale, total_k, first_token, rows, workspace,
-                         stream)
+                         block_table, cu_seqlens_k, (float(k_scale),), total_k, first_token, rows,
+                         workspace, stream)
 
 
 def make_span_plan(batch, num_heads, max_blocks_per_seq, *, max_groups=0, num_sms=None,
@@ -977,31 +1029,63 @@ def make_span_plan(batch, num_heads, max_blocks_per_seq, *, max_groups=0, num_sm
     return plan
 
 
-def _decode_span(fn, cache_dtype, q, latent_cache, block_table, seq_lens, middle, groups, scales,
-                 plan, out, lse, return_lse, workspace, stream):
-    """One of the decodes over parts of the tokens; `middle` are the arguments
-    between the lengths and the scales (tensors as (name, tensor, shape))."""
+def _check_span(cache_dtype, q, latent_cache, block_table, seq_lens, groups, plan):
     import torch
     i32 = torch.int32
     dev = _device_of("q", q)
     B, N, _ = _ndim("q", q, 3, "[B, N, 576]")
     blocks = _ndim("latent_cache", latent_cache, 3, "[num_blocks, 64, 576]")[0]
     mb = _ndim("block_table", block_table, 2, "[B, max_blocks_per_seq]")[1]
-    if plan is None:
-        plan = make_span_plan(B, N, mb, max_groups=groups, num_sms=torch.cuda.get_device_properties(
-            dev).multi_processor_count)
-    elif plan.batch != B or plan.num_heads != N or plan.max_blocks_per_seq != mb:
+    if plan is not None and (plan.batch, plan.num_heads, plan.max_blocks_per_seq) != (B, N, mb):
         raise ValueError(f"the plan is for (B, N, max_blocks_per_seq) = "
                          f"{plan.batch, plan.num_heads, plan.max_blocks_per_seq}, not {B, N, mb}")
-    elif groups > plan.max_groups:
-        raise ValueError(f"the plan is for up to {plan.max_groups} groups, not {groups}")
-    args = [_arg("q", q, torch.bfloat16, dev, (B, N, HEAD_DIM)),
-            _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM)),
-            blocks, _arg("block_table", block_table, i32, dev, (B, mb)),
-            _arg("seq_lens", seq_lens, i32, dev, (B,))]
-    for m in middle:
-        args.append(_arg(m[0], m[1], i32, dev, m[2]) if type(m) is tuple else m)
-    args.extend(scales)
+    _arg("q", q, torch.bfloat16, dev, (B, N, HEAD_DIM))
+    _arg("latent_cache", latent_cache, cache_dtype, dev, (blocks, PAGE_SIZE, HEAD_DIM))
+    _arg("block_table", block_table, i32, dev, (B, mb))
+    _arg("seq_lens", seq_lens, i32, dev, (B,))
+    if groups is not None:
+        group_starts, shared_lens = groups
+        G = _ndim("shared_lens", shared_lens, 1, "[groups]")[0]
+        if plan is not None and G > plan.max_groups:
+            raise ValueError(f"the plan is for up to {plan.max_groups} groups, not {G}")
+        _arg("group_starts", group_starts, i32, dev, (G + 1,))
+        _arg("shared_lens", shared_lens, i32, dev, (G,))
+
+
+def _decode_span(fn, cache_dtype, q, latent_cache, block_table, seq_lens, groups, window, scales,
+                 plan, out, lse, return_lse, workspace, stream):
+    """One of the decodes over parts of the tokens: `groups` (their starts and
+    shared lengths) or None, and else the window and the sinks."""
+    import torch
+    i32, G, middle = torch.int32, 0, window
+    try:
+        dev, (B, N, width), shape = q.device, q.shape, latent_cache.shape
+        mb = block_table.shape[1]
+        fine = (q.is_cuda and q.dtype is torch.bfloat16 and width == HEAD_DIM and q.is_contiguous()
+                and latent_cache.dtype is cache_dtype and latent_cache.device == dev
+                and shape == (shape[0], PAGE_SIZE, HEAD_DIM) and latent_cache.is_contiguous()
+                and block_table.dtype is i32 and block_table.device == dev
+                and block_table.shape == (B, mb) and block_table.is_contiguous()
+                and seq_lens.dtype is i32 and seq_lens.device == dev and seq_lens.shape == (B,)
+                and seq_lens.is_contiguous()
+                and (plan is None or plan.batch == B and plan.num_heads == N
+                     and plan.max_blocks_per_seq == mb))
+        if fine and groups is not None:
+            group_starts, shared_lens = groups
+            G = shared_lens.shape[0]
+            fine = (shared_lens.dtype is i32 and shared_lens.device == dev
+                    and shared_lens.shape == (G,) and shared_lens.is_contiguous()
+                    and group_starts.dtype is i32 and group_starts.device == dev
+                    and group_starts.shape == (G + 1,) and group_starts.is_contiguous()
+                    and (plan is None or G <= plan.max_groups))
+            middle = (group_starts.data_ptr(), shared_lens.data_ptr(), G)
+    except _NOT_FINE:
+        fine = False
+    if not fine:
+        _check_span(cache_dtype, q, latent_cache, block_table, seq_lens, groups, plan)
+    if plan is None:
+        plan = make_span_plan(B, N, mb, max_groups=G, num_sms=torch.cuda.get_device_properties(
+            dev).multi_processor_count)
     out, out_ptr = _result("out", out, (B, N, KV_LORA_RANK), torch.bfloat16, dev, stream)
     lse_ptr = None
     if lse is not None or return_lse:
@@ -1010,14 +1094,10 @@ def _decode_span(fn, cache_dtype, q, latent_cache, block_table, seq_lens, middle
         workspace = _empty((int(plan.workspace_bytes),), torch.uint8, dev, stream)
         _call(dev, stream, load_library().mla_workspace_init, workspace.data_ptr(),
               workspace.numel())
-    _call(dev, stream, fn, ctypes.byref(plan), *args, out_ptr, lse_ptr,
+    _call(dev, stream, fn, ctypes.byref(plan), q.data_ptr(), latent_cache.data_ptr(), shape[0],
+          block_table.data_ptr(), seq_lens.data_ptr(), *middle, *scales, out_ptr, lse_ptr,
           _arg("workspace", workspace, torch.uint8, dev), workspace.numel())
     return out, lse
-
-
-def _groups(group_starts, shared_lens):
-    G = _ndim("shared_lens", shared_lens, 1, "[groups]")[0]
-    return G, (("group_starts", group_starts, (G + 1,)), ("shared_lens", shared_lens, (G,)), G)
 
 
 def mla_decode_shared(q, latent_cache, block_table, seq_lens, group_starts, shared_lens,
@@ -1029,10 +1109,9 @@ def mla_decode_shared(q, latent_cache, block_table, seq_lens, group_starts, shar
     once for the group's rows together. Returns ``(out bf16 [B, N, 512], lse
     fp32 [B, N] | None)``, as ``mla_decode`` would."""
     import torch
-    G, middle = _groups(group_starts, shared_lens)
     return _decode_span(load_library().mla_decode_shared, torch.bfloat16, q, latent_cache,
-                        block_table, seq_lens, middle, G, (float(softmax_scale),), plan, out, lse,
-                        return_lse, workspace, stream)
+                        block_table, seq_lens, (group_starts, shared_lens), None,
+                        (float(softmax_scale),), plan, out, lse, return_lse, workspace, stream)
 
 
 def mla_decode_shared_fp8(q, latent_cache_fp8, block_table, seq_lens, group_starts, shared_lens,
@@ -1040,10 +1119,10 @@ def mla_decode_shared_fp8(q, latent_cache_fp8, block_table, seq_lens, group_star
                           return_lse=True, workspace=None, stream=None):
     """``mla_decode_shared`` over an fp8 cache (uint8 E4M3 codes, per-tensor ``k_scale``)."""
     import torch
-    G, middle = _groups(group_starts, shared_lens)
     return _decode_span(load_library().mla_decode_shared_fp8, torch.uint8, q, latent_cache_fp8,
-                        block_table, seq_lens, middle, G, (float(softmax_scale), float(k_scale)),
-                        plan, out, lse, return_lse, workspace, stream)
+                        block_table, seq_lens, (group_starts, shared_lens), None,
+                        (float(softmax_scale), float(k_scale)), plan, out, lse, return_lse,
+                        workspace, stream)
 
 
 def _window(window, sinks):
@@ -1062,7 +1141,7 @@ def mla_decode_window(q, latent_cache, block_table, seq_lens, softmax_scale, *, 
     ``(out bf16 [B, N, 512], lse fp32 [B, N] | None)``."""
     import torch
     return _decode_span(load_library().mla_decode_window, torch.bfloat16, q, latent_cache,
-                        block_table, seq_lens, _window(window, sinks), 0,
+                        block_table, seq_lens, None, _window(window, sinks),
                         (float(softmax_scale),), plan, out, lse, return_lse, workspace, stream)
 
 
@@ -1072,7 +1151,7 @@ def mla_decode_window_fp8(q, latent_cache_fp8, block_table, seq_lens, softmax_sc
     """``mla_decode_window`` over an fp8 cache (uint8 E4M3 codes, per-tensor ``k_scale``)."""
     import torch
     return _decode_span(load_library().mla_decode_window_fp8, torch.uint8, q, latent_cache_fp8,
-                        block_table, seq_lens, _window(window, sinks), 0,
+                        block_table, seq_lens, None, _window(window, sinks),
                         (float(softmax_scale), float(k_scale)), plan, out, lse, return_lse,
                         workspace, stream)
 
