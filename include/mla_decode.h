@@ -825,15 +825,16 @@ int mla_span_plan(int batch, int num_heads, int max_blocks_per_seq, int max_grou
  * mla_decode_shared -- mla_decode of a batch in which neighbouring requests
  * share a prefix (pages that mla_cache_fork shares): the prefix is attended to
  * once for all rows of a group, 128 at a time, the rest request by request,
- * and the parts are merged (fp32). Requests group_starts[g] ..
+ * and the parts are merged (fp32), where that is the faster way. Requests group_starts[g] ..
  * group_starts[g + 1] - 1 are group g; their first shared_lens[g] tokens are
  * the same. Of these the whole pages are shared, read through the block-table
  * row of the group's first request that has tokens, as far as its shortest
  * request that has any reaches; all other tokens (the rest of the prefix,
  * requests in no group) are read through each request's own row. out and lse
  * are those of mla_decode, whatever the groups. A group whose rows would fill
- * no fewer tiles together than one by one (128 heads, one member) is decoded
- * request by request.
+ * no fewer tiles together than one by one (128 heads, one member), and a batch
+ * whose groups would save less than two steps of 128 tokens for every CTA pair,
+ * is decoded request by request, every token through its request's own row.
  *
  *   group_starts   device, int32 [num_groups + 1], not decreasing, within
  *                  [0, B]; else MLA_ERR_BAD_ROW is recorded and nothing shared.

@@ -39,6 +39,7 @@ struct SpanScratch {
     int32_t group_unit0[kSpanMaxBatch];       // where their units begin
     int32_t leader[kSpanMaxBatch];            // its first member with tokens
     int32_t shared[kSpanMaxBatch];
+    int32_t saved;                            // the units that sharing saves
 };
 
 __device__ __forceinline__ int4 operator+(int4 a, int4 b) {
@@ -107,6 +108,7 @@ __device__ __forceinline__ void span_schedule(const SpanParams& p, SpanScratch& 
     if (tid == 0) {
         range->first = range->end = 0;
         range->g0 = range->g1 = 0;
+        s.saved = 0;
     }
     // Lengths and groups, read together; groups only if their starts make sense:
     // not decreasing, within the batch.
@@ -153,17 +155,19 @@ __device__ __forceinline__ void span_schedule(const SpanParams& p, SpanScratch& 
             const int tiles = (members * p.heads + kSpanRows - 1) / kSpanRows;
             // Worth it where a tile holds the rows of several requests: the
             // steps that this saves against the tiles' fixed cost.
-            s.pages[g] =
-                int64_t(members - tiles) * span_steps(pg) > int64_t(tiles) * kSpanItemCost ? pg : 0;
+            const int saved = (members - tiles) * span_steps(pg) - tiles * kSpanItemCost;
+            s.pages[g] = saved > 0 ? pg : 0;
+            if (saved > 0) atomicAdd(&s.saved, saved);
         }
         __syncthreads();
+        if (s.saved < kSpanShareGain * p.pairs) G = 0;
     }
 
     // A request's own item, but for its place.
     auto own_item = [&](int b) {
         SpanItem it{};
         const int L = s.lens[b], g = s.req_group[b];
-        const int shared = g >= 0 && L > 0 ? s.pages[g] : 0;
+        const int shared = G > 0 && g >= 0 && L > 0 ? s.pages[g] : 0;
         it.row0 = b * p.heads;
         it.rows = p.heads;
         it.table_row = b;
@@ -292,7 +296,7 @@ __device__ __forceinline__ void span_schedule(const SpanParams& p, SpanScratch& 
     if (first_cta)
         for (int b = tid; b < B; b += threads) {
             const int g = s.req_group[b];
-            p.tile_row[b] = g >= 0 && s.pages[g] > 0 && s.lens[b] > 0
+            p.tile_row[b] = G > 0 && g >= 0 && s.pages[g] > 0 && s.lens[b] > 0
                                 ? s.tile0[g] * kSpanRows + (b - s.starts[g]) * p.heads
                                 : -1;
             p.own_item[b] =
