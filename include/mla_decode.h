@@ -814,7 +814,9 @@ typedef struct mla_span_plan {
 } mla_span_plan_t;
 
 /*
- * mla_span_plan -- size the workspace. Host only. flags: 0 (or
+ * mla_span_plan -- size the workspace. Host only; MLA_ERR_UNSUPPORTED beyond the
+ * sizes above, and where batch * (max_blocks_per_seq + 6) passes 2^31 - 1 (a
+ * block table of 8 GB). flags: 0 (or
  * MLA_PLAN_DEBUG_WITHHOLD_LOAD, tests only: the first CTA withholds a load, so
  * that a wait for it runs out after 2 ms).
  */

@@ -88,6 +88,7 @@ def test_an_empty_batch_needs_no_tensors(lib):
     (dict(extra_flags=1), BAD), (dict(heads=129), binding.MLA_ERR_UNSUPPORTED),
     (dict(batch=4097), binding.MLA_ERR_UNSUPPORTED), (dict(groups=4097), binding.MLA_ERR_UNSUPPORTED),
     (dict(mb=2 ** 31 - 1), binding.MLA_ERR_UNSUPPORTED),
+    (dict(batch=4096, mb=2 ** 19 - 6), binding.MLA_ERR_UNSUPPORTED),
 ])
 def test_plan_refusals(lib, kw, code):
     with pytest.raises(binding.MlaError) as e:

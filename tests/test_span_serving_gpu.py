@@ -145,3 +145,46 @@ def test_forked_requests_step_by_step(fp8):
         got = bf16_tensor_bits(s.rows)
         assert np.array_equal(got[:cu[-1]], want[:cu[-1]])
         assert not got[cu[-1]:].any()      # rows behind the last request are left as they were
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_calls_behind_one_another_without_a_wait(fp8):
+    """Each call's queries and lengths are written by kernels right in front of
+    it, its results read by one right behind it, all over the same tensors."""
+    import torch
+    rng = np.random.default_rng(5)
+    B, N, M, turns = 6, 16, 9, 24
+    host = f32_to_bf16_bits(rng.standard_normal((B * M, 64, 576)).astype(np.float32))
+    if fp8:
+        host = e4m3_codes(bf16_bits_to_f64(host), K_SCALE)
+    cache, table = dev(host), rng.permutation(B * M).reshape(B, M).astype(np.int32)
+    table[1:3, :4] = table[0, :4]                       # 256 tokens together
+    queries = [random_q(rng, B, N) for _ in range(turns)]
+    lens = [np.concatenate([rng.integers(256, 576, 3), rng.integers(0, 576, 3)]) for _ in range(turns)]
+    d_q, d_l = torch.stack([dev(q) for q in queries]), torch.stack([ints(n) for n in lens])
+    plan = binding.make_span_plan(B, N, M, max_groups=1, num_sms=4)
+    ws = binding.new_workspace(plan)
+    q, length = d_q[0].clone(), d_l[0].clone()
+    out = torch.empty((B, N, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((B, N), dtype=torch.float32, device="cuda")
+    got = torch.empty((2, turns, B, N, 512), dtype=torch.bfloat16, device="cuda")
+    got_lse = torch.empty((2, turns, B, N), dtype=torch.float32, device="cuda")
+    starts, shared, d_table = ints([0, 3]), ints([256]), ints(table)
+    scale, tail = ((SCALE, K_SCALE), "_fp8") if fp8 else ((SCALE,), "")
+    load = torch.ones((2048, 2048), device="cuda")
+    kw = dict(plan=plan, workspace=ws, out=out, lse=lse)
+    torch.cuda.synchronize()
+    for i in range(turns):
+        (load @ load)                                   # the kernels behind it queue up
+        q.copy_(d_q[i]), length.copy_(d_l[i])
+        getattr(binding, "mla_decode_shared" + tail)(q, cache, d_table, length, starts, shared, *scale, **kw)
+        got[0, i].copy_(out), got_lse[0, i].copy_(lse)
+        getattr(binding, "mla_decode_window" + tail)(q, cache, d_table, length, *scale, window=130, sinks=3, **kw)
+        got[1, i].copy_(out), got_lse[1, i].copy_(lse)
+    torch.cuda.synchronize()
+    assert binding.read_error(ws) == 0
+    for i in range(turns):
+        seen = [np.arange(n) for n in lens[i]]
+        part = [t[(t < 3) | (t >= n - 130)] for t, n in zip(seen, lens[i])]
+        for k, s in enumerate((seen, part)):
+            check(got[k, i], got_lse[k, i], reference(queries[i], host, table, s, SCALE), (k, i))

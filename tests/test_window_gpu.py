@@ -6,7 +6,7 @@ import pytest
 from mla_latent_cache_paged_gb300 import binding
 from mla_latent_cache_paged_gb300.workloads import bf16_bits_to_f64, bf16_tensor_bits
 from oracle import mla_decode_window_reference
-from span_util import (NAN, SCALE, check, random_cache, random_q, reference, run_window, values)
+from span_util import (K_SCALE, NAN, SCALE, check, dev, ints, random_cache, random_q, reference, run_window, values)
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +152,72 @@ def test_pages_past_two_to_the_31():
         torch.cuda.synchronize()
         check(out, lse, reference(q, small, np.array([[0, 1, 2]]), _seen(lens, 140, 2), SCALE))
         del pool
+
+
+def test_replays_with_other_lengths_at_the_same_time():
+    """Two captured calls, a workspace each, replayed together on two streams."""
+    import torch
+    rng = np.random.default_rng(8)
+    B, N, M, window, sinks = 5, 16, 12, 200, 66
+    calls = []
+    for k in range(2):
+        plan = binding.make_span_plan(B, N, M)
+        c = dict(plan=plan, ws=binding.new_workspace(plan), stream=torch.cuda.Stream(),
+                 q=torch.zeros((B, N, 576), dtype=torch.bfloat16, device="cuda"),
+                 table=torch.zeros((B, M), dtype=torch.int32, device="cuda"), lens=ints([0] * B),
+                 out=torch.empty((B, N, 512), dtype=torch.bfloat16, device="cuda"),
+                 lse=torch.empty((B, N), dtype=torch.float32, device="cuda"))
+        calls.append(c)
+    host = random_cache(rng, B * M, False)
+    cache = dev(host)
+
+    def call(c):
+        binding.mla_decode_window(c["q"], cache, c["table"], c["lens"], SCALE, window=window, sinks=sinks,
+                                  plan=c["plan"], workspace=c["ws"], out=c["out"], lse=c["lse"])
+
+    for c in calls:
+        call(c)
+        torch.cuda.synchronize()
+        c["graph"] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(c["graph"]):
+            call(c)
+    for turn in range(3):
+        refs = []
+        for c in calls:
+            lens, q = rng.integers(0, 64 * M + 1, B), random_q(rng, B, N)
+            table = rng.permutation(B * M).reshape(B, M)
+            c["q"].copy_(dev(q)), c["lens"].copy_(ints(lens)), c["table"].copy_(ints(table))
+            refs.append(reference(q, host, table, _seen(lens, window, sinks), SCALE))
+        torch.cuda.synchronize()
+        for c in calls:
+            with torch.cuda.stream(c["stream"]):
+                c["graph"].replay()
+        torch.cuda.synchronize()
+        for c, ref in zip(calls, refs):
+            assert binding.read_error(c["ws"]) == 0
+            check(c["out"], c["lse"], ref, turn)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_wait_that_runs_out_is_reported(fp8):
+    """The first CTA withholds a load: the wait for it runs out, the kernel
+    drains and returns, and the workspace serves the next call."""
+    import torch
+    rng = np.random.default_rng(3)
+    lens, window, sinks = [900, 40, 300], 400, 10
+    host, table = random_cache(rng, 30, fp8), rng.permutation(30).reshape(2, 15)
+    table = np.concatenate([table, table[:1, ::-1]])
+    q = random_q(rng, 3, 16)
+    bad = binding.make_span_plan(3, 16, 15, num_sms=4, extra_flags=binding.MLA_PLAN_DEBUG_WITHHOLD_LOAD)
+    plan = binding.make_span_plan(3, 16, 15, num_sms=4)
+    ws = binding.new_workspace(plan)
+    for p, status in ((bad, binding.MLA_ERR_TIMEOUT), (plan, 0)):
+        args = (dev(q), dev(host), ints(table), ints(lens), SCALE)
+        if fp8:
+            out, lse = binding.mla_decode_window_fp8(*args, K_SCALE, window=window, sinks=sinks, plan=p,
+                                                     workspace=ws)
+        else:
+            out, lse = binding.mla_decode_window(*args, window=window, sinks=sinks, plan=p, workspace=ws)
+        torch.cuda.synchronize()
+        assert binding.read_error(ws) == status
+    check(out, lse, reference(q, host, table, _seen(lens, window, sinks), SCALE))
