@@ -44,9 +44,9 @@
 // a prefix of 16,384 tokens and 100 to 1,500 of their own (308 GFLOP) 204 us,
 // 1,510 TFLOP/s; a step takes some 2,900 cycles, of which the MMAs need 2,176;
 // the operands that they read and the tiles that TMA writes take shared memory
-// for 2,750 (128 bytes a cycle). With an fp8 cache a step takes 3,850 to 4,150:
-// the codes' way through registers, and the softmax beside it (its warps share
-// the issue slots with the thirteen); 64 requests of 32 heads over two prefixes of
+// for 2,750 (128 bytes a cycle). With an fp8 cache a step takes some 3,800: the
+// same port, with 1,886 for the operands and 1,900 for the codes' way through L1
+// and registers and the weights; 64 requests of 32 heads over two prefixes of
 // 8,000 to 12,000 tokens 73.5 us. 128 requests of 128 heads through a window of
 // 1,024 tokens (177 MB) 57 us; small batches take 15 to 16 us: the schedule (2 to
 // 3), the first page (2), a step or two, results (2), the merge (3).
@@ -393,9 +393,9 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, bool& big) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Each of thirteen warps has one 64-column block of every step (a page's
-// eight, the RoPE block, four of the other page's value blocks): it holds the
-// block's codes in registers, loaded while the slot was still in use, and
+// Each of thirteen warps has a part as large as a 64-column block of every step (a
+// page's eight, the RoPE block, four of the other page's value blocks): it holds
+// the part's codes in registers, loaded while the slot was still in use, and
 // widens them into the slot when that is free, so that between one use of a
 // slot and the next there is no load, only the conversion. (Six warps that
 // loaded codes into the slot by TMA and widened them in place: 6,500 cycles a
@@ -420,36 +420,65 @@ struct Widener {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster(to);
     }
-    // 64 rows of 64 codes from row y of the cache, columns 64 kb ..; zeros for
-    // a page that is not there (y < 0).
-    __device__ __forceinline__ void load(int32_t y, int kb, uint4 (&v)[8]) const {
+    // A warp's codes of a page: 32 rows of 128 (two blocks), or 64 rows of 64
+    // (the RoPE block). 16 codes a lane and load: a load of two blocks touches six
+    // lines of 128 bytes; one of a block's rows, 576 bytes apart, eight (96 requests
+    // of 32 heads through a window of 4,000 tokens: 63.7 us against 66.4).
+    struct Part {
+        int row, step;       // the lane's first row, and rows from one load to the next
+        int column;          // and its first column
+        int to;              // bytes from the first slot to the row's in its block
+        int first, second;   // its two 16-byte pieces there (swizzled)
+        int flip;            // what the swizzle does to them in every second load
+        bool swapped;        // it stores the second one first (no bank conflicts)
+    };
+    __device__ __forceinline__ Part part(bool two, int half, int column) const {
+        Part q;
+        const int c = two ? lane & 7 : lane & 3;
+        q.row = two ? 32 * half + (lane >> 3) : lane >> 2;
+        q.step = two ? 4 : 8;
+        q.column = column + 16 * c;
+        q.to = (c >> 2) * kBlock + q.row * 128;
+        q.swapped = c >= 4;
+        const int piece = 2 * (c & 3) + (q.swapped ? 1 : 0);
+        q.first = (piece ^ (q.row & 7)) * 16;
+        q.second = q.first ^ 16;
+        q.flip = two ? 64 : 0;
+        return q;
+    }
+    // From row y of the cache; zeros for a page that is not there (y < 0).
+    __device__ __forceinline__ void load(int32_t y, const Part& q, uint4 (&v)[8]) const {
         const unsigned char* src = static_cast<const unsigned char*>(p.cache) +
-                                   (int64_t(y) + (lane >> 2)) * kD + 64 * kb + 16 * (lane & 3);
+                                   (int64_t(y) + q.row) * kD + q.column;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            v[k] = y >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + 8 * k * kD))
+            v[k] = y >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + k * q.step * kD))
                           : make_uint4(0, 0, 0, 0);
     }
     // Them as f16 in the swizzled layout.
-    __device__ __forceinline__ void store(const uint4 (&v)[8], int at) const {
-        const int r = lane >> 2, c = lane & 3;
-        unsigned char* row = smem + at + r * 128;
-        const int even = ((2 * c) ^ r) * 16, odd = ((2 * c + 1) ^ r) * 16;
+    __device__ __forceinline__ void store(const uint4 (&v)[8], const Part& q, int at) const {
+        unsigned char* row = smem + at + q.to;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const uint2 a = widen4(v[k].x), b = widen4(v[k].y);
-            const uint2 d = widen4(v[k].z), e = widen4(v[k].w);
-            *reinterpret_cast<uint4*>(row + k * 1024 + even) = make_uint4(a.x, a.y, b.x, b.y);
-            *reinterpret_cast<uint4*>(row + k * 1024 + odd) = make_uint4(d.x, d.y, e.x, e.y);
+            const uint32_t u0 = q.swapped ? v[k].z : v[k].x, u1 = q.swapped ? v[k].w : v[k].y;
+            const uint32_t u2 = q.swapped ? v[k].x : v[k].z, u3 = q.swapped ? v[k].y : v[k].w;
+            const uint2 a = widen4(u0), b = widen4(u1), d = widen4(u2), e = widen4(u3);
+            unsigned char* to = row + k * q.step * 128;
+            const int flip = (k & 1) ? q.flip : 0;
+            *reinterpret_cast<uint4*>(to + (q.first ^ flip)) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4*>(to + (q.second ^ flip)) = make_uint4(d.x, d.y, e.x, e.y);
         }
     }
 
-    // Warp w: block w (0 .. 7) of this CTA's page, 8: its RoPE block, 9 .. 12:
-    // block w - 9 of this CTA's value columns of the other page.
+    // Warps 2 g and 2 g + 1: half of the rows of blocks 2 g and 2 g + 1 (0 .. 7) of
+    // this CTA's page, 8: its RoPE block, 9 .. 12: likewise this CTA's value
+    // columns of the other page.
     __device__ __forceinline__ void blocks(const SpanRange* range, int pair, int w) const {
         const bool own = w <= 8;
-        const int kb = own ? w : 4 * rank + w - 9;
-        const int slot = own ? w : (rank == 0 ? 4 : 0) + w - 9;
+        const int two = own ? w >> 1 : (w - 9) >> 1;         // which two blocks
+        const int slot = 2 * two + (own || rank != 0 ? 0 : 4);
+        const Part q = part(w != 8, own ? w & 1 : (w - 9) & 1,
+                            own ? 128 * two : 256 * rank + 128 * two);
         const int side = own ? rank : 1 - rank;
         Steps s(range, pair);
         uint4 v[8];
@@ -457,7 +486,7 @@ struct Widener {
         int rows = 0, row0 = 0;
         uint32_t pieces = 0;
         int32_t y = -1;
-        if (more) load(page_row(p, s.pc.it, s.page() + side, w == 0), kb, v);
+        if (more) load(page_row(p, s.pc.it, s.page() + side, w == 0), q, v);
         for (int j = 0; more; ++j) {
             const int st = j & 1;
             const uint32_t ph = (j >> 1) & 1;
@@ -498,9 +527,9 @@ struct Widener {
                 to = ptx::map_to_rank(bar(offsetof(Bars, v_full)) + 8 * st, uint32_t(rank));
             }
             if (free_at != 0 && !until(free_at, free_ph, site)) return;
-            store(v, at);
+            store(v, q, at);
             done(to);
-            if (more) load(y, kb, v);
+            if (more) load(y, q, v);
         }
     }
     // An eighth of the queries, from bf16, in place.
