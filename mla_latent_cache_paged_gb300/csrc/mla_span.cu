@@ -499,10 +499,6 @@ struct Widener {
             more = s.next(p);
             first = more && s.first();
             if (more) y = page_row(p, s.pc.it, s.page() + side, w == 0);
-            if (w < 8 && begins) {
-                if (!until(bar(offsetof(Bars, q_staged)), pieces++ & 1, kSiteStaged)) return;
-                widen_queries(w, rows - rank * kCtaRows, row0);
-            }
             // (The stores are there once: the warps' code has to fit the
             // instruction caches.)
             uint32_t free_at = 0, free_ph = ph, to;
@@ -530,6 +526,11 @@ struct Widener {
             store(v, q, at);
             done(to);
             if (more) load(y, q, v);
+            // (The queries land after the codes, but for the first piece's.)
+            if (w < 8 && begins) {
+                if (!until(bar(offsetof(Bars, q_staged)), pieces++ & 1, kSiteStaged)) return;
+                widen_queries(w, rows - rank * kCtaRows, row0);
+            }
         }
     }
     // An eighth of the queries, from bf16, in place.
