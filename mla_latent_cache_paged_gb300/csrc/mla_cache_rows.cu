@@ -141,7 +141,7 @@ struct GatherParams {
     const int32_t* first;        // [B] or null
     const int32_t* cu;           // [B + 1]
     int batch, total;
-    float scale;
+    float scale, power;          // fp8: a code's value * scale * power (gather_scale)
     uint16_t* rows;              // bf16 [total, 576]
     int32_t* status;
 };
@@ -174,11 +174,42 @@ __device__ __forceinline__ int64_t find_slot(const GatherParams& p, int t) {
     return int64_t(page) * kPageSize + pos % kPageSize;
 }
 
-// Two codes times the scale as bf16, one rounding.
-__device__ __forceinline__ uint32_t scaled2(uint32_t codes16, float scale) {
+// A code's value has four significant bits, k_scale 24: their product does not
+// fit fp32, and rounded there it may become a tie between two bf16 numbers that
+// it was next to. A tie has at most nine significant bits, so this takes a
+// k_scale next to a ratio t / f with t <= 512 and f < 16, times a power of two.
+// Two such ratios are further apart than 2^-13 of them (512 * 15 < 2^13), so
+// k_scale is within 2^-15 of one at most, and all of its products that are that
+// near to a tie lie on the same side of theirs: above, below, or on it. So
+// gather_scale splits k_scale = scale * power, power = 2^k, and moves a scale
+// that is within 2^-15 of a ratio, but not the ratio itself, to 2^-14 beyond it
+// on its side, which takes no product past a tie. A product is then a tie (in
+// fp32 too) or at least 2^-15 of it away from one, and neither its rounding to
+// fp32 (2^-24) nor, for a result below 2^-126, that of its product with the
+// power (2^-150, where the least tie is 2^-134) brings it there: the rounding to
+// bf16 is that of the exact product.
+void gather_scale(float k_scale, GatherParams& p) {
+    int e = 0;
+    double m = 2. * std::frexp(double(k_scale), &e);      // k_scale = m * 2^(e - 1)
+    for (int f = 1; f < 16; f += 2) {
+        double v = m * f, power = 1.;        // (exact: 24 bits and 4)
+        while (v < 256.) v *= 2., power *= 2.;
+        const double t = std::nearbyint(v);
+        if (std::fabs(v - t) >= t * 0x1p-15) continue;
+        if (v != t) m = t / (f * power) * (v > t ? 1. + 0x1p-14 : 1. - 0x1p-14);
+        break;
+    }
+    p.scale = float(m);
+    p.power = float(std::ldexp(1., e - 1));
+}
+
+// Two codes times k_scale as bf16, rounded once.
+__device__ __forceinline__ uint32_t scaled2(uint32_t codes16, const GatherParams& p) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(codes16), __NV_E4M3);
-    const float2 f = __half22float2(__half2(h));
-    return pack_bf16(f.x * scale, f.y * scale);
+    const float2 f = __fmul2_rn(
+        __fmul2_rn(__half22float2(__half2(h)), make_float2(p.scale, p.scale)),
+        make_float2(p.power, p.power));
+    return pack_bf16(f.x, f.y);
 }
 
 template <bool kFp8, int kRounds>
@@ -213,8 +244,8 @@ __global__ void __launch_bounds__(kThreads) mla_cache_gather_kernel(const Gather
     for (int k = 0; k < kRounds; ++k) {
         if (slot[k] == kNoRow) continue;
         if constexpr (kFp8)
-            v[k] = make_uint4(scaled2(v[k].x & 0xffffu, p.scale), scaled2(v[k].x >> 16, p.scale),
-                              scaled2(v[k].y & 0xffffu, p.scale), scaled2(v[k].y >> 16, p.scale));
+            v[k] = make_uint4(scaled2(v[k].x & 0xffffu, p), scaled2(v[k].x >> 16, p),
+                              scaled2(v[k].y & 0xffffu, p), scaled2(v[k].y >> 16, p));
         *reinterpret_cast<uint4*>(p.rows + (t0 + r + k * kRowsAtOnce) * kD + 8 * c) = v[k];
     }
 }
@@ -259,10 +290,10 @@ int write(WriteParams p, float k_scale, int64_t num_blocks, void* workspace,
 }
 
 template <bool kFp8>
-int gather(GatherParams p, void* workspace, size_t workspace_bytes, void* stream) {
+int gather(GatherParams p, float k_scale, void* workspace, size_t workspace_bytes, void* stream) {
     if (p.batch < 0 || p.total < 0 || p.num_blocks < 1 || p.max_blocks < 1)
         return MLA_ERR_INVALID_ARG;
-    if (kFp8 && (!std::isfinite(p.scale) || !(p.scale > 0.f))) return MLA_ERR_INVALID_ARG;
+    if (kFp8 && (!std::isfinite(k_scale) || !(k_scale > 0.f))) return MLA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < kStatusBytes || !aligned(workspace, 256))
         return MLA_ERR_WORKSPACE;
     if (p.batch == 0 || p.total == 0) return MLA_OK;
@@ -271,6 +302,7 @@ int gather(GatherParams p, void* workspace, size_t workspace_bytes, void* stream
         !aligned(p.cu, 4) || (p.first && !aligned(p.first, 4)))
         return MLA_ERR_INVALID_ARG;
     p.status = static_cast<int32_t*>(workspace);
+    if (kFp8) gather_scale(k_scale, p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int rounds = p.total <= kFewRows ? kFewRounds : kManyRounds;
     const int per_cta = kRowsAtOnce * rounds;
@@ -295,12 +327,11 @@ WriteParams write_params(const void* kv_c, int64_t kv_stride, const void* k_pe, 
     return p;
 }
 
-GatherParams gather_params(const void* cache, float scale, int64_t num_blocks,
-                           const int32_t* table, int max_blocks, const int32_t* first,
-                           const int32_t* cu, int batch, int total, void* rows) {
+GatherParams gather_params(const void* cache, int64_t num_blocks, const int32_t* table,
+                           int max_blocks, const int32_t* first, const int32_t* cu, int batch,
+                           int total, void* rows) {
     GatherParams p{};
     p.cache = cache;
-    p.scale = scale;
     p.num_blocks = num_blocks;
     p.table = table;
     p.max_blocks = max_blocks;
@@ -341,9 +372,9 @@ extern "C" int mla_cache_gather(const void* latent_cache, int64_t num_blocks,
                                 const int32_t* first_token, const int32_t* cu_seqlens_k, int batch,
                                 int total_k, void* rows, void* workspace, size_t workspace_bytes,
                                 void* stream) {
-    return gather<false>(gather_params(latent_cache, 1.f, num_blocks, block_table,
-                                       max_blocks_per_seq, first_token, cu_seqlens_k, batch,
-                                       total_k, rows), workspace, workspace_bytes, stream);
+    return gather<false>(gather_params(latent_cache, num_blocks, block_table, max_blocks_per_seq,
+                                       first_token, cu_seqlens_k, batch, total_k, rows),
+                         1.f, workspace, workspace_bytes, stream);
 }
 
 extern "C" int mla_cache_gather_fp8(const void* latent_cache_fp8, float k_scale,
@@ -352,7 +383,8 @@ extern "C" int mla_cache_gather_fp8(const void* latent_cache_fp8, float k_scale,
                                     const int32_t* cu_seqlens_k, int batch, int total_k,
                                     void* rows, void* workspace, size_t workspace_bytes,
                                     void* stream) {
-    return gather<true>(gather_params(latent_cache_fp8, k_scale, num_blocks, block_table,
+    return gather<true>(gather_params(latent_cache_fp8, num_blocks, block_table,
                                       max_blocks_per_seq, first_token, cu_seqlens_k, batch,
-                                      total_k, rows), workspace, workspace_bytes, stream);
+                                      total_k, rows),
+                        k_scale, workspace, workspace_bytes, stream);
 }
