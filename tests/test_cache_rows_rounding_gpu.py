@@ -1,5 +1,6 @@
 """The roundings that the cache's row calls promise, bit for bit: a gathered
-fp8 row is k_scale times its codes' values rounded once to bf16."""
+fp8 row is k_scale times its codes' values rounded once to bf16, a written NaN
+is the code 0x7F."""
 
 import math
 
@@ -58,3 +59,17 @@ def test_gathered_rows_are_rounded_once(k_scale):
     assert ((got[nan] & 0x7FFF) > 0x7F80).all()
     want = _bf16_once(e4m3_to_float(np.where(nan, 0, codes)) * float(np.float32(k_scale)))
     assert np.array_equal(got[~nan], want[~nan]), np.unique(codes[~nan][got[~nan] != want[~nan]])
+
+
+@pytest.mark.parametrize("k_scale", [1.0, 0.0123, 1e-30, 1e30])
+def test_a_nan_of_either_sign_is_written_as_0x7f(k_scale):
+    import torch
+    bits = np.array([0x7F81, 0x7FC0, 0x7FFF, 0xFF81, 0xFFC0, 0xFFFF], np.uint16)
+    rows = torch.from_numpy(np.resize(bits, (5, 576)).view(np.int16)).view(torch.bfloat16).cuda()
+    cache = torch.zeros((1, 64, 576), dtype=torch.uint8, device="cuda")
+    ws = binding.new_status_workspace()
+    binding.mla_cache_write_fp8(rows[:, :512], rows[:, 512:], torch.arange(5, device="cuda"), cache, k_scale,
+                                workspace=ws)
+    torch.cuda.synchronize()
+    assert binding.read_error(ws) == 0
+    assert (cache[0, :5] == 0x7F).all() and not cache[0, 5:].any()
