@@ -393,6 +393,14 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, bool& big) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// A query of that row is beyond f16. (A tile has its rows of requests without
+// tokens too: nothing is computed for them, and they may hold anything.)
+__device__ __noinline__ void range_error(const SpanParams& p, int row) {
+    const int b = row / p.heads, L = p.seq_lens[b];
+    if (L > 0 && int64_t(L) <= int64_t(p.max_blocks) * kPageSize)
+        record_error(p.status, MLA_ERR_RANGE, b);
+}
+
 // Each of thirteen warps has a part as large as a 64-column block of every step (a
 // page's eight, the RoPE block, four of the other page's value blocks): it holds
 // the part's codes in registers, loaded while the slot was still in use, and
@@ -529,23 +537,31 @@ struct Widener {
             // (The queries land after the codes, but for the first piece's.)
             if (w < 8 && begins) {
                 if (!until(bar(offsetof(Bars, q_staged)), pieces++ & 1, kSiteStaged)) return;
-                widen_queries(w, rows - rank * kCtaRows, row0);
+                widen_queries(w, rows - rank * kCtaRows, row0 + rank * kCtaRows);
             }
         }
     }
-    // An eighth of the queries, from bf16, in place.
+    // An eighth of the queries, from bf16, in place: 16-byte pieces of rows 4 w + lane / 8
+    // and 32 more, of each of the nine blocks.
     __device__ __forceinline__ void widen_queries(int w, int live, int row0) const {
-        bool big = false;
-#pragma unroll 2
-        for (int i = 32 * w + lane; i < 9 * kBlock / 16; i += 256) {
-            uint4* a = reinterpret_cast<uint4*>(smem + kOffQ) + i;
-            const uint4 v = *a;
-            bool b = false;
-            *a = make_uint4(bf16x2_to_f16x2(v.x, b), bf16x2_to_f16x2(v.y, b),
-                            bf16x2_to_f16x2(v.z, b), bf16x2_to_f16x2(v.w, b));
-            big = big || (b && ((i >> 3) & 63) < live);
+        bool big[2] = {false, false};
+#pragma unroll 1
+        for (int k = 0; k < 9; ++k) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint4* a = reinterpret_cast<uint4*>(smem + kOffQ + k * kBlock) + 32 * w + lane +
+                           256 * half;
+                const uint4 v = *a;
+                *a = make_uint4(
+                    bf16x2_to_f16x2(v.x, big[half]), bf16x2_to_f16x2(v.y, big[half]),
+                    bf16x2_to_f16x2(v.z, big[half]), bf16x2_to_f16x2(v.w, big[half]));
+            }
         }
-        if (big) record_error(p.status, MLA_ERR_RANGE, row0 / p.heads);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = 32 * half + 4 * w + (lane >> 3);
+            if (big[half] && r < live) range_error(p, row0 + r);
+        }
         done(ptx::map_to_rank(bar(offsetof(Bars, q_full)), 0));
     }
     // One thread: a piece's queries, when the scores of the piece before it have
