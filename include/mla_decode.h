@@ -220,8 +220,9 @@ int mla_decode(const mla_decode_plan_t* plan, const void* q, const void* latent_
  *                   16-byte aligned. 36,864 bytes per page.
  *   k_scale         finite, > 0.
  *   q               bf16 [B, N, 576]; every entry within +-65504 (the kernel
- *                   multiplies in f16, into which every E4M3 value and every
- *                   such bf16 value convert exactly; a larger entry is
+ *                   multiplies in f16, into which every E4M3 value converts
+ *                   exactly and every such bf16 value from 2^-17 up; up to
+ *                   2^-25 of a smaller one is lost; a larger entry is
  *                   recorded as MLA_ERR_RANGE, detail = its request).
  *   other arguments as for mla_decode.
  * The tensor cores take f16 operands (q, the widened cache entries and the
@@ -793,7 +794,9 @@ int mla_cache_gather_fp8(const void* latent_cache_fp8, float k_scale, int64_t nu
  * Decode over parts of the cached tokens: prefixes that several requests share,
  * or a window with sinks. The arithmetic and the arguments are those of
  * mla_decode and mla_decode_fp8 (softmax weights rounded to bf16, or to f16
- * with an fp8 cache, for the tensor cores; an fp8 cache's q within +-65504).
+ * with an fp8 cache, for the tensor cores; an fp8 cache's q within +-65504,
+ * and of a row's entries at most 2^-21 of its greatest is lost, however small
+ * that is: rows below 2^-4 are multiplied by a power of two first).
  *
  * A plan is plain data computed on the host from sizes alone; the lengths and
  * groups are read on the device, so a captured call can be replayed with

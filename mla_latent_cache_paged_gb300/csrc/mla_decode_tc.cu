@@ -188,7 +188,7 @@ __device__ __forceinline__ float2 unpack_x2(uint32_t w) {
     }
 }
 
-// Two bf16 q values (one 32-bit word) as two f16 (exact for |q| <= 65504;
+// Two bf16 q values (one 32-bit word) as two f16 (exact from 2^-17 to 65504;
 // `big` is set when a value lies beyond that).
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, bool& big) {
     const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
@@ -882,7 +882,7 @@ mla_decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap t
                     r32[4 * i + 3] = v.w;
                 }
                 if constexpr (kFp8) {
-                    // f16 operands: q widened exactly (bf16 -> f16)
+                    // f16 operands: q as f16 (exact from 2^-17 on)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) r32[i] = bf16x2_to_f16x2(r32[i], q_big);
                 }

@@ -82,7 +82,8 @@ constexpr int kOffP = kOffRope + kBlock;          // a block per page of the ste
 constexpr int kOffBar = kOffP + 2 * kBlock;       // 229,376
 constexpr int kOffSwap = kOffBar + 512;           // 2 x 128 floats that rows' halves exchange
 constexpr int kOffRange = kOffSwap + 2 * 128 * 4;
-constexpr int kSmemBytes = kOffRange + int(sizeof(SpanRange));
+constexpr int kOffScale = kOffRange + int(sizeof(SpanRange));   // fp8 cache: 2 x 64 rows' scales
+constexpr int kSmemBytes = kOffScale + 2 * kCtaRows * 4;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 static_assert(sizeof(SpanScratch) <= kOffBar, "the schedule is made where the operands go");
 
@@ -385,13 +386,26 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
     return h;
 }
 
-// Two bf16 as two f16 (exact for |v| <= 65504; `big` is set beyond that).
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, bool& big) {
-    const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
-    big = big || !(fabsf(lo) <= 65504.f) || !(fabsf(hi) <= 65504.f);
-    const __half2 v = __floats2half2_rn(lo, hi);
+// Two bf16 times a power of two as two f16.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float up = 1.f) {
+    const __half2 v = __floats2half2_rn(__uint_as_float(w << 16) * up,
+                                        __uint_as_float(w & 0xffff0000u) * up);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ uint4 bf16_to_f16(const uint4& v, float up = 1.f) {
+    return make_uint4(bf16x2_to_f16x2(v.x, up), bf16x2_to_f16x2(v.y, up),
+                      bf16x2_to_f16x2(v.z, up), bf16x2_to_f16x2(v.w, up));
+}
+
+// The greater magnitudes of two pairs of bf16 (a NaN is the greatest; signs mean
+// nothing).
+__device__ __forceinline__ uint32_t greater2(uint32_t m, uint32_t w) {
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+    return m;
+}
+
+// bf16 magnitudes: the greatest that f16 holds (65280), and 2^-4.
+constexpr uint32_t kGreatestF16 = 0x477f, kSmallRow = (127 - 4) << 7;
 
 // A query of that row is beyond f16. (A tile has its rows of requests without
 // tokens too: nothing is computed for them, and they may hold anything.)
@@ -536,31 +550,52 @@ struct Widener {
             if (more) load(y, q, v);
             // (The queries land after the codes, but for the first piece's.)
             if (w < 8 && begins) {
-                if (!until(bar(offsetof(Bars, q_staged)), pieces++ & 1, kSiteStaged)) return;
-                widen_queries(w, rows - rank * kCtaRows, row0 + rank * kCtaRows);
+                if (!until(bar(offsetof(Bars, q_staged)), pieces & 1, kSiteStaged)) return;
+                // (A range's pieces are of items one after another.)
+                widen_queries(w, rows - rank * kCtaRows, row0 + rank * kCtaRows,
+                              range->first + int(pieces++));
             }
         }
     }
     // An eighth of the queries, from bf16, in place: 16-byte pieces of rows 4 w + lane / 8
-    // and 32 more, of each of the nine blocks.
-    __device__ __forceinline__ void widen_queries(int w, int live, int row0) const {
-        bool big[2] = {false, false};
+    // and 32 more, of each of the nine blocks. f16 has all of a bf16 number's bits
+    // from 2^-17 to 65504 and loses 2^-25 at most of a smaller one, 2^-21 of a
+    // row's greatest if that is 2^-4 or more. A row of smaller ones is read
+    // again (the conversion above has rounded them) and multiplied by the power
+    // of two that brings its greatest to [2^14, 2^15), 2^126 at most; its scores are
+    // divided by that power (exactly, or to 2^-150, which the softmax scale makes
+    // 2^-22 of at most). Looking for such rows costs nothing here, and the branch
+    // for them in the softmax 1 us (64 requests of 32 heads over two prefixes 73.3
+    // us against 72.3, a window of 4,000 over 96 of them 64.2 against 63.0).
+    __device__ __forceinline__ void widen_queries(int w, int live, int row0, int item) const {
+        float* scales = reinterpret_cast<float*>(smem + kOffScale) + (item & 1) * kCtaRows;
 #pragma unroll 1
-        for (int k = 0; k < 9; ++k) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint4* a = reinterpret_cast<uint4*>(smem + kOffQ + k * kBlock) + 32 * w + lane +
-                           256 * half;
-                const uint4 v = *a;
-                *a = make_uint4(
-                    bf16x2_to_f16x2(v.x, big[half]), bf16x2_to_f16x2(v.y, big[half]),
-                    bf16x2_to_f16x2(v.z, big[half]), bf16x2_to_f16x2(v.w, big[half]));
-            }
-        }
-#pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int r = 32 * half + 4 * w + (lane >> 3);
-            if (big[half] && r < live) range_error(p, row0 + r);
+            uint4* a = reinterpret_cast<uint4*>(smem + kOffQ) + 8 * r + (lane & 7);
+            uint32_t m2 = 0;
+#pragma unroll 3
+            for (int k = 0; k < 9; ++k) {
+                const uint4 v = a[k * (kBlock / 16)];
+                m2 = greater2(greater2(greater2(greater2(m2, v.x), v.y), v.z), v.w);
+                a[k * (kBlock / 16)] = bf16_to_f16(v);
+            }
+            uint32_t m = max(m2 & 0x7fffu, (m2 >> 16) & 0x7fffu);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            int up = 0;
+            if (m != 0 && m < kSmallRow && r < live) {
+                up = min(127 + 14 - int(m >> 7), 126);
+                const uint16_t* q = p.q + int64_t(row0 + r) * kD + 8 * ((lane ^ r) & 7);
+#pragma unroll 1
+                for (int k = 0; k < 9; ++k)
+                    a[k * (kBlock / 16)] = bf16_to_f16(*reinterpret_cast<const uint4*>(q + 64 * k),
+                                                       __uint_as_float(uint32_t(127 + up) << 23));
+            }
+            if ((lane & 7) == 0) {
+                scales[r] = copysignf(__uint_as_float(uint32_t(127 - up) << 23), p.scale_log2);
+                if (m > kGreatestF16 && r < live) range_error(p, row0 + r);
+            }
         }
         done(ptx::map_to_rank(bar(offsetof(Bars, q_full)), 0));
     }
@@ -770,11 +805,21 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
             float m_ref = -INFINITY;   // log2 units
             float l_sum = 0.f;         // of the weights (for the LSE)
             float l_mma = 0.f;         // of the rounded ones (for the results)
+            // fp8 cache: what a row's scores are multiplied by first (widen_queries;
+            // negative with a negative softmax scale), and whether that is not 1 for a
+            // row of this warp. (Written before the queries were announced, which
+            // the scores waited for, and again with those of the second item after
+            // this one, whose queries land when this one's last weights have been
+            // announced.)
+            bool scaled = false;
+            const float* row_scale = reinterpret_cast<const float*>(smem + kOffScale) +
+                                     ((w.item - 1) & 1) * kCtaRows + r;
             for (int k = 0; k < pc.steps; ++k, ++j) {
                 const int st = j & 1;
                 const int v = kSpanStepPages * (pc.first + k);
                 const PageMask mine = page_mask(pc.it, v + f);
                 ok = ok && until(bar(offsetof(Bars, s_full)) + 8 * st, (j >> 1) & 1, kSiteQkDone);
+                if (kFp8 && k == 0) scaled = ok && __any_sync(0xffffffffu, *row_scale != 1.f);
                 // With an fp8 cache the scores are read twice, half of them at a
                 // time: its many warps leave 96 registers a thread.
                 constexpr int kPart = kFp8 ? 32 : 64;
@@ -787,9 +832,10 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
                         ptx::tmem_ld64(trow + kTmemS + uint32_t(st * 64), raw);
 #pragma unroll
                     for (int i = 0; i < kPart; ++i) x[i] = __uint_as_float(raw[i]);
-                    if (p.scale_log2 < 0.f) {
+                    if (kFp8 ? scaled : p.scale_log2 < 0.f) {
+                        const float by = kFp8 ? *row_scale : -1.f;
 #pragma unroll
-                        for (int i = 0; i < kPart; ++i) x[i] = -x[i];
+                        for (int i = 0; i < kPart; ++i) x[i] *= by;
                     }
                     if (!mine.all()) {
 #pragma unroll
