@@ -802,7 +802,7 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
             return __all_sync(0xffffffffu, wait(b, parity, bars, p.status, site, lim_dep));
         };
         while (ok && walk_next(p, w, pc)) {
-            float m_ref = -INFINITY;   // log2 units
+            float x_ref = -INFINITY;   // a score, before the scale
             float l_sum = 0.f;         // of the weights (for the LSE)
             float l_mma = 0.f;         // of the rounded ones (for the results)
             // fp8 cache: what a row's scores are multiplied by first (widen_queries;
@@ -854,28 +854,32 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
                         for (int i = 0; i < kPart; i += 2)
                             m4[(i >> 1) & 3] = ptx::fmax3(m4[(i >> 1) & 3], x[i], x[i + 1]);
                     }
-                    mx = ptx::fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * scale;
+                    mx = ptx::fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
                 }
                 float other;
                 exchange(mx, &other);
                 if (!ok) break;
-                const float m_new = fmaxf(m_ref, fmaxf(mx, other));
+                mx = fmaxf(mx, other);
                 float alpha = 1.f;
-                if (m_new > m_ref + kRescaleThreshold) {
-                    alpha = ptx::ex2(m_ref - m_new);
-                    m_ref = m_new;
+                if ((mx - x_ref) * scale > kRescaleThreshold) {
+                    alpha = ptx::ex2((x_ref - mx) * scale);
+                    x_ref = mx;
                 }
-                // A row that has seen no token yet keeps m_ref = -inf: its
-                // weights are 2^-inf = 0, not NaN.
-                const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+                // The reference is taken off the scores, not their products with the
+                // scale: rounded, the greatest product may lie above itself by more
+                // than a weight can be (from 2^27 on), or below. A row that has
+                // seen no token yet keeps x_ref = -inf: its weights are 2^-inf = 0,
+                // not NaN.
+                const float neg = x_ref == -INFINITY ? 0.f : -x_ref;
                 uint32_t pk[32];
                 float2 ls = make_float2(0.f, 0.f), lm = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const int at = (2 * i) % kPart;
                     if (kFp8 && at == 0) read_scores(2 * i);
-                    const float2 d = __ffma2_rn(make_float2(x[at], x[at + 1]),
-                                                make_float2(scale, scale), make_float2(neg, neg));
+                    const float2 d = __fmul2_rn(
+                        __fadd2_rn(make_float2(x[at], x[at + 1]), make_float2(neg, neg)),
+                        make_float2(scale, scale));
                     const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
                     ls = __fadd2_rn(ls, e);
                     if constexpr (kFp8) {
@@ -952,7 +956,7 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
             l_mma += other_mma;
             const float inv = l_mma == 0.f ? 0.f : p.v_scale / l_mma;
             // (a NaN comes through)
-            const float lse = l_sum == 0.f ? -INFINITY : (m_ref + log2f(l_sum)) * kLn2;
+            const float lse = l_sum == 0.f ? -INFINITY : (x_ref * scale + log2f(l_sum)) * kLn2;
             const int row = rank * kCtaRows + r;           // of the item
             const int64_t row0 = pc.part_row < 0 ? int64_t(pc.it.row0) : pc.part_row;
             // 128 bytes of a warp's 32 rows at a time, through the weights' place

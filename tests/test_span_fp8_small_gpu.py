@@ -10,6 +10,7 @@ import numpy as np
 import pytest
 
 from mla_latent_cache_paged_gb300 import binding
+from mla_latent_cache_paged_gb300.workloads import f32_to_bf16_bits
 from span_sharing import assert_shared
 from span_util import SCALE, check, random_q, reference, run_shared, run_window, shared_problem
 
@@ -40,3 +41,25 @@ def test_small_queries(exponent):
     assert binding.read_error(ws) == 0
     seen = [np.array([t for t in range(n) if t < 66 or t >= n - 300]) for n in lens]
     check(out, lse, reference(q, cache, table, seen, scale), exponent)
+
+
+def test_rows_of_very_different_sizes():
+    """Each row has its own power of two, piece after piece of a pair's work."""
+    import torch
+    rng = np.random.default_rng(41)
+    B, heads = 40, 12
+    lens = [int(x) for x in rng.integers(1, 700, B)]
+    cache, table = shared_problem(rng, lens, [0, B], [0], True)
+    gain = np.exp2(rng.integers(-40, 3, (B, heads, 1)).astype(np.float64))
+    q = f32_to_bf16_bits((rng.standard_normal((B, heads, 576)) * gain).astype(np.float32))
+    q[3], q[5, 2], q[7, :, 100:] = 0, 0x8000, 0
+    q[9, 4, :] = 0
+    q[9, 4, 17] = 0x477F                                    # 65280, alone in its row
+    q[11, 0, :] = 0x0003                                    # bf16's smallest numbers
+    for scale in (SCALE, -2.0 ** 20, 0.0):
+        for num_sms in (2, 14, 152):
+            out, lse, ws = run_window(q, cache, table, lens, 500, 3, scale, num_sms=num_sms)
+            torch.cuda.synchronize()
+            assert binding.read_error(ws) == 0
+            seen = [np.array([t for t in range(n) if t < 3 or t >= n - 500]) for n in lens]
+            check(out, lse, reference(q, cache, table, seen, scale), (scale, num_sms))
