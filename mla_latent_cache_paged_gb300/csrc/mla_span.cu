@@ -28,9 +28,10 @@
 // Softmax: a thread has 64 scores of a row; the two threads of a row exchange
 // their maxima through shared memory. fp32, base 2; the reference maximum moves
 // only when a step raises it by more than 8, so that results are seldom
-// rescaled. Weights are rounded to bf16 (f16 with an fp8 cache: half a step,
-// 2^-8 or 2^-11, of each weight) for the tensor cores; results are normalised
-// by the sum of the rounded weights, the LSE keeps the sum of the others.
+// rescaled. Weights are rounded to bf16 for the tensor cores, or to f16 with an
+// fp8 cache: by half a step, 2^-8 or 2^-11, of each weight, in f16 by up to 2^-32 of
+// the row's greatest. Results are normalised by the sum of the rounded weights,
+// the LSE keeps the sum of the others.
 //
 // What the weights' barrier announces to the first CTA's MMA thread lies in the
 // announcing SM: shared memory, written before a proxy fence and read by that
@@ -94,6 +95,10 @@ constexpr uint32_t kTmemO = 128;                  // 256 columns
 constexpr uint32_t kSuspendNs = 20000;
 constexpr uint16_t kBoth = 3;                     // the pair's CTAs
 constexpr float kRescaleThreshold = 8.f;          // log2 units
+// The weight of the reference (log2): f16 has no more than 2^-25 of a weight, 2^-32
+// of the greatest with this, and up to 2^15 of it. bf16 has fp32's range.
+template <bool kFp8>
+constexpr float kLift = kFp8 ? 7.f : 0.f;
 constexpr float kLn2 = 0.693147180559945309f;
 
 enum SpanSite : int32_t { kSiteQ = 70, kSiteK, kSiteRope, kSiteV, kSiteSlot, kSiteQkDone,
@@ -865,11 +870,10 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
                     alpha = ptx::ex2((x_ref - mx) * scale);
                     x_ref = mx;
                 }
-                // The reference is taken off the scores, not their products with the
-                // scale: rounded, the greatest product may lie above itself by more
-                // than a weight can be (from 2^27 on), or below. A row that has
-                // seen no token yet keeps x_ref = -inf: its weights are 2^-inf = 0,
-                // not NaN.
+                // The reference is taken off the scores, not off their products
+                // with the scale: beyond 2^27 a product's rounding is more than the
+                // exponents of the weights' type. A row that has seen no token
+                // yet keeps x_ref = -inf: its weights are 2^-inf = 0, not NaN.
                 const float neg = x_ref == -INFINITY ? 0.f : -x_ref;
                 uint32_t pk[32];
                 float2 ls = make_float2(0.f, 0.f), lm = make_float2(0.f, 0.f);
@@ -877,9 +881,10 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
                 for (int i = 0; i < 32; ++i) {
                     const int at = (2 * i) % kPart;
                     if (kFp8 && at == 0) read_scores(2 * i);
-                    const float2 d = __fmul2_rn(
-                        __fadd2_rn(make_float2(x[at], x[at + 1]), make_float2(neg, neg)),
-                        make_float2(scale, scale));
+                    const float2 a =
+                        __fadd2_rn(make_float2(x[at], x[at + 1]), make_float2(neg, neg));
+                    const float2 d = __ffma2_rn(a, make_float2(scale, scale),
+                                                make_float2(kLift<kFp8>, kLift<kFp8>));
                     const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
                     ls = __fadd2_rn(ls, e);
                     if constexpr (kFp8) {
@@ -956,7 +961,7 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
             l_mma += other_mma;
             const float inv = l_mma == 0.f ? 0.f : p.v_scale / l_mma;
             // (a NaN comes through)
-            const float lse = l_sum == 0.f ? -INFINITY : (x_ref * scale + log2f(l_sum)) * kLn2;
+            const float lse = l_sum == 0.f ? -INFINITY : (x_ref * scale + (log2f(l_sum) - kLift<kFp8>)) * kLn2;
             const int row = rank * kCtaRows + r;           // of the item
             const int64_t row0 = pc.part_row < 0 ? int64_t(pc.it.row0) : pc.part_row;
             // 128 bytes of a warp's 32 rows at a time, through the weights' place
