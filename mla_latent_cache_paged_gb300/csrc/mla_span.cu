@@ -630,10 +630,18 @@ struct Widener {
 
 // ------------------------------------------------------------ the kernel
 
+// The cache's tensor map. (An fp8 cache's codes are loaded by threads.)
+template <bool kFp8>
+struct CacheMap {
+    CUtensorMap map;
+};
+template <>
+struct CacheMap<true> {};
+
 template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
 mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
-                const __grid_constant__ CUtensorMap map_c) {
+                const __grid_constant__ CacheMap<kFp8> cache) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = ptx::smem_addr(smem);
     Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
@@ -689,21 +697,20 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
     const uint32_t tmem = bars->tmem_base;
     const uint64_t lim_mma = p.timeout_ns, lim_dep = 2 * p.timeout_ns;
 
-    if (!kFp8 && (warp == 0 || warp == 6)) {
-        if (ptx::elect_one()) {
-            const Loader l{p, &map_q, &map_c, bars, sbase, b0, rank, lim_dep};
+    if (warp == 0 || warp >= 6) {
+        if constexpr (kFp8) {
+            const Widener l{p, &map_q, bars, smem, sbase, b0, rank, lane, lim_dep};
+            if (warp >= 6)
+                l.blocks(range, pair, warp - 6);
+            else if (ptx::elect_one())
+                l.queries(range, pair);
+        } else if (ptx::elect_one()) {
+            const Loader l{p, &map_q, &cache.map, bars, sbase, b0, rank, lim_dep};
             if (warp == 0)
                 l.pages(range, pair);
             else
                 l.values(range, pair);
         }
-        __syncwarp();
-    } else if (kFp8 && (warp == 0 || warp >= 6)) {
-        const Widener l{p, &map_q, bars, smem, sbase, b0, rank, lane, lim_dep};
-        if (warp >= 6)
-            l.blocks(range, pair, warp - 6);
-        else if (ptx::elect_one())
-            l.queries(range, pair);
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && ptx::elect_one()) {
@@ -1032,22 +1039,13 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
 
 template <bool kFp8>
 int launch(const SpanParams& p, cudaStream_t st) {
-    CUtensorMap map_q, map_c;
+    CUtensorMap map_q;
+    CacheMap<kFp8> cache;
     if (!encode_2d(&map_q, p.q, kD, uint64_t(p.batch) * p.heads, kCtaRows))
         return int(cudaErrorInvalidValue);
-    const uint64_t rows = uint64_t(p.num_blocks) * kPageSize;
-    if constexpr (kFp8) {
-        const cuuint64_t dims[2] = {cuuint64_t(kD), rows};
-        const cuuint64_t strides[1] = {cuuint64_t(kD)};
-        const cuuint32_t box[2] = {64, kPageSize}, estr[2] = {1, 1};
-        if (tensor_map_encoder()(&map_c, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-                                 const_cast<void*>(p.cache), dims, strides, box, estr,
-                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if constexpr (!kFp8) {
+        if (!encode_2d(&cache.map, p.cache, kD, uint64_t(p.num_blocks) * kPageSize, kPageSize))
             return int(cudaErrorInvalidValue);
-    } else if (!encode_2d(&map_c, p.cache, kD, rows, kPageSize)) {
-        return int(cudaErrorInvalidValue);
     }
     auto kernel = mla_span_kernel<kFp8>;
     static std::atomic<uint64_t> allowed{0};
@@ -1063,7 +1061,7 @@ int launch(const SpanParams& p, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return int(cudaLaunchKernelEx(&cfg, kernel, p, map_q, map_c));
+    return int(cudaLaunchKernelEx(&cfg, kernel, p, map_q, cache));
 }
 
 }  // namespace
