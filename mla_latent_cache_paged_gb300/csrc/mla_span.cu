@@ -473,13 +473,15 @@ struct Widener {
         q.flip = two ? 64 : 0;
         return q;
     }
-    // From row y of the cache; zeros for a page that is not there (y < 0).
+    // From row y of the cache; zeros for a page that is not there (y < 0). (Not
+    // through the read-only path: this kernel starts while the one that writes the
+    // cache may still run.)
     __device__ __forceinline__ void load(int32_t y, const Part& q, uint4 (&v)[8]) const {
         const unsigned char* src = static_cast<const unsigned char*>(p.cache) +
                                    (int64_t(y) + q.row) * kD + q.column;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            v[k] = y >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + k * q.step * kD))
+            v[k] = y >= 0 ? *reinterpret_cast<const uint4*>(src + k * q.step * kD)
                           : make_uint4(0, 0, 0, 0);
     }
     // Them as f16 in the swizzled layout.
