@@ -571,9 +571,9 @@ struct Widener {
     // again (the conversion above has rounded them) and multiplied by the power
     // of two that brings its greatest to [2^14, 2^15), 2^126 at most; its scores are
     // divided by that power (exactly, or to 2^-150, which the softmax scale makes
-    // 2^-22 of at most). Looking for such rows costs nothing here, and the branch
-    // for them in the softmax 1 us (64 requests of 32 heads over two prefixes 73.3
-    // us against 72.3, a window of 4,000 over 96 of them 64.2 against 63.0).
+    // 2^-22 of at most). Looking for such rows costs nothing here, asking for
+    // them in the softmax 0.7 us (64 requests of 32 heads over two prefixes 73.4 us
+    // against 72.7, a window of 4,000 over 96 of them 64.6 against 64.0).
     __device__ __forceinline__ void widen_queries(int w, int live, int row0, int item) const {
         float* scales = reinterpret_cast<float*>(smem + kOffScale) + (item & 1) * kCtaRows;
 #pragma unroll 1
@@ -629,6 +629,19 @@ struct Widener {
             wait(staged, uint32_t(pieces - 1) & 1, bars, p.status, kSiteDrain, limit, true);
     }
 };
+
+// A row's scores of a step times a factor, in TMEM. (Few calls come here: it is kept
+// out of the softmax's code.)
+__device__ __noinline__ void scale_scores(uint32_t at, float by) {
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+        uint32_t o[32];
+        ptx::tmem_ld32(at + uint32_t(c), o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+        ptx::tmem_st32(at + uint32_t(c), o);
+    }
+}
 
 // ------------------------------------------------------------ the kernel
 
@@ -820,12 +833,10 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
             float l_sum = 0.f;         // of the weights (for the LSE)
             float l_mma = 0.f;         // of the rounded ones (for the results)
             // fp8 cache: what a row's scores are multiplied by first (widen_queries;
-            // negative with a negative softmax scale), and whether that is not 1 for a
-            // row of this warp. (Written before the queries were announced, which
-            // the scores waited for, and again with those of the second item after
-            // this one, whose queries land when this one's last weights have been
-            // announced.)
-            bool scaled = false;
+            // negative with a negative softmax scale). (Written before the queries
+            // were announced, which the scores waited for, and again with those of
+            // the second item after this one, whose queries land when this one's
+            // last weights have been announced.)
             const float* row_scale = reinterpret_cast<const float*>(smem + kOffScale) +
                                      ((w.item - 1) & 1) * kCtaRows + r;
             for (int k = 0; k < pc.steps; ++k, ++j) {
@@ -833,7 +844,12 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
                 const int v = kSpanStepPages * (pc.first + k);
                 const PageMask mine = page_mask(pc.it, v + f);
                 ok = ok && until(bar(offsetof(Bars, s_full)) + 8 * st, (j >> 1) & 1, kSiteQkDone);
-                if (kFp8 && k == 0) scaled = ok && __any_sync(0xffffffffu, *row_scale != 1.f);
+                // (Asked at each step: an answer kept from the item's first one, or the
+                // product where the scores are read below, took 1 to 2 us of 73.)
+                if (kFp8 && ok && __any_sync(0xffffffffu, *row_scale != 1.f)) {
+                    ptx::tc_fence_after();
+                    scale_scores(trow + kTmemS + uint32_t(st * 64), *row_scale);
+                }
                 // With an fp8 cache the scores are read twice, half of them at a
                 // time: its many warps leave 96 registers a thread.
                 constexpr int kPart = kFp8 ? 32 : 64;
@@ -846,10 +862,9 @@ mla_span_kernel(const SpanParams p, const __grid_constant__ CUtensorMap map_q,
                         ptx::tmem_ld64(trow + kTmemS + uint32_t(st * 64), raw);
 #pragma unroll
                     for (int i = 0; i < kPart; ++i) x[i] = __uint_as_float(raw[i]);
-                    if (kFp8 ? scaled : p.scale_log2 < 0.f) {
-                        const float by = kFp8 ? *row_scale : -1.f;
+                    if (!kFp8 && p.scale_log2 < 0.f) {
 #pragma unroll
-                        for (int i = 0; i < kPart; ++i) x[i] *= by;
+                        for (int i = 0; i < kPart; ++i) x[i] = -x[i];
                     }
                     if (!mine.all()) {
 #pragma unroll
