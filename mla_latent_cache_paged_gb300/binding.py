@@ -1105,9 +1105,11 @@ def mla_decode_shared(q, latent_cache, block_table, seq_lens, group_starts, shar
                       workspace=None, stream=None):
     """``mla_decode`` of a batch whose requests ``group_starts[g]`` ..
     ``group_starts[g + 1] - 1`` (int32 ``[G + 1]``) share their first
-    ``shared_lens[g]`` tokens (int32 ``[G]``), whose whole pages are attended to
-    once for the group's rows together. Returns ``(out bf16 [B, N, 512], lse
-    fp32 [B, N] | None)``, as ``mla_decode`` would."""
+    ``shared_lens[g]`` tokens (int32 ``[G]``). Where that saves time, their whole
+    pages are attended to once for the group's rows together; a batch that
+    would gain little, and any of 128 heads, is decoded request by request.
+    Returns ``(out bf16 [B, N, 512], lse fp32 [B, N] | None)``, as ``mla_decode``
+    would."""
     import torch
     return _decode_span(load_library().mla_decode_shared, torch.bfloat16, q, latent_cache,
                         block_table, seq_lens, (group_starts, shared_lens), None,

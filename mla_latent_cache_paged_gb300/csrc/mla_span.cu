@@ -42,15 +42,18 @@
 // the slots (exact).
 //
 // Measured, calls one behind the other in a graph: 64 requests of 128 heads over
-// a prefix of 16,384 tokens and 100 to 1,500 of their own (308 GFLOP) 204 us,
-// 1,510 TFLOP/s; a step takes some 2,900 cycles, of which the MMAs need 2,176;
-// the operands that they read and the tiles that TMA writes take shared memory
-// for 2,750 (128 bytes a cycle). With an fp8 cache a step takes some 3,800: the
-// same port, with 1,886 for the operands and 1,900 for the codes' way through L1
-// and registers and the weights; 64 requests of 32 heads over two prefixes of
-// 8,000 to 12,000 tokens 73.5 us. 128 requests of 128 heads through a window of
-// 1,024 tokens (177 MB) 57 us; small batches take 15 to 16 us: the schedule (2 to
-// 3), the first page (2), a step or two, results (2), the merge (3).
+// a prefix of 16,384 tokens and 100 to 1,500 of their own (308 GFLOP) 205 us,
+// 1,500 TFLOP/s; a step takes 2,900 cycles in a short call and 3,100 to 3,600 in a
+// long one, of which the MMAs need 2,176; the operands that they read and the
+// tiles that TMA writes take shared memory for 2,750 (128 bytes a cycle). With an
+// fp8 cache a step takes some 4,000: the same port, with 1,886 for the operands and
+// 1,900 for the codes' way through L1 and registers and the weights; 64 requests
+// of 32 heads over two prefixes of 8,000 to 12,000 tokens 73 us. 128 requests of
+// 128 heads through a window of 1,024 tokens (177 MB) 57 to 59 us; small batches
+// take 15 to 16 us: the schedule (2 to 3), the first page (2), a step or two,
+// results (2), the merge (3).
+//
+// Registers: 201 a thread, 96 with an fp8 cache (19 warps), neither spilled.
 //
 // Warps: 1 = MMAs (first CTA), 2-5 = softmax and epilogue, 0 and 6 = loads (fp8
 // cache: 0 = queries, 6-18 = codes). Every wait is bounded (MLA_ERR_TIMEOUT).

@@ -27,19 +27,22 @@ namespace mla {
 constexpr int kSpanRows = 128;
 constexpr int kSpanStepPages = 2;
 // An item's fixed cost. 64 requests of 32 heads over two fp8 prefixes of 8,000 to
-// 12,000 tokens take 77.7 us with 2, 85 with 1, 75.6 with 3; a window of 4,000
-// over 96 requests of 32 heads 68.6, 74 and 71.
+// 12,000 tokens take 72.8 us with 2, 79.4 with 1, 72.6 with 3, a window of 4,000
+// over 96 of them 63.7, 70.7 and 64.5; in bf16 48 requests of 16 heads over five
+// prefixes 27.7, 28.6 and 28.7, a prefix of 16,384 under 64 requests of 128 heads
+// 203, 208 and 204.
 constexpr int kSpanItemCost = 2;
 // All cuts move to items' edges if no pair's share grows by more than this: the
-// pieces of an item that is cut are merged from fp32 rows. 8 requests of 16 heads
-// over 500 to 800 tokens: 18.8 us with 4, 21.3 with 6; 10 is worse, 2 is like 4.
+// pieces of an item that is cut are merged from fp32 rows. 128 requests of 64 heads
+// over 640 tokens take 30.8 us with 4, 2 or 6 and 34.8 with 0; a window of 1,024 over
+// 128 requests of 128 heads 56 to 59 with 4 or 6, 60 with 0 or 2.
 constexpr int kSpanCutCost = 4;
 // Prefixes are shared if that saves as many steps for every pair: items of their
 // own come with pieces to merge for every row. With 4 groups of 8 requests of 16
-// heads, 1,024 tokens together and 128 each, it saves 2.84 and takes 18.5 us
-// (22.2 apart); 32 groups of 4 requests of 64 heads, 512 together, would save
-// 1.68 and take 37.1 (30.5 apart). Between 1.1 and 2.9 the two are mostly within
-// 1 us of each other (fp8 cache: the same, 22.0 against 26.6, 44.2 against 38.7).
+// heads, 1,024 tokens together and 128 each, it saves 2.84 and takes 18.8 us
+// (22.6 apart); 32 groups of 4 requests of 64 heads, 512 together, would save
+// 1.68 and take 37.1 (30.8 apart). Between 1.1 and 2.9 the two are mostly within
+// 1 us of each other (fp8 cache: the same, 22.6 against 27.5, 44.7 against 39.5).
 constexpr int kSpanShareGain = 2;
 constexpr int kSpanMaxBatch = 4096;
 

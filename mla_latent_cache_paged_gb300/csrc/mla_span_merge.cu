@@ -20,10 +20,13 @@ namespace {
 
 constexpr int kMaxPieces = 2 * kMaxBalancedPairs;
 // Eight warps a row, four, or one: a row's pieces are read one behind the other
-// by each warp, so few rows (two, then eight, an SM) get more of them. 48 requests
-// of 16 heads (768 rows, some 10 pieces each) take 30.2 us a call with four and 39
-// with one; 128 requests of 128 heads (mostly one piece) 58 with one, 73 with
-// eight.
+// by each warp, so few rows (two, then eight, for each of 152 SMs: the merge's
+// CTAs spread over the GPU, whatever number of SMs the plan is for) get more of
+// them. 8 requests of 16 heads (128 rows) take 16.6 us a call with eight, 17.1 with
+// four and 18.0 with one; 48 of 16 (768 rows, some 10 pieces each) 28.0 with four,
+// 28.9 with eight, 30.7 with one; 128 of 128 (mostly one piece) 57 to 59 with one, 64
+// with four, 71 with eight. (With four and eight the compiler spills 24 bytes, at 48
+// registers a thread.)
 constexpr int kMergeRows8 = 304, kMergeRows4 = 1216;
 
 // The weight of a part with LSE `l` among parts whose greatest is m. (A NaN
