@@ -53,7 +53,7 @@
 // take 15 to 16 us: the schedule (2 to 3), the first page (2), a step or two,
 // results (2), the merge (3).
 //
-// Registers: 201 a thread, 96 with an fp8 cache (19 warps), neither spilled.
+// Registers: 201 a thread; 96 with an fp8 cache (19 warps), which spills 28 bytes.
 //
 // Warps: 1 = MMAs (first CTA), 2-5 = softmax and epilogue, 0 and 6 = loads (fp8
 // cache: 0 = queries, 6-18 = codes). Every wait is bounded (MLA_ERR_TIMEOUT).
